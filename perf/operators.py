@@ -264,7 +264,7 @@ def _scan(s):
         la, x = s["la"].float(), s["x"].float()
         a = la.exp()
         after = torch.cat([a[:, 1:], torch.zeros_like(a[:, :1])], 1)
-        g = s["dh"].float()
+        g = s["dh"].to(torch.float32, copy=True)  # the state's own gradient stays as it is
         g[:, -1] += s["dhT"]
         g = _recur(after.flip(1), g.flip(1)).flip(1)
         gain, slope = _gain(c, la, a)
