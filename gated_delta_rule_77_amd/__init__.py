@@ -16,6 +16,13 @@ Entry points (same names as the C ABI):
     pdn_chunk_bwd(...)                 gradients of the prefill
     pdn_chunk_bwd_workspace_size(...)  scratch bytes the backward needs
     pdn_abi_version(), pdn_strerror(code)
+and the operators around the recurrence:
+    pdn_qk_norm_fwd / _bwd(...)        norm and rotation of q and k, [B,T,Hx,d] -> [B,H,T,d]
+    pdn_out_norm_fwd / _bwd(...)       gated norm of o, [B,H,T,dv] -> [B,T,H,dv]
+    pdn_scan_fwd / _bwd / _step(...)   the gated recurrence with a vector state, [B,T,D]
+    pdn_scan_marks(T)                  kept states of a scan over T tokens
+    pdn_rope_freqs(...)                inverse frequencies, scaled for long contexts
+with pdn_*_workspace_size(...) for those that take scratch.
 """
 from __future__ import annotations
 
@@ -36,9 +43,17 @@ PDN_ALPHA_NONE, PDN_ALPHA_SCALAR, PDN_ALPHA_VEC = 0, 1, 2
 PDN_GATE_SCALAR, PDN_GATE_VEC, PDN_GAMMA_SAME_AS_BETA = 1, 2, 3
 PDN_KEY_SYMMETRIC, PDN_KEY_ERASE_GATE, PDN_KEY_WRITE_GATE = 0, 1, 2
 PDN_PRECOND_INVERSE, PDN_PRECOND_STABILISED = 0, 1
+PDN_NORM_NONE, PDN_NORM_RMS, PDN_NORM_L2 = 0, 1, 2
+PDN_ROPE_HALF, PDN_ROPE_INTERLEAVED = 0, 1
+PDN_ROPE_PLAIN, PDN_ROPE_LINEAR, PDN_ROPE_BASE, PDN_ROPE_BY_PARTS = 0, 1, 2, 3
+PDN_ACT_NONE, PDN_ACT_SILU, PDN_ACT_SIGMOID = 0, 1, 2
+PDN_GAIN_NONE, PDN_GAIN_COMPLEMENT, PDN_GAIN_NORM = 0, 1, 2
+PDN_SCAN_MARK = 128
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_L = ctypes.c_int64
+_F = ctypes.c_float
 
 
 class ChunkFwdArgs(ctypes.Structure):
@@ -79,10 +94,82 @@ class DecodeArgs(ctypes.Structure):
                 ("S", _P), ("o", _P)]
 
 
+class QkNormArgs(ctypes.Structure):
+    """Mirror of ``pdn_qk_norm_args``."""
+    _fields_ = [("B", _I), ("T", _I), ("H", _I), ("Hq", _I), ("Hk", _I), ("d", _I),
+                ("dtype", _I), ("norm", _I), ("eps", _F), ("q_scale", _F), ("k_scale", _F),
+                ("rot_dim", _I), ("rope_layout", _I), ("rope_scale", _F),
+                ("inv_freq", _P), ("positions", _P), ("wq", _P), ("wk", _P),
+                ("xq", _P), ("xk", _P),
+                ("xq_sb", _L), ("xq_st", _L), ("xq_sh", _L),
+                ("xk_sb", _L), ("xk_st", _L), ("xk_sh", _L),
+                ("q", _P), ("k", _P)]
+
+
+class QkNormBwdArgs(ctypes.Structure):
+    """Mirror of ``pdn_qk_norm_bwd_args``."""
+    _fields_ = [("fwd", QkNormArgs), ("dq", _P), ("dk", _P), ("dxq", _P), ("dxk", _P),
+                ("dxq_sb", _L), ("dxq_st", _L), ("dxq_sh", _L),
+                ("dxk_sb", _L), ("dxk_st", _L), ("dxk_sh", _L),
+                ("dwq", _P), ("dwk", _P),
+                ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class OutNormArgs(ctypes.Structure):
+    """Mirror of ``pdn_out_norm_args``."""
+    _fields_ = [("B", _I), ("H", _I), ("T", _I), ("dv", _I), ("o_dtype", _I), ("dtype", _I),
+                ("act", _I), ("eps", _F), ("o", _P), ("w", _P),
+                ("z", _P), ("z_sb", _L), ("z_st", _L), ("z_sh", _L),
+                ("y", _P), ("y_sb", _L), ("y_st", _L), ("y_sh", _L)]
+
+
+class OutNormBwdArgs(ctypes.Structure):
+    """Mirror of ``pdn_out_norm_bwd_args``."""
+    _fields_ = [("fwd", OutNormArgs),
+                ("dy", _P), ("dy_sb", _L), ("dy_st", _L), ("dy_sh", _L), ("d_o", _P),
+                ("dz", _P), ("dz_sb", _L), ("dz_st", _L), ("dz_sh", _L), ("dw", _P),
+                ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class ScanArgs(ctypes.Structure):
+    """Mirror of ``pdn_scan_args``."""
+    _fields_ = [("B", _I), ("T", _I), ("D", _I), ("dtype", _I), ("log_dtype", _I), ("gain", _I),
+                ("x", _P), ("x_sb", _L), ("x_st", _L),
+                ("log_a", _P), ("log_a_sb", _L), ("log_a_st", _L),
+                ("h0", _P), ("hT", _P), ("h", _P), ("h_sb", _L), ("h_st", _L), ("marks", _P),
+                ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class ScanBwdArgs(ctypes.Structure):
+    """Mirror of ``pdn_scan_bwd_args``."""
+    _fields_ = [("fwd", ScanArgs), ("dh", _P), ("dh_sb", _L), ("dh_st", _L), ("dhT", _P),
+                ("dx", _P), ("dx_sb", _L), ("dx_st", _L),
+                ("dlog_a", _P), ("dlog_a_sb", _L), ("dlog_a_st", _L), ("dh0", _P),
+                ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class ScanStepArgs(ctypes.Structure):
+    """Mirror of ``pdn_scan_step_args``."""
+    _fields_ = [("B", _I), ("D", _I), ("dtype", _I), ("log_dtype", _I), ("gain", _I),
+                ("x", _P), ("x_sb", _L), ("log_a", _P), ("log_a_sb", _L),
+                ("h_prev", _P), ("h_next", _P), ("h", _P), ("h_sb", _L)]
+
+
+# the operators around the recurrence: their argument structs, and which of
+# them have a workspace size to ask for
+_AROUND = {"pdn_qk_norm_fwd": (QkNormArgs, "pdn_qk_norm_check", None),
+           "pdn_qk_norm_bwd": (QkNormBwdArgs, "pdn_qk_norm_bwd_check", "pdn_qk_norm_bwd_workspace_size"),
+           "pdn_out_norm_fwd": (OutNormArgs, "pdn_out_norm_check", None),
+           "pdn_out_norm_bwd": (OutNormBwdArgs, "pdn_out_norm_bwd_check", "pdn_out_norm_bwd_workspace_size"),
+           "pdn_scan_fwd": (ScanArgs, "pdn_scan_check", "pdn_scan_fwd_workspace_size"),
+           "pdn_scan_bwd": (ScanBwdArgs, "pdn_scan_bwd_check", "pdn_scan_bwd_workspace_size"),
+           "pdn_scan_step": (ScanStepArgs, "pdn_scan_step_check", None)}
+
 EXPORTED = ("pdn_abi_version", "pdn_strerror", "pdn_chunk_fwd_workspace_size",
             "pdn_chunk_fwd_check", "pdn_chunk_fwd", "pdn_chunk_fwd_noalloc", "pdn_decode_check",
             "pdn_decode_step", "pdn_chunk_bwd_workspace_size", "pdn_chunk_bwd_check",
-            "pdn_chunk_bwd")
+            "pdn_chunk_bwd", "pdn_rope_freqs",
+            *(n for call, (_, check, size) in _AROUND.items() for n in (call, check, size) if n))
 
 _lib = None
 _lock = threading.Lock()
@@ -130,6 +217,17 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.pdn_decode_check.restype = ctypes.c_int
         lib.pdn_decode_step.argtypes = [ctypes.POINTER(DecodeArgs), _P]
         lib.pdn_decode_step.restype = ctypes.c_int
+        for name, (struct, check, size) in _AROUND.items():
+            getattr(lib, name).argtypes = [ctypes.POINTER(struct), _P]
+            getattr(lib, check).argtypes = [ctypes.POINTER(struct)]
+            if size:
+                getattr(lib, size).argtypes = [ctypes.POINTER(struct), ctypes.POINTER(ctypes.c_size_t)]
+            for n in (name, check, size):
+                if n:
+                    getattr(lib, n).restype = ctypes.c_int
+        lib.pdn_rope_freqs.argtypes = [_I, ctypes.c_double, _I, ctypes.c_double, _L,
+                                       ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_F)]
+        lib.pdn_rope_freqs.restype = ctypes.c_int
         # a library built from another header version would read the
         # argument structs at other offsets (device pointers included)
         ver = int(lib.pdn_abi_version())
@@ -479,3 +577,310 @@ def pdn_decode_step(q, k, v, o, S, log_alpha=None, beta=None, gamma=None,
     rc = load_library().pdn_decode_step(ctypes.byref(a), _stream(stream))
     if rc != PDN_OK:
         raise PdnError(rc, "pdn_decode_step")
+
+
+# ---------------------------------------------------------------------------
+# the operators around the recurrence
+# ---------------------------------------------------------------------------
+
+def _dtype_of(t, name):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return PDN_BF16
+    if t.dtype == torch.float32:
+        return PDN_F32
+    raise ValueError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
+
+
+def _around_tensor(t, name, shape, device, dtype, strided):
+    """Checks one tensor of a call and returns (pointer, strides without the
+    last); None gives (None, zeros)."""
+    if t is None:
+        return None, (0,) * (len(shape) - 1)
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, list(shape), list(t.shape)))
+    if not t.is_cuda:
+        raise ValueError("%s must live in device memory" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, the first argument on %s: every tensor must share its device"
+                         % (name, t.device, device))
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    stride = t.stride()
+    if strided:
+        if stride[-1] != 1 and shape[-1] != 1:
+            raise ValueError("the last dimension of %s must be contiguous" % name)
+    elif not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr(), stride[:-1]
+
+
+class _Call:
+    """One call's argument struct, with the device and types that its first tensor sets."""
+
+    def __init__(self, struct, first):
+        import torch
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise ValueError("the first argument must be a tensor in device memory")
+        self.a, self.device, self.f32 = struct(), first.device, torch.float32
+
+    def rows(self, a, field, t, name, shape, dtype, *strides):
+        """A strided tensor: its pointer and strides."""
+        p, s = _around_tensor(t, name, shape, self.device, dtype, True)
+        setattr(a, field, p)
+        for suffix, v in zip(strides, s):
+            setattr(a, field + suffix, v)
+
+    def plain(self, a, field, t, name, shape, dtype=None):
+        setattr(a, field, _around_tensor(t, name, shape, self.device, dtype or self.f32, False)[0])
+
+    def size(self, name):
+        n = ctypes.c_size_t(0)
+        rc = getattr(load_library(), name)(ctypes.byref(self.a), ctypes.byref(n))
+        if rc != PDN_OK:
+            raise PdnError(rc, name)
+        return int(n.value)
+
+    def launch(self, name, stream, workspace=None):
+        """Makes the call on `stream`, or torch's current stream of the tensors'
+        device, with that device current.  A workspace that the caller does not
+        give comes from torch's caching allocator, allocated on the launch's own
+        stream, whose order then protects its reuse."""
+        import torch
+        if self.device.index != torch.cuda.current_device():
+            with torch.cuda.device(self.device):
+                return self.launch(name, stream, workspace)
+        a, size = self.a, _AROUND[name][2]
+        if size:
+            if workspace is None:
+                n = self.size(size)
+                if n and stream is not None:
+                    own = torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream
+                    with torch.cuda.stream(own):
+                        workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+                elif n:
+                    workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+            elif workspace.device != self.device:
+                raise ValueError("workspace must be on %s" % self.device)
+            if workspace is not None:
+                a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+        rc = getattr(load_library(), name)(ctypes.byref(a), _stream(stream))
+        if rc != PDN_OK:
+            raise PdnError(rc, name)
+
+
+def _qk_norm(c, a, xq, xk, H, norm, eps, wq, wk, q_scale, k_scale, inv_freq, positions, rope_layout, rope_scale):
+    if xq.dim() != 4 or xk.dim() != 4:
+        raise ValueError("xq and xk must be [B,T,heads,d]")
+    B, T, a.Hq, d = xq.shape
+    a.B, a.T, a.H, a.Hk, a.d = B, T, H, xk.shape[2], d
+    a.dtype, a.norm, a.eps = _dtype_of(xq, "xq"), int(norm), float(eps)
+    a.q_scale, a.k_scale = float(q_scale), float(k_scale)
+    c.rows(a, "xq", xq, "xq", (B, T, a.Hq, d), xq.dtype, "_sb", "_st", "_sh")
+    c.rows(a, "xk", xk, "xk", (B, T, a.Hk, d), xq.dtype, "_sb", "_st", "_sh")
+    c.plain(a, "wq", wq, "wq", (d,))
+    c.plain(a, "wk", wk, "wk", (d,))
+    if inv_freq is not None:
+        import torch
+        a.rot_dim, a.rope_layout, a.rope_scale = 2 * inv_freq.shape[0], int(rope_layout), float(rope_scale)
+        c.plain(a, "inv_freq", inv_freq, "inv_freq", (a.rot_dim // 2,), torch.float64)
+        c.plain(a, "positions", positions, "positions", (B, T), torch.int64)
+    elif positions is not None:
+        raise ValueError("positions need inv_freq")
+    return B, T, d
+
+
+def pdn_qk_norm_fwd(xq, xk, q, k, norm=PDN_NORM_L2, eps=1e-6, wq=None, wk=None, q_scale=1.0, k_scale=1.0,
+                    inv_freq=None, positions=None, rope_layout=PDN_ROPE_HALF, rope_scale=1.0, stream=None) -> None:
+    """Norm of each head's queries and keys, and their rotation, into the
+    recurrence's layout: xq [B,T,Hq,d], xk [B,T,Hk,d] (views into a
+    projection's rows are fine) to q, k [B,H,T,d], which hold what the
+    recurrence takes; an input head serves H / Hq (H / Hk) output heads.
+
+    norm is one of PDN_NORM_*, wq / wk its fp32 weights [d].  inv_freq
+    (float64 [rot_dim / 2], see pdn_rope_freqs) turns the rotation on, at
+    positions (int64 [B,T]; None = 0, 1, .. in each sequence)."""
+    c = _Call(QkNormArgs, xq)
+    if q.dim() != 4:
+        raise ValueError("q and k must be [B,H,T,d]")
+    H = q.shape[1]
+    B, T, d = _qk_norm(c, c.a, xq, xk, H, norm, eps, wq, wk, q_scale, k_scale, inv_freq, positions, rope_layout, rope_scale)
+    c.plain(c.a, "q", q, "q", (B, H, T, d), xq.dtype)
+    c.plain(c.a, "k", k, "k", (B, H, T, d), xq.dtype)
+    c.launch("pdn_qk_norm_fwd", stream)
+
+
+def _qk_norm_bwd(xq, xk, dq, dk, dxq, dxk, dwq, dwk, norm, eps, wq, wk, q_scale, k_scale, inv_freq, positions,
+                 rope_layout, rope_scale):
+    c = _Call(QkNormBwdArgs, xq)
+    if dq.dim() != 4:
+        raise ValueError("dq and dk must be [B,H,T,d]")
+    a, H = c.a, dq.shape[1]
+    B, T, d = _qk_norm(c, a.fwd, xq, xk, H, norm, eps, wq, wk, q_scale, k_scale, inv_freq, positions, rope_layout, rope_scale)
+    c.plain(a, "dq", dq, "dq", (B, H, T, d))
+    c.plain(a, "dk", dk, "dk", (B, H, T, d))
+    c.rows(a, "dxq", dxq, "dxq", tuple(xq.shape), xq.dtype, "_sb", "_st", "_sh")
+    c.rows(a, "dxk", dxk, "dxk", tuple(xk.shape), xq.dtype, "_sb", "_st", "_sh")
+    c.plain(a, "dwq", dwq, "dwq", (d,))
+    c.plain(a, "dwk", dwk, "dwk", (d,))
+    return c
+
+
+def pdn_qk_norm_bwd_workspace_size(xq, xk, dq, dk, dxq, dxk, dwq=None, dwk=None, norm=PDN_NORM_L2, eps=1e-6, wq=None,
+                                   wk=None, q_scale=1.0, k_scale=1.0, inv_freq=None, positions=None,
+                                   rope_layout=PDN_ROPE_HALF, rope_scale=1.0) -> int:
+    return _qk_norm_bwd(xq, xk, dq, dk, dxq, dxk, dwq, dwk, norm, eps, wq, wk, q_scale, k_scale, inv_freq, positions,
+                        rope_layout, rope_scale).size("pdn_qk_norm_bwd_workspace_size")
+
+
+def pdn_qk_norm_bwd(xq, xk, dq, dk, dxq, dxk, dwq=None, dwk=None, norm=PDN_NORM_L2, eps=1e-6, wq=None, wk=None,
+                    q_scale=1.0, k_scale=1.0, inv_freq=None, positions=None, rope_layout=PDN_ROPE_HALF, rope_scale=1.0,
+                    workspace=None, stream=None) -> None:
+    """Backward of pdn_qk_norm_fwd: from dq, dk (fp32 [B,H,T,d], as
+    pdn_chunk_bwd writes them) to dxq, dxk (shapes and type of xq, xk; views
+    are fine) and, where the norm has weights, dwq, dwk (fp32 [d])."""
+    _qk_norm_bwd(xq, xk, dq, dk, dxq, dxk, dwq, dwk, norm, eps, wq, wk, q_scale, k_scale, inv_freq, positions,
+                 rope_layout, rope_scale).launch("pdn_qk_norm_bwd", stream, workspace)
+
+
+def _out_norm(c, a, o, z, w, dtype, act, eps):
+    if o.dim() != 4:
+        raise ValueError("o must be [B,H,T,dv]")
+    a.B, a.H, a.T, a.dv = B, H, T, dv = o.shape
+    a.o_dtype, a.act, a.eps = _dtype_of(o, "o"), int(act), float(eps)
+    c.plain(a, "o", o, "o", (B, H, T, dv), o.dtype)
+    c.rows(a, "z", z, "z", (B, T, H, dv), dtype, "_sb", "_st", "_sh")
+    c.plain(a, "w", w, "w", (dv,))
+    return B, T, H, dv
+
+
+def _act_of(act, z):
+    return (PDN_ACT_NONE if z is None else PDN_ACT_SILU) if act is None else act
+
+
+def pdn_out_norm_fwd(o, y, z=None, w=None, act=None, eps=1e-6, stream=None) -> None:
+    """Gated norm of the recurrence's output, back to the projection's layout:
+    o [B,H,T,dv] to y [B,T,H,dv] (a view is fine), times the weights w (fp32
+    [dv]) and the gate act(z), z [B,T,H,dv].  act is one of PDN_ACT_*; None
+    means PDN_ACT_SILU where z is given."""
+    c = _Call(OutNormArgs, o)
+    c.a.dtype = _dtype_of(y, "y")
+    shape = _out_norm(c, c.a, o, z, w, y.dtype, _act_of(act, z), eps)
+    c.rows(c.a, "y", y, "y", shape, y.dtype, "_sb", "_st", "_sh")
+    c.launch("pdn_out_norm_fwd", stream)
+
+
+def _out_norm_bwd(o, dy, do, z, dz, w, dw, act, eps):
+    c = _Call(OutNormBwdArgs, o)
+    a = c.a
+    a.fwd.dtype = _dtype_of(dy, "dy")
+    shape = _out_norm(c, a.fwd, o, z, w, dy.dtype, _act_of(act, z), eps)
+    c.rows(a, "dy", dy, "dy", shape, dy.dtype, "_sb", "_st", "_sh")
+    c.plain(a, "d_o", do, "do", tuple(o.shape))
+    c.rows(a, "dz", dz, "dz", shape, dy.dtype, "_sb", "_st", "_sh")
+    c.plain(a, "dw", dw, "dw", shape[-1:])
+    return c
+
+
+def pdn_out_norm_bwd_workspace_size(o, dy, do, z=None, dz=None, w=None, dw=None, act=None, eps=1e-6) -> int:
+    return _out_norm_bwd(o, dy, do, z, dz, w, dw, act, eps).size("pdn_out_norm_bwd_workspace_size")
+
+
+def pdn_out_norm_bwd(o, dy, do, z=None, dz=None, w=None, dw=None, act=None, eps=1e-6, workspace=None,
+                     stream=None) -> None:
+    """Backward of pdn_out_norm_fwd: from dy [B,T,H,dv] to do (fp32
+    [B,H,T,dv], the dO of pdn_chunk_bwd), dz (given exactly when z is) and dw
+    (fp32 [dv], given exactly when w is)."""
+    _out_norm_bwd(o, dy, do, z, dz, w, dw, act, eps).launch("pdn_out_norm_bwd", stream, workspace)
+
+
+def pdn_scan_marks(T: int) -> int:
+    """How many states a scan over T tokens keeps in `marks`."""
+    return -(-int(T) // PDN_SCAN_MARK)
+
+
+def _scan(c, a, x, log_a, h0, marks, gain):
+    if x.dim() != 3:
+        raise ValueError("x must be [B,T,D]")
+    a.B, a.T, a.D = B, T, D = x.shape
+    a.dtype, a.log_dtype, a.gain = _dtype_of(x, "x"), _dtype_of(log_a, "log_a"), int(gain)
+    c.rows(a, "x", x, "x", (B, T, D), x.dtype, "_sb", "_st")
+    c.rows(a, "log_a", log_a, "log_a", (B, T, D), log_a.dtype, "_sb", "_st")
+    c.plain(a, "h0", h0, "h0", (B, D))
+    c.plain(a, "marks", marks, "marks", (B, pdn_scan_marks(T), D))
+    return B, T, D
+
+
+def _scan_fwd(x, log_a, h, h0, hT, marks, gain):
+    c = _Call(ScanArgs, x)
+    B, T, D = _scan(c, c.a, x, log_a, h0, marks, gain)
+    c.rows(c.a, "h", h, "h", (B, T, D), x.dtype, "_sb", "_st")
+    c.plain(c.a, "hT", hT, "hT", (B, D))
+    return c
+
+
+def pdn_scan_fwd_workspace_size(x, log_a, h, h0=None, hT=None, marks=None, gain=PDN_GAIN_NONE) -> int:
+    return _scan_fwd(x, log_a, h, h0, hT, marks, gain).size("pdn_scan_fwd_workspace_size")
+
+
+def pdn_scan_fwd(x, log_a, h, h0=None, hT=None, marks=None, gain=PDN_GAIN_NONE, workspace=None, stream=None) -> None:
+    """The gated recurrence with a vector state: h_t = exp(log_a_t) h_{t-1} +
+    g x_t over x, log_a, h [B,T,D] (views are fine), from h0 to hT (fp32
+    [B,D]).  log_a = -inf starts a sequence within a row.  gain is one of
+    PDN_GAIN_*.  marks (fp32 [B, pdn_scan_marks(T), D]), when given, receives
+    the states that pdn_scan_bwd starts from."""
+    _scan_fwd(x, log_a, h, h0, hT, marks, gain).launch("pdn_scan_fwd", stream, workspace)
+
+
+def _scan_bwd(x, log_a, dh, dx, dlog_a, h0, dhT, dh0, marks, gain):
+    c = _Call(ScanBwdArgs, x)
+    a = c.a
+    B, T, D = _scan(c, a.fwd, x, log_a, h0, marks, gain)
+    c.rows(a, "dh", dh, "dh", (B, T, D), x.dtype, "_sb", "_st")
+    c.rows(a, "dx", dx, "dx", (B, T, D), x.dtype, "_sb", "_st")
+    c.rows(a, "dlog_a", dlog_a, "dlog_a", (B, T, D), log_a.dtype, "_sb", "_st")
+    c.plain(a, "dhT", dhT, "dhT", (B, D))
+    c.plain(a, "dh0", dh0, "dh0", (B, D))
+    return c
+
+
+def pdn_scan_bwd_workspace_size(x, log_a, dh, dx, dlog_a, h0=None, dhT=None, dh0=None, marks=None,
+                                gain=PDN_GAIN_NONE) -> int:
+    return _scan_bwd(x, log_a, dh, dx, dlog_a, h0, dhT, dh0, marks, gain).size("pdn_scan_bwd_workspace_size")
+
+
+def pdn_scan_bwd(x, log_a, dh, dx, dlog_a, h0=None, dhT=None, dh0=None, marks=None, gain=PDN_GAIN_NONE,
+                 workspace=None, stream=None) -> None:
+    """Backward of pdn_scan_fwd: from dh [B,T,D] and dhT to dx, dlog_a and dh0.
+    marks: as the forward wrote them, or None (they are formed here)."""
+    _scan_bwd(x, log_a, dh, dx, dlog_a, h0, dhT, dh0, marks, gain).launch("pdn_scan_bwd", stream, workspace)
+
+
+def pdn_scan_step(x, log_a, h, h_prev, h_next, gain=PDN_GAIN_NONE, stream=None) -> None:
+    """One token of the recurrence for every sequence: x, log_a, h [B,D]
+    (views are fine), h_prev and h_next fp32 [B,D], which may be one tensor."""
+    c = _Call(ScanStepArgs, x)
+    if x.dim() != 2:
+        raise ValueError("x must be [B,D]")
+    a = c.a
+    a.B, a.D = B, D = x.shape
+    a.dtype, a.log_dtype, a.gain = _dtype_of(x, "x"), _dtype_of(log_a, "log_a"), int(gain)
+    c.rows(a, "x", x, "x", (B, D), x.dtype, "_sb")
+    c.rows(a, "log_a", log_a, "log_a", (B, D), log_a.dtype, "_sb")
+    c.plain(a, "h_prev", h_prev, "h_prev", (B, D))
+    c.plain(a, "h_next", h_next, "h_next", (B, D))
+    c.rows(a, "h", h, "h", (B, D), x.dtype, "_sb")
+    c.launch("pdn_scan_step", stream)
+
+
+def pdn_rope_freqs(rot_dim, base=10000.0, scaling=PDN_ROPE_PLAIN, factor=1.0, original_context=1):
+    """(inverse frequencies, a list of rot_dim / 2 floats; rope_scale) for a
+    rotation of rot_dim elements, changed for contexts `factor` times as long
+    as original_context by one of PDN_ROPE_*."""
+    n = int(rot_dim)
+    freqs, scale = (ctypes.c_double * max(n // 2, 1))(), _F(1.0)
+    rc = load_library().pdn_rope_freqs(n, float(base), int(scaling), float(factor), int(original_context), freqs,
+                                       ctypes.byref(scale))
+    if rc != PDN_OK:
+        raise PdnError(rc, "pdn_rope_freqs")
+    return list(freqs), float(scale.value)

@@ -151,6 +151,256 @@ int check_decode(const pdn_decode_args* a) {
     return PDN_OK;
 }
 
+// ---- the operators around the recurrence ----
+
+// B * T of the strided operators: their kernels index tokens in 32 bits.
+constexpr long kMaxRows = (1L << 31) - 1;
+
+int elt_bytes(int32_t dtype) { return dtype == PDN_BF16 ? 2 : 4; }
+
+// A strided tensor: a pointer, the sizes of its dimensions but the last (which
+// is contiguous, `width` elements) and their strides.
+struct View {
+    const void* p;
+    int64_t size[3], stride[3];
+    int64_t width;
+    int bytes;
+};
+
+View view3(const void* p, int64_t s0, int64_t s1, int64_t s2, int64_t t0, int64_t t1, int64_t t2, int64_t width, int32_t dtype) {
+    return View{p, {s0, s1, s2}, {t0, t1, t2}, width, elt_bytes(dtype)};
+}
+
+// Strides of a strided tensor (only dimensions longer than 1 are stepped
+// over): not negative, every row 16-byte aligned, the whole within 63 bits;
+// and, for an output, no row over another.
+int check_view(const View& v, bool output) {
+    if (!aligned16(v.p)) return PDN_EINVAL;
+    constexpr int64_t kMost = int64_t{1} << 56;
+    int64_t size[3], stride[3];
+    int n = 0;
+    __int128 reach = v.width;
+    for (int i = 0; i < 3; ++i) {
+        if (v.size[i] <= 1) continue;
+        if (v.stride[i] < 0 || v.stride[i] > kMost) return PDN_EINVAL;
+        if (v.stride[i] * v.bytes % 16 != 0) return PDN_EINVAL;
+        reach += static_cast<__int128>(v.stride[i]) * (v.size[i] - 1);
+        size[n] = v.size[i];
+        stride[n++] = v.stride[i];
+    }
+    if (reach > kMost) return PDN_EINVAL;
+    if (!output) return PDN_OK;
+    // from the smallest stride up, each step passes all that lies below it
+    for (int i = 0; i < n; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if (stride[j] < stride[i]) {
+                const int64_t a = stride[i], b = size[i];
+                stride[i] = stride[j];
+                size[i] = size[j];
+                stride[j] = a;
+                size[j] = b;
+            }
+    int64_t span = v.width;
+    for (int i = 0; i < n; ++i) {
+        if (stride[i] < span) return PDN_EINVAL;
+        span = stride[i] * (size[i] - 1) + span;
+    }
+    return PDN_OK;
+}
+
+bool valid_eps(float eps) { return std::isnormal(eps) && eps > 0.0f; }
+
+int check_rows(int32_t B, int32_t H, int32_t T) {
+    if (B < 1 || H < 1 || T < 0) return PDN_EINVAL;
+    if (static_cast<long>(B) * H > kMaxBH) return PDN_EUNSUPPORTED;
+    if (static_cast<long>(B) * T > kMaxRows || static_cast<long>(B) * H * T > kMaxTokens) return PDN_EUNSUPPORTED;
+    return PDN_OK;
+}
+
+// backward: the forward's outputs are not read
+int check_qk_norm(const pdn_qk_norm_args* a, bool backward = false) {
+    if (!a) return PDN_EINVAL;
+    int rc = check_rows(a->B, a->H, a->T);
+    if (rc != PDN_OK) return rc;
+    if (a->Hq < 1 || a->Hk < 1 || a->H % a->Hq != 0 || a->H % a->Hk != 0) return PDN_EINVAL;
+    if (!valid_dtype(a->dtype)) return PDN_EINVAL;
+    if (a->norm != PDN_NORM_NONE && a->norm != PDN_NORM_RMS && a->norm != PDN_NORM_L2) return PDN_EINVAL;
+    if (a->norm != PDN_NORM_NONE ? !valid_eps(a->eps) : (a->wq || a->wk)) return PDN_EINVAL;
+    if (!std::isfinite(a->q_scale) || !std::isfinite(a->k_scale)) return PDN_EINVAL;
+    if (a->d != 64 && a->d != 128) return PDN_EUNSUPPORTED;
+    if (a->rot_dim < 0 || a->rot_dim > a->d) return PDN_EINVAL;
+    if (a->rot_dim % 16 != 0) return PDN_EUNSUPPORTED;
+    if (a->rot_dim > 0) {
+        if (a->rope_layout != PDN_ROPE_HALF && a->rope_layout != PDN_ROPE_INTERLEAVED) return PDN_EINVAL;
+        if (!std::isfinite(a->rope_scale) || !a->inv_freq) return PDN_EINVAL;
+    }
+    if (a->T == 0) return PDN_OK;
+    if (!a->xq || !a->xk || (!backward && (!a->q || !a->k))) return PDN_EINVAL;
+    const void* ptrs[] = {a->inv_freq, a->positions, a->wq, a->wk, backward ? nullptr : a->q, backward ? nullptr : a->k};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return PDN_EINVAL;
+    rc = check_view(view3(a->xq, a->B, a->T, a->Hq, a->xq_sb, a->xq_st, a->xq_sh, a->d, a->dtype), false);
+    if (rc != PDN_OK) return rc;
+    return check_view(view3(a->xk, a->B, a->T, a->Hk, a->xk_sb, a->xk_st, a->xk_sh, a->d, a->dtype), false);
+}
+
+int check_workspace(const void* workspace, size_t bytes, size_t need) {
+    if (need == 0) return PDN_OK;
+    if (workspace && !aligned16(workspace)) return PDN_EINVAL;
+    return !workspace || bytes < need ? PDN_EWORKSPACE : PDN_OK;
+}
+
+int check_qk_norm_bwd(const pdn_qk_norm_bwd_args* a, bool check_ws = true) {
+    if (!a) return PDN_EINVAL;
+    const pdn_qk_norm_args& f = a->fwd;
+    int rc = check_qk_norm(&f, true);
+    if (rc != PDN_OK) return rc;
+    if ((f.wq != nullptr) != (a->dwq != nullptr) || (f.wk != nullptr) != (a->dwk != nullptr)) return PDN_EINVAL;
+    const void* ptrs[] = {a->dq, a->dk, a->dwq, a->dwk};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return PDN_EINVAL;
+    if (f.T > 0) {
+        if (!a->dq || !a->dk || !a->dxq || !a->dxk) return PDN_EINVAL;
+        rc = check_view(view3(a->dxq, f.B, f.T, f.Hq, a->dxq_sb, a->dxq_st, a->dxq_sh, f.d, f.dtype), true);
+        if (rc != PDN_OK) return rc;
+        rc = check_view(view3(a->dxk, f.B, f.T, f.Hk, a->dxk_sb, a->dxk_st, a->dxk_sh, f.d, f.dtype), true);
+        if (rc != PDN_OK) return rc;
+    }
+    return check_ws ? check_workspace(a->workspace, a->workspace_bytes, pdn::qk_norm_bwd_workspace_bytes(*a)) : PDN_OK;
+}
+
+int check_out_norm(const pdn_out_norm_args* a, bool backward = false) {
+    if (!a) return PDN_EINVAL;
+    int rc = check_rows(a->B, a->H, a->T);
+    if (rc != PDN_OK) return rc;
+    if (!valid_dtype(a->o_dtype) || !valid_dtype(a->dtype) || !valid_eps(a->eps) || a->dv < 1) return PDN_EINVAL;
+    if (a->act != PDN_ACT_NONE && a->act != PDN_ACT_SILU && a->act != PDN_ACT_SIGMOID) return PDN_EINVAL;
+    if (a->dv % 16 != 0 || a->dv > 256) return PDN_EUNSUPPORTED;
+    if (a->w && !aligned16(a->w)) return PDN_EINVAL;
+    if (a->T == 0) return PDN_OK;
+    if (!a->o || !aligned16(a->o) || (a->z != nullptr) != (a->act != PDN_ACT_NONE)) return PDN_EINVAL;
+    if (a->z) {
+        rc = check_view(view3(a->z, a->B, a->T, a->H, a->z_sb, a->z_st, a->z_sh, a->dv, a->dtype), false);
+        if (rc != PDN_OK) return rc;
+    }
+    if (backward) return PDN_OK;
+    if (!a->y) return PDN_EINVAL;
+    return check_view(view3(a->y, a->B, a->T, a->H, a->y_sb, a->y_st, a->y_sh, a->dv, a->dtype), true);
+}
+
+int check_out_norm_bwd(const pdn_out_norm_bwd_args* a, bool check_ws = true) {
+    if (!a) return PDN_EINVAL;
+    const pdn_out_norm_args& f = a->fwd;
+    int rc = check_out_norm(&f, true);
+    if (rc != PDN_OK) return rc;
+    if ((f.w != nullptr) != (a->dw != nullptr) || (a->dw && !aligned16(a->dw))) return PDN_EINVAL;
+    if (f.T > 0) {
+        if (!a->dy || !a->d_o || !aligned16(a->d_o) || (a->dz != nullptr) != (f.z != nullptr)) return PDN_EINVAL;
+        rc = check_view(view3(a->dy, f.B, f.T, f.H, a->dy_sb, a->dy_st, a->dy_sh, f.dv, f.dtype), false);
+        if (rc != PDN_OK) return rc;
+        if (a->dz) {
+            rc = check_view(view3(a->dz, f.B, f.T, f.H, a->dz_sb, a->dz_st, a->dz_sh, f.dv, f.dtype), true);
+            if (rc != PDN_OK) return rc;
+        }
+    }
+    return check_ws ? check_workspace(a->workspace, a->workspace_bytes, pdn::out_norm_bwd_workspace_bytes(*a)) : PDN_OK;
+}
+
+bool valid_gain(int32_t g) { return g == PDN_GAIN_NONE || g == PDN_GAIN_COMPLEMENT || g == PDN_GAIN_NORM; }
+
+// sizes, types and gain of the scan's calls
+int check_scan_kind(int32_t B, int32_t T, int32_t D, int32_t dtype, int32_t log_dtype, int32_t gain) {
+    if (B < 1 || T < 0 || D < 1) return PDN_EINVAL;
+    if (!valid_dtype(dtype) || !valid_dtype(log_dtype) || !valid_gain(gain)) return PDN_EINVAL;
+    if (D % 8 != 0 || (dtype == PDN_F32 && log_dtype == PDN_BF16)) return PDN_EUNSUPPORTED;
+    if (static_cast<long>(B) * T > kMaxRows || static_cast<long>(B) * D > kMaxRows) return PDN_EUNSUPPORTED;
+    return PDN_OK;
+}
+
+// a forward's arguments (backward: its outputs are not read)
+int check_scan(const pdn_scan_args* a, bool backward = false, bool check_ws = true) {
+    if (!a) return PDN_EINVAL;
+    int rc = check_scan_kind(a->B, a->T, a->D, a->dtype, a->log_dtype, a->gain);
+    if (rc != PDN_OK) return rc;
+    if (pdn::scan_blocks(*a) > kMaxRows) return PDN_EUNSUPPORTED;
+    const void* ptrs[] = {a->h0, a->marks, backward ? nullptr : a->hT};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return PDN_EINVAL;
+    if (a->T > 0) {
+        if (!a->x || !a->log_a || (!backward && !a->h)) return PDN_EINVAL;
+        rc = check_view(view3(a->x, a->B, a->T, 1, a->x_sb, a->x_st, 0, a->D, a->dtype), false);
+        if (rc != PDN_OK) return rc;
+        rc = check_view(view3(a->log_a, a->B, a->T, 1, a->log_a_sb, a->log_a_st, 0, a->D, a->log_dtype), false);
+        if (rc != PDN_OK) return rc;
+        if (!backward) rc = check_view(view3(a->h, a->B, a->T, 1, a->h_sb, a->h_st, 0, a->D, a->dtype), true);
+        if (rc != PDN_OK) return rc;
+    }
+    if (backward || !check_ws) return PDN_OK;
+    return check_workspace(a->workspace, a->workspace_bytes, pdn::scan_fwd_workspace_bytes(*a));
+}
+
+int check_scan_bwd(const pdn_scan_bwd_args* a, bool check_ws = true) {
+    if (!a) return PDN_EINVAL;
+    const pdn_scan_args& f = a->fwd;
+    int rc = check_scan(&f, true);
+    if (rc != PDN_OK) return rc;
+    if ((a->dhT && !aligned16(a->dhT)) || (a->dh0 && !aligned16(a->dh0))) return PDN_EINVAL;
+    if (f.T > 0) {
+        if (!a->dh || !a->dx || !a->dlog_a) return PDN_EINVAL;
+        rc = check_view(view3(a->dh, f.B, f.T, 1, a->dh_sb, a->dh_st, 0, f.D, f.dtype), false);
+        if (rc != PDN_OK) return rc;
+        rc = check_view(view3(a->dx, f.B, f.T, 1, a->dx_sb, a->dx_st, 0, f.D, f.dtype), true);
+        if (rc != PDN_OK) return rc;
+        rc = check_view(view3(a->dlog_a, f.B, f.T, 1, a->dlog_a_sb, a->dlog_a_st, 0, f.D, f.log_dtype), true);
+        if (rc != PDN_OK) return rc;
+    }
+    return check_ws ? check_workspace(a->workspace, a->workspace_bytes, pdn::scan_bwd_workspace_bytes(*a)) : PDN_OK;
+}
+
+int check_scan_step(const pdn_scan_step_args* a) {
+    if (!a) return PDN_EINVAL;
+    int rc = check_scan_kind(a->B, 1, a->D, a->dtype, a->log_dtype, a->gain);
+    if (rc != PDN_OK) return rc;
+    if (!a->x || !a->log_a || !a->h_prev || !a->h_next || !a->h) return PDN_EINVAL;
+    if (!aligned16(a->h_prev) || !aligned16(a->h_next)) return PDN_EINVAL;
+    rc = check_view(view3(a->x, a->B, 1, 1, a->x_sb, 0, 0, a->D, a->dtype), false);
+    if (rc != PDN_OK) return rc;
+    rc = check_view(view3(a->log_a, a->B, 1, 1, a->log_a_sb, 0, 0, a->D, a->log_dtype), false);
+    if (rc != PDN_OK) return rc;
+    return check_view(view3(a->h, a->B, 1, 1, a->h_sb, 0, 0, a->D, a->dtype), true);
+}
+
+// The extern "C" bodies: an answer, a size or a launch, and no exception out.
+template <class F>
+int answer(F f) {
+    try {
+        return f();
+    } catch (...) {
+        return PDN_EINVAL;
+    }
+}
+
+template <class A, class Check, class Launch>
+int call(const A* args, void* stream, Check check, Launch launch) {
+    try {
+        const int rc = check(args);
+        if (rc != PDN_OK) return rc;
+        return launch(*args, static_cast<hipStream_t>(stream)) == hipSuccess ? PDN_OK : PDN_EHIP;
+    } catch (...) {
+        return PDN_EHIP;
+    }
+}
+
+template <class A, class Check, class Size>
+int size_of(const A* args, size_t* bytes, Check check, Size size) {
+    if (!args || !bytes) return PDN_EINVAL;
+    return answer([&] {
+        const int rc = check(args);
+        if (rc == PDN_OK) *bytes = size(*args);
+        return rc;
+    });
+}
+
 // Scratch of pdn_chunk_fwd_noalloc: one copy per GPU, loaded with the code
 // object (no allocation call makes it).  In host code `scratch` is a host-side
 // stand-in for the symbol, never a device address: every use goes through the
@@ -315,6 +565,76 @@ int pdn_decode_step(const pdn_decode_args* args, void* stream) {
     } catch (...) {
         return PDN_EHIP;
     }
+}
+
+int pdn_qk_norm_check(const pdn_qk_norm_args* args) { return answer([&] { return check_qk_norm(args); }); }
+int pdn_qk_norm_bwd_check(const pdn_qk_norm_bwd_args* args) { return answer([&] { return check_qk_norm_bwd(args); }); }
+int pdn_out_norm_check(const pdn_out_norm_args* args) { return answer([&] { return check_out_norm(args); }); }
+int pdn_out_norm_bwd_check(const pdn_out_norm_bwd_args* args) { return answer([&] { return check_out_norm_bwd(args); }); }
+int pdn_scan_check(const pdn_scan_args* args) { return answer([&] { return check_scan(args); }); }
+int pdn_scan_bwd_check(const pdn_scan_bwd_args* args) { return answer([&] { return check_scan_bwd(args); }); }
+int pdn_scan_step_check(const pdn_scan_step_args* args) { return answer([&] { return check_scan_step(args); }); }
+
+int pdn_qk_norm_bwd_workspace_size(const pdn_qk_norm_bwd_args* args, size_t* bytes) {
+    return size_of(args, bytes, [](auto* a) { return check_qk_norm_bwd(a, false); }, pdn::qk_norm_bwd_workspace_bytes);
+}
+int pdn_out_norm_bwd_workspace_size(const pdn_out_norm_bwd_args* args, size_t* bytes) {
+    return size_of(args, bytes, [](auto* a) { return check_out_norm_bwd(a, false); }, pdn::out_norm_bwd_workspace_bytes);
+}
+int pdn_scan_fwd_workspace_size(const pdn_scan_args* args, size_t* bytes) {
+    return size_of(args, bytes, [](auto* a) { return check_scan(a, false, false); }, pdn::scan_fwd_workspace_bytes);
+}
+int pdn_scan_bwd_workspace_size(const pdn_scan_bwd_args* args, size_t* bytes) {
+    return size_of(args, bytes, [](auto* a) { return check_scan_bwd(a, false); }, pdn::scan_bwd_workspace_bytes);
+}
+
+int pdn_qk_norm_fwd(const pdn_qk_norm_args* args, void* stream) {
+    return call(args, stream, [](auto* a) { return check_qk_norm(a); }, pdn::launch_qk_norm);
+}
+int pdn_qk_norm_bwd(const pdn_qk_norm_bwd_args* args, void* stream) {
+    return call(args, stream, [](auto* a) { return check_qk_norm_bwd(a); }, pdn::launch_qk_norm_bwd);
+}
+int pdn_out_norm_fwd(const pdn_out_norm_args* args, void* stream) {
+    return call(args, stream, [](auto* a) { return check_out_norm(a); }, pdn::launch_out_norm);
+}
+int pdn_out_norm_bwd(const pdn_out_norm_bwd_args* args, void* stream) {
+    return call(args, stream, [](auto* a) { return check_out_norm_bwd(a); }, pdn::launch_out_norm_bwd);
+}
+int pdn_scan_fwd(const pdn_scan_args* args, void* stream) {
+    return call(args, stream, [](auto* a) { return check_scan(a); }, pdn::launch_scan_fwd);
+}
+int pdn_scan_bwd(const pdn_scan_bwd_args* args, void* stream) {
+    return call(args, stream, [](auto* a) { return check_scan_bwd(a); }, pdn::launch_scan_bwd);
+}
+int pdn_scan_step(const pdn_scan_step_args* args, void* stream) {
+    return call(args, stream, [](auto* a) { return check_scan_step(a); }, pdn::launch_scan_step);
+}
+
+int pdn_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, int64_t original_context,
+                   double* inv_freq, float* rope_scale) {
+    if (!inv_freq || !rope_scale || rot_dim < 2 || rot_dim % 2 != 0) return PDN_EINVAL;
+    if (!(base > 1.0) || !std::isfinite(base) || !(factor >= 1.0) || !std::isfinite(factor) || original_context < 1)
+        return PDN_EINVAL;
+    if (scaling < PDN_ROPE_PLAIN || scaling > PDN_ROPE_BY_PARTS) return PDN_EINVAL;
+    if (scaling == PDN_ROPE_BASE) {
+        if (rot_dim < 4) return PDN_EINVAL;
+        base *= std::pow(factor, static_cast<double>(rot_dim) / (rot_dim - 2));
+    }
+    constexpr double kFewTurns = 1.0, kManyTurns = 32.0;
+    constexpr double kTwoPi = 6.283185307179586;
+    for (int32_t i = 0; i < rot_dim / 2; ++i) {
+        const double f = std::pow(base, -2.0 * i / rot_dim);
+        double keep = 1.0;  // share of the frequency that is not divided
+        if (scaling == PDN_ROPE_LINEAR) keep = 0.0;
+        if (scaling == PDN_ROPE_BY_PARTS) {
+            const double turns = static_cast<double>(original_context) * f / kTwoPi;
+            keep = (turns - kFewTurns) / (kManyTurns - kFewTurns);
+            keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+        }
+        inv_freq[i] = keep * f + (1.0 - keep) * f / factor;
+    }
+    *rope_scale = scaling == PDN_ROPE_BY_PARTS ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return PDN_OK;
 }
 
 }  // extern "C"
