@@ -48,7 +48,7 @@ PDN_ROPE_HALF, PDN_ROPE_INTERLEAVED = 0, 1
 PDN_ROPE_PLAIN, PDN_ROPE_LINEAR, PDN_ROPE_BASE, PDN_ROPE_BY_PARTS = 0, 1, 2, 3
 PDN_ACT_NONE, PDN_ACT_SILU, PDN_ACT_SIGMOID = 0, 1, 2
 PDN_GAIN_NONE, PDN_GAIN_COMPLEMENT, PDN_GAIN_NORM = 0, 1, 2
-PDN_SCAN_MARK = 128
+PDN_SCAN_MARK = 96
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
@@ -592,54 +592,56 @@ def _dtype_of(t, name):
     raise ValueError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
 
 
-def _around_tensor(t, name, shape, device, dtype, strided):
-    """Checks one tensor of a call and returns (pointer, strides without the
-    last); None gives (None, zeros)."""
-    if t is None:
-        return None, (0,) * (len(shape) - 1)
-    if tuple(t.shape) != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, list(shape), list(t.shape)))
-    if not t.is_cuda:
-        raise ValueError("%s must live in device memory" % name)
-    if t.device != device:
-        raise ValueError("%s is on %s, the first argument on %s: every tensor must share its device"
-                         % (name, t.device, device))
-    if t.dtype != dtype:
-        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    stride = t.stride()
-    if strided:
-        if stride[-1] != 1 and shape[-1] != 1:
-            raise ValueError("the last dimension of %s must be contiguous" % name)
-    elif not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr(), stride[:-1]
-
-
 class _Call:
-    """One call's argument struct, with the device and types that its first tensor sets."""
+    """One call's argument struct, with the device that its first tensor sets.
+
+    The checks below are most of what a single-token call costs on the host, so
+    each is one comparison on the way through; the message is put together only
+    when one fails."""
+
+    __slots__ = ("a", "index")
 
     def __init__(self, struct, first):
-        import torch
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        index = first.get_device() if hasattr(first, "get_device") else -1
+        if index < 0:
             raise ValueError("the first argument must be a tensor in device memory")
-        self.a, self.device, self.f32 = struct(), first.device, torch.float32
+        self.a, self.index = struct(), index
 
-    def rows(self, a, field, t, name, shape, dtype, *strides):
-        """A strided tensor: its pointer and strides."""
-        p, s = _around_tensor(t, name, shape, self.device, dtype, True)
-        setattr(a, field, p)
-        for suffix, v in zip(strides, s):
-            setattr(a, field + suffix, v)
+    def plain(self, t, name, shape, dtype):
+        """Pointer of a contiguous tensor (None stays None)."""
+        if t is None:
+            return None
+        if t.shape != shape or t.dtype != dtype or t.get_device() != self.index or not t.is_contiguous():
+            self._refuse(t, name, shape, dtype)
+            raise ValueError("%s must be contiguous" % name)
+        return t.data_ptr()
 
-    def plain(self, a, field, t, name, shape, dtype=None):
-        setattr(a, field, _around_tensor(t, name, shape, self.device, dtype or self.f32, False)[0])
+    def rows(self, t, name, shape, dtype):
+        """Pointer of a strided tensor; its last dimension must be contiguous."""
+        if t is None:
+            return None
+        if t.shape != shape or t.dtype != dtype or t.get_device() != self.index or (t.stride(-1) != 1 and shape[-1] != 1):
+            self._refuse(t, name, shape, dtype)
+            raise ValueError("the last dimension of %s must be contiguous" % name)
+        return t.data_ptr()
+
+    def _refuse(self, t, name, shape, dtype):
+        if t.shape != shape:
+            raise ValueError("%s must have shape %s, got %s" % (name, list(shape), list(t.shape)))
+        if not t.is_cuda:
+            raise ValueError("%s must live in device memory" % name)
+        if t.get_device() != self.index:
+            raise ValueError("%s is on %s, the first argument on cuda:%d: every tensor must share its device"
+                             % (name, t.device, self.index))
+        if t.dtype != dtype:
+            raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
 
     def size(self, name):
         n = ctypes.c_size_t(0)
         rc = getattr(load_library(), name)(ctypes.byref(self.a), ctypes.byref(n))
         if rc != PDN_OK:
             raise PdnError(rc, name)
-        return int(n.value)
+        return n.value
 
     def launch(self, name, stream, workspace=None):
         """Makes the call on `stream`, or torch's current stream of the tensors'
@@ -647,44 +649,49 @@ class _Call:
         give comes from torch's caching allocator, allocated on the launch's own
         stream, whose order then protects its reuse."""
         import torch
-        if self.device.index != torch.cuda.current_device():
-            with torch.cuda.device(self.device):
+        if self.index != torch.cuda.current_device():
+            with torch.cuda.device(self.index):
                 return self.launch(name, stream, workspace)
         a, size = self.a, _AROUND[name][2]
         if size:
             if workspace is None:
                 n = self.size(size)
                 if n and stream is not None:
-                    own = torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream
+                    own = torch.cuda.ExternalStream(stream, device=self.index) if isinstance(stream, int) else stream
                     with torch.cuda.stream(own):
-                        workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
+                        workspace = torch.empty(n, dtype=torch.uint8, device="cuda")
                 elif n:
-                    workspace = torch.empty(n, dtype=torch.uint8, device=self.device)
-            elif workspace.device != self.device:
-                raise ValueError("workspace must be on %s" % self.device)
+                    workspace = torch.empty(n, dtype=torch.uint8, device="cuda")
+            elif workspace.get_device() != self.index:
+                raise ValueError("workspace must be on cuda:%d" % self.index)
             if workspace is not None:
                 a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
-        rc = getattr(load_library(), name)(ctypes.byref(a), _stream(stream))
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(self.index)
+        elif not isinstance(stream, int):
+            stream = stream.cuda_stream
+        rc = getattr(load_library(), name)(ctypes.byref(a), stream)
         if rc != PDN_OK:
             raise PdnError(rc, name)
 
 
 def _qk_norm(c, a, xq, xk, H, norm, eps, wq, wk, q_scale, k_scale, inv_freq, positions, rope_layout, rope_scale):
+    import torch
     if xq.dim() != 4 or xk.dim() != 4:
         raise ValueError("xq and xk must be [B,T,heads,d]")
-    B, T, a.Hq, d = xq.shape
-    a.B, a.T, a.H, a.Hk, a.d = B, T, H, xk.shape[2], d
-    a.dtype, a.norm, a.eps = _dtype_of(xq, "xq"), int(norm), float(eps)
-    a.q_scale, a.k_scale = float(q_scale), float(k_scale)
-    c.rows(a, "xq", xq, "xq", (B, T, a.Hq, d), xq.dtype, "_sb", "_st", "_sh")
-    c.rows(a, "xk", xk, "xk", (B, T, a.Hk, d), xq.dtype, "_sb", "_st", "_sh")
-    c.plain(a, "wq", wq, "wq", (d,))
-    c.plain(a, "wk", wk, "wk", (d,))
+    B, T, Hq, d = xq.shape
+    Hk, dtype = xk.shape[2], xq.dtype
+    a.B, a.T, a.H, a.Hq, a.Hk, a.d = B, T, H, Hq, Hk, d
+    a.dtype, a.norm, a.eps, a.q_scale, a.k_scale = _dtype_of(xq, "xq"), norm, eps, q_scale, k_scale
+    a.xq, a.xk = c.rows(xq, "xq", (B, T, Hq, d), dtype), c.rows(xk, "xk", (B, T, Hk, d), dtype)
+    a.xq_sb, a.xq_st, a.xq_sh, _ = xq.stride()
+    a.xk_sb, a.xk_st, a.xk_sh, _ = xk.stride()
+    a.wq, a.wk = c.plain(wq, "wq", (d,), torch.float32), c.plain(wk, "wk", (d,), torch.float32)
     if inv_freq is not None:
-        import torch
-        a.rot_dim, a.rope_layout, a.rope_scale = 2 * inv_freq.shape[0], int(rope_layout), float(rope_scale)
-        c.plain(a, "inv_freq", inv_freq, "inv_freq", (a.rot_dim // 2,), torch.float64)
-        c.plain(a, "positions", positions, "positions", (B, T), torch.int64)
+        half = inv_freq.shape[0]
+        a.rot_dim, a.rope_layout, a.rope_scale = 2 * half, rope_layout, rope_scale
+        a.inv_freq = c.plain(inv_freq, "inv_freq", (half,), torch.float64)
+        a.positions = c.plain(positions, "positions", (B, T), torch.int64)
     elif positions is not None:
         raise ValueError("positions need inv_freq")
     return B, T, d
@@ -705,24 +712,24 @@ def pdn_qk_norm_fwd(xq, xk, q, k, norm=PDN_NORM_L2, eps=1e-6, wq=None, wk=None, 
         raise ValueError("q and k must be [B,H,T,d]")
     H = q.shape[1]
     B, T, d = _qk_norm(c, c.a, xq, xk, H, norm, eps, wq, wk, q_scale, k_scale, inv_freq, positions, rope_layout, rope_scale)
-    c.plain(c.a, "q", q, "q", (B, H, T, d), xq.dtype)
-    c.plain(c.a, "k", k, "k", (B, H, T, d), xq.dtype)
+    c.a.q, c.a.k = c.plain(q, "q", (B, H, T, d), xq.dtype), c.plain(k, "k", (B, H, T, d), xq.dtype)
     c.launch("pdn_qk_norm_fwd", stream)
 
 
 def _qk_norm_bwd(xq, xk, dq, dk, dxq, dxk, dwq, dwk, norm, eps, wq, wk, q_scale, k_scale, inv_freq, positions,
                  rope_layout, rope_scale):
+    import torch
     c = _Call(QkNormBwdArgs, xq)
     if dq.dim() != 4:
         raise ValueError("dq and dk must be [B,H,T,d]")
     a, H = c.a, dq.shape[1]
     B, T, d = _qk_norm(c, a.fwd, xq, xk, H, norm, eps, wq, wk, q_scale, k_scale, inv_freq, positions, rope_layout, rope_scale)
-    c.plain(a, "dq", dq, "dq", (B, H, T, d))
-    c.plain(a, "dk", dk, "dk", (B, H, T, d))
-    c.rows(a, "dxq", dxq, "dxq", tuple(xq.shape), xq.dtype, "_sb", "_st", "_sh")
-    c.rows(a, "dxk", dxk, "dxk", tuple(xk.shape), xq.dtype, "_sb", "_st", "_sh")
-    c.plain(a, "dwq", dwq, "dwq", (d,))
-    c.plain(a, "dwk", dwk, "dwk", (d,))
+    f32 = torch.float32
+    a.dq, a.dk = c.plain(dq, "dq", (B, H, T, d), f32), c.plain(dk, "dk", (B, H, T, d), f32)
+    a.dxq, a.dxk = c.rows(dxq, "dxq", xq.shape, xq.dtype), c.rows(dxk, "dxk", xk.shape, xq.dtype)
+    a.dxq_sb, a.dxq_st, a.dxq_sh, _ = dxq.stride()
+    a.dxk_sb, a.dxk_st, a.dxk_sh, _ = dxk.stride()
+    a.dwq, a.dwk = c.plain(dwq, "dwq", (d,), f32), c.plain(dwk, "dwk", (d,), f32)
     return c
 
 
@@ -743,19 +750,28 @@ def pdn_qk_norm_bwd(xq, xk, dq, dk, dxq, dxk, dwq=None, dwk=None, norm=PDN_NORM_
                  rope_layout, rope_scale).launch("pdn_qk_norm_bwd", stream, workspace)
 
 
-def _out_norm(c, a, o, z, w, dtype, act, eps):
+def _strides(a, field, t):
+    """The strides of a [B,T,heads,d] tensor (None: all zero, as they are)."""
+    if t is not None:
+        sb, st, sh, _ = t.stride()
+        setattr(a, field + "_sb", sb)
+        setattr(a, field + "_st", st)
+        setattr(a, field + "_sh", sh)
+
+
+def _out_norm(c, a, o, z, w, like, act, eps):
+    import torch
     if o.dim() != 4:
         raise ValueError("o must be [B,H,T,dv]")
-    a.B, a.H, a.T, a.dv = B, H, T, dv = o.shape
-    a.o_dtype, a.act, a.eps = _dtype_of(o, "o"), int(act), float(eps)
-    c.plain(a, "o", o, "o", (B, H, T, dv), o.dtype)
-    c.rows(a, "z", z, "z", (B, T, H, dv), dtype, "_sb", "_st", "_sh")
-    c.plain(a, "w", w, "w", (dv,))
+    B, H, T, dv = o.shape
+    a.B, a.H, a.T, a.dv = B, H, T, dv
+    a.o_dtype, a.dtype, a.eps = _dtype_of(o, "o"), _dtype_of(like, "y and dy"), eps
+    a.act = (PDN_ACT_NONE if z is None else PDN_ACT_SILU) if act is None else act
+    a.o = c.plain(o, "o", (B, H, T, dv), o.dtype)
+    a.z = c.rows(z, "z", (B, T, H, dv), like.dtype)
+    _strides(a, "z", z)
+    a.w = c.plain(w, "w", (dv,), torch.float32)
     return B, T, H, dv
-
-
-def _act_of(act, z):
-    return (PDN_ACT_NONE if z is None else PDN_ACT_SILU) if act is None else act
 
 
 def pdn_out_norm_fwd(o, y, z=None, w=None, act=None, eps=1e-6, stream=None) -> None:
@@ -764,21 +780,22 @@ def pdn_out_norm_fwd(o, y, z=None, w=None, act=None, eps=1e-6, stream=None) -> N
     [dv]) and the gate act(z), z [B,T,H,dv].  act is one of PDN_ACT_*; None
     means PDN_ACT_SILU where z is given."""
     c = _Call(OutNormArgs, o)
-    c.a.dtype = _dtype_of(y, "y")
-    shape = _out_norm(c, c.a, o, z, w, y.dtype, _act_of(act, z), eps)
-    c.rows(c.a, "y", y, "y", shape, y.dtype, "_sb", "_st", "_sh")
+    shape = _out_norm(c, c.a, o, z, w, y, act, eps)
+    c.a.y = c.rows(y, "y", shape, y.dtype)
+    _strides(c.a, "y", y)
     c.launch("pdn_out_norm_fwd", stream)
 
 
 def _out_norm_bwd(o, dy, do, z, dz, w, dw, act, eps):
+    import torch
     c = _Call(OutNormBwdArgs, o)
     a = c.a
-    a.fwd.dtype = _dtype_of(dy, "dy")
-    shape = _out_norm(c, a.fwd, o, z, w, dy.dtype, _act_of(act, z), eps)
-    c.rows(a, "dy", dy, "dy", shape, dy.dtype, "_sb", "_st", "_sh")
-    c.plain(a, "d_o", do, "do", tuple(o.shape))
-    c.rows(a, "dz", dz, "dz", shape, dy.dtype, "_sb", "_st", "_sh")
-    c.plain(a, "dw", dw, "dw", shape[-1:])
+    shape = _out_norm(c, a.fwd, o, z, w, dy, act, eps)
+    a.dy, a.dz = c.rows(dy, "dy", shape, dy.dtype), c.rows(dz, "dz", shape, dy.dtype)
+    _strides(a, "dy", dy)
+    _strides(a, "dz", dz)
+    a.d_o = c.plain(do, "do", o.shape, torch.float32)
+    a.dw = c.plain(dw, "dw", shape[-1:], torch.float32)
     return c
 
 
@@ -800,22 +817,28 @@ def pdn_scan_marks(T: int) -> int:
 
 
 def _scan(c, a, x, log_a, h0, marks, gain):
+    import torch
     if x.dim() != 3:
         raise ValueError("x must be [B,T,D]")
-    a.B, a.T, a.D = B, T, D = x.shape
-    a.dtype, a.log_dtype, a.gain = _dtype_of(x, "x"), _dtype_of(log_a, "log_a"), int(gain)
-    c.rows(a, "x", x, "x", (B, T, D), x.dtype, "_sb", "_st")
-    c.rows(a, "log_a", log_a, "log_a", (B, T, D), log_a.dtype, "_sb", "_st")
-    c.plain(a, "h0", h0, "h0", (B, D))
-    c.plain(a, "marks", marks, "marks", (B, pdn_scan_marks(T), D))
+    B, T, D = x.shape
+    a.B, a.T, a.D = B, T, D
+    a.dtype, a.log_dtype, a.gain = _dtype_of(x, "x"), _dtype_of(log_a, "log_a"), gain
+    a.x, a.log_a = c.rows(x, "x", (B, T, D), x.dtype), c.rows(log_a, "log_a", (B, T, D), log_a.dtype)
+    a.x_sb, a.x_st, _ = x.stride()
+    a.log_a_sb, a.log_a_st, _ = log_a.stride()
+    a.h0 = c.plain(h0, "h0", (B, D), torch.float32)
+    a.marks = c.plain(marks, "marks", (B, pdn_scan_marks(T), D), torch.float32)
     return B, T, D
 
 
 def _scan_fwd(x, log_a, h, h0, hT, marks, gain):
+    import torch
     c = _Call(ScanArgs, x)
-    B, T, D = _scan(c, c.a, x, log_a, h0, marks, gain)
-    c.rows(c.a, "h", h, "h", (B, T, D), x.dtype, "_sb", "_st")
-    c.plain(c.a, "hT", hT, "hT", (B, D))
+    a = c.a
+    B, T, D = _scan(c, a, x, log_a, h0, marks, gain)
+    a.h = c.rows(h, "h", (B, T, D), x.dtype)
+    a.h_sb, a.h_st, _ = h.stride()
+    a.hT = c.plain(hT, "hT", (B, D), torch.float32)
     return c
 
 
@@ -833,14 +856,16 @@ def pdn_scan_fwd(x, log_a, h, h0=None, hT=None, marks=None, gain=PDN_GAIN_NONE, 
 
 
 def _scan_bwd(x, log_a, dh, dx, dlog_a, h0, dhT, dh0, marks, gain):
+    import torch
     c = _Call(ScanBwdArgs, x)
     a = c.a
     B, T, D = _scan(c, a.fwd, x, log_a, h0, marks, gain)
-    c.rows(a, "dh", dh, "dh", (B, T, D), x.dtype, "_sb", "_st")
-    c.rows(a, "dx", dx, "dx", (B, T, D), x.dtype, "_sb", "_st")
-    c.rows(a, "dlog_a", dlog_a, "dlog_a", (B, T, D), log_a.dtype, "_sb", "_st")
-    c.plain(a, "dhT", dhT, "dhT", (B, D))
-    c.plain(a, "dh0", dh0, "dh0", (B, D))
+    a.dh, a.dx = c.rows(dh, "dh", (B, T, D), x.dtype), c.rows(dx, "dx", (B, T, D), x.dtype)
+    a.dlog_a = c.rows(dlog_a, "dlog_a", (B, T, D), log_a.dtype)
+    a.dh_sb, a.dh_st, _ = dh.stride()
+    a.dx_sb, a.dx_st, _ = dx.stride()
+    a.dlog_a_sb, a.dlog_a_st, _ = dlog_a.stride()
+    a.dhT, a.dh0 = c.plain(dhT, "dhT", (B, D), torch.float32), c.plain(dh0, "dh0", (B, D), torch.float32)
     return c
 
 
@@ -859,17 +884,17 @@ def pdn_scan_bwd(x, log_a, dh, dx, dlog_a, h0=None, dhT=None, dh0=None, marks=No
 def pdn_scan_step(x, log_a, h, h_prev, h_next, gain=PDN_GAIN_NONE, stream=None) -> None:
     """One token of the recurrence for every sequence: x, log_a, h [B,D]
     (views are fine), h_prev and h_next fp32 [B,D], which may be one tensor."""
+    import torch
     c = _Call(ScanStepArgs, x)
     if x.dim() != 2:
         raise ValueError("x must be [B,D]")
     a = c.a
-    a.B, a.D = B, D = x.shape
-    a.dtype, a.log_dtype, a.gain = _dtype_of(x, "x"), _dtype_of(log_a, "log_a"), int(gain)
-    c.rows(a, "x", x, "x", (B, D), x.dtype, "_sb")
-    c.rows(a, "log_a", log_a, "log_a", (B, D), log_a.dtype, "_sb")
-    c.plain(a, "h_prev", h_prev, "h_prev", (B, D))
-    c.plain(a, "h_next", h_next, "h_next", (B, D))
-    c.rows(a, "h", h, "h", (B, D), x.dtype, "_sb")
+    B, D = x.shape
+    a.B, a.D = B, D
+    a.dtype, a.log_dtype, a.gain = _dtype_of(x, "x"), _dtype_of(log_a, "log_a"), gain
+    a.x, a.log_a, a.h = c.rows(x, "x", (B, D), x.dtype), c.rows(log_a, "log_a", (B, D), log_a.dtype), c.rows(h, "h", (B, D), x.dtype)
+    a.x_sb, a.log_a_sb, a.h_sb = x.stride(0), log_a.stride(0), h.stride(0)
+    a.h_prev, a.h_next = c.plain(h_prev, "h_prev", (B, D), torch.float32), c.plain(h_next, "h_next", (B, D), torch.float32)
     c.launch("pdn_scan_step", stream)
 
 

@@ -9,18 +9,20 @@
 //   (A2, H2) after (A1, H1) = (A2 A1, A2 H1 + H2).
 // Nothing here needs more than a few operations an element, so the bound is
 // bytes: every element is read once and written once.  A workgroup takes a tile
-// of 64 channels (one 128-byte line of bf16 a token) by R * 32 tokens: a lane
-// holds 8 channels of R tokens in registers, reduces them to its (A, H), the
-// eight lanes' worth of token groups in a wave are scanned by lane shifts, the
-// four waves through LDS.  What is left is the state before the tile:
+// of 128 channels by (waves x R) tokens.  A wave holds R tokens of all 128
+// channels in registers, two neighbouring channels to a lane (a row of bf16 is
+// one 256-byte access), and reduces them to (A, H) without a word to another
+// lane; its row addresses are scalars.  The waves' runs meet in LDS.  What is
+// left is the state before the tile:
 //
 // each tile publishes its (A, H) as soon as it has it, then looks back along
 // its column for the nearest tile whose state behind it is known, applies the
 // (A, H) of the tiles between in their order, and publishes the state behind
 // itself.  Whichever tile it starts from, that is the same chain of operations
 // h_{j+1} = A_j h_j + H_j, so results are the same bits whatever the timing.
-// Tiles are dealt by a counter, in the order of their tokens: a tile waits only
-// for tiles that started before it, so every wait ends.  (The waits are bounded
+// A column's tiles are dealt by a counter of its own, in the order of their
+// tokens: a tile waits only for tiles that started before it, so every wait
+// ends.  (The waits are bounded
 // all the same: a call whose workspace another call overwrites gives NaN
 // instead of hanging.)
 //
@@ -39,19 +41,24 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
-constexpr int kCols = 64;    // channels of a tile
-constexpr int kFwdR = 8;     // tokens of a lane, forward (256 of a tile)
-constexpr int kBwdR = 4;     // backward (128 of a tile: three inputs in registers)
-constexpr int kFwdTile = kFwdR * kThreads / 8;
-constexpr int kBwdTile = kBwdR * kThreads / 8;
-constexpr int kWindow = 8;   // predecessors looked at together
+constexpr int kThreads = 256;  // of the step, reset and copy kernels
+constexpr int kCols = 128;     // channels of a tile
+// Waves of a workgroup and tokens of a wave.  Both directions fit 128 registers
+// (two workgroups to a compute unit).  Measured at B2 T8192 D4096 bf16, forward
+// 8 x 16 93 us, 16 x 16 101, 4 x 32 104, 8 x 8 108; backward 8 x 12 144, 4 x 16
+// 150, 16 x 8 154, 8 x 8 157, 8 x 16 (one workgroup to a compute unit) 177.
+constexpr int kFwdWaves = 8, kFwdR = 16;
+constexpr int kBwdWaves = 8, kBwdR = 12;
+constexpr int kFwdTile = kFwdWaves * kFwdR;
+constexpr int kBwdTile = kBwdWaves * kBwdR;
+// Predecessors looked at together: 2 and 8 measured 1 to 5% slower (rounds, and
+// registers and traffic).
+constexpr int kWindow = 4;
 constexpr u64 kEmpty = ~0ull;
-constexpr unsigned kPolls = 1u << 21;  // polls before a wait gives up: seconds
+constexpr unsigned kPolls = 1u << 21;  // loads before a tile gives up: seconds, where thousands are the most that is needed
 
 static_assert(kBwdTile == PDN_SCAN_MARK, "the backward's tiles start at the marks");
-static_assert(kFwdTile % PDN_SCAN_MARK == 0, "marks lie at wave boundaries of the forward's tiles");
+static_assert(PDN_SCAN_MARK % kFwdR == 0, "marks lie at the boundaries of the forward's waves");
 
 struct Rows {
     const void* p;
@@ -62,10 +69,10 @@ struct RowsOut {
     long sb, st;
 };
 
-// Where a launch's tiles meet: the counter that deals them and, for every
-// column and tile in processing order, 64 words of each kind.
+// Where a launch's tiles meet: the counter that deals each column's, and, for
+// every column and tile in processing order, kCols words of each kind.
 struct Chain {
-    unsigned* counter;
+    unsigned* counters;
     u64* agg;   // (A, H) of a tile
     u64* inc;   // the state behind it
 };
@@ -80,7 +87,7 @@ struct ScanParams {
     const float* dhT;
     float* dh0;
     int T, D;
-    int strips;          // 64-channel strips of a row
+    int strips;          // kCols-channel strips of a row
     int columns;         // B * strips
     int tiles;           // along T
     Chain chain;
@@ -98,87 +105,108 @@ __device__ __forceinline__ u64 pair_word(float A, float H) {
 __device__ __forceinline__ float word_A(u64 w) { return __uint_as_float(static_cast<uint32_t>(w)); }
 __device__ __forceinline__ float word_H(u64 w) { return __uint_as_float(static_cast<uint32_t>(w >> 32)); }
 
-__device__ __forceinline__ u64 peek(const u64* p) {
+template <class T>
+__device__ __forceinline__ T peek(const T* p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ void publish(u64* p, u64 w) {
+template <class T>
+__device__ __forceinline__ void publish(T* p, T w) {
     __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// The word at p, once it is there; `polls` counts down over all of a wave's waits.
+__device__ __forceinline__ u64 settled(const u64* p, u64 w, unsigned& polls) {
+    while (!__all(w != kEmpty) && polls) {
+        --polls;
+        __builtin_amdgcn_s_sleep(1);
+        w = peek(p);
+    }
+    return w;
+}
+
+// The published states behind the kWindow tiles up to `from`.
+struct Window {
+    u64 w[kWindow];
+    __device__ __forceinline__ void load(const u64* first, int from) {
+#pragma unroll
+        for (int k = 0; k < kWindow; ++k) w[k] = peek(first + static_cast<long>(max(from - k, 0)) * kCols);
+    }
+};
+
 // The state before tile `at` of this column (at > 0), one channel to a lane of
-// one wave; agg and inc point at this lane's word of the column's first tile.
-__device__ float look_back(const u64* agg, const u64* inc, int at) {
-    unsigned polls = 0;
-    float h = 0.0f;
+// one wave; agg and inc point at this lane's word of the column's first tile,
+// `inc_words` holds the states behind the tiles up to at - 1.
+//
+// A load from where other workgroups publish takes 1.5 to 2 us here under the
+// tiles' own traffic, so what counts is how many of them follow one another:
+// one for the known states, one for the runs behind the nearest of them.  (The
+// first is issued before the tile's own run is published: the memory counter is
+// in order, so a load behind a store waits for both.)
+__device__ __forceinline__ float look_back(const u64* agg, const u64* inc, Window& inc_words, int at) {
+    unsigned polls = kPolls;
     int known = -1;
-    for (int from = at - 1; known < 0;) {
-        u64 w[kWindow];
+    float h = 0.0f;
+    for (int from = at - 1;;) {
 #pragma unroll
-        for (int i = 0; i < kWindow; ++i) w[i] = from - i >= 0 ? peek(inc + static_cast<long>(from - i) * kCols) : kEmpty;
-#pragma unroll
-        for (int i = 0; i < kWindow; ++i)
-            if (known < 0 && __all(w[i] != kEmpty)) {
-                known = from - i;
-                h = word_H(w[i]);
+        for (int k = 0; k < kWindow; ++k)
+            if (known < 0 && from - k >= 0 && __all(inc_words.w[k] != kEmpty)) {
+                known = from - k;
+                h = word_H(inc_words.w[k]);
             }
         if (known >= 0) break;
+        if (!--polls) return __uint_as_float(0x7fc00000u);
         if (from >= kWindow) {
             from -= kWindow;
         } else {
             from = at - 1;
-            if (++polls > kPolls) return __uint_as_float(0x7fc00000u);
             __builtin_amdgcn_s_sleep(1);
         }
+        inc_words.load(inc, from);
     }
     for (int j = known + 1; j < at; j += kWindow) {
-        u64 w[kWindow];
+        u64 r[kWindow];
 #pragma unroll
-        for (int i = 0; i < kWindow; ++i) w[i] = j + i < at ? peek(agg + static_cast<long>(j + i) * kCols) : 0;
+        for (int k = 0; k < kWindow; ++k) r[k] = peek(agg + static_cast<long>(min(j + k, at - 1)) * kCols);
 #pragma unroll
-        for (int i = 0; i < kWindow; ++i) {
-            if (j + i >= at) break;
-            while (!__all(w[i] != kEmpty)) {
-                if (++polls > kPolls) return __uint_as_float(0x7fc00000u);
-                __builtin_amdgcn_s_sleep(1);
-                w[i] = peek(agg + static_cast<long>(j + i) * kCols);
-            }
-            h = apply(word_A(w[i]), h, word_H(w[i]));
+        for (int k = 0; k < kWindow; ++k) {
+            if (j + k >= at) break;
+            r[k] = settled(agg + static_cast<long>(j + k) * kCols, r[k], polls);
+            h = apply(word_A(r[k]), h, word_H(r[k]));
         }
     }
-    return h;
+    return polls ? h : __uint_as_float(0x7fc00000u);
 }
 
-// The tile of this workgroup, dealt in processing order: all columns' first
-// tiles, then their second ones, ..
+// The counters lie a 128-byte line apart and start at all ones, one below 0.
+constexpr int kCounterStep = 32;
+
+// This workgroup's column goes by its number (neighbouring workgroups have
+// neighbouring columns), its tile by the order in which the column's
+// workgroups start.
 __device__ __forceinline__ void deal(const ScanParams& p, int* slot, int& column, int& at) {
-    if (p.tiles == 1) {
-        column = blockIdx.x;
-        at = 0;
-        return;
-    }
+    column = blockIdx.x % p.columns;
+    at = 0;
+    if (p.tiles == 1) return;
     if (threadIdx.x == 0)
-        *slot = static_cast<int>(__hip_atomic_fetch_add(p.chain.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+        *slot = static_cast<int>(1u + __hip_atomic_fetch_add(p.chain.counters + static_cast<long>(column) * kCounterStep, 1u,
+                                                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
     __syncthreads();
-    const int n = *slot;
-    at = n / p.columns;
-    column = n - at * p.columns;
+    at = __builtin_amdgcn_readfirstlane(*slot);
 }
 
 __device__ __forceinline__ float decay(float la) { return __builtin_amdgcn_exp2f(la * kLog2e); }
 
 // 1 - e^y for y <= 0 to fp32 accuracy, given e = e^y: the difference where e
-// is far from 1 (y < -0.5), else the series of e^y, whose ninth term is below
-// 2^-24 of the sum there.
+// is far from 1 (y < -0.35: an error of e counts under 2.4 times there), else
+// -y times a polynomial for (e^y - 1) / y, fitted to relative error at
+// Chebyshev points of [-0.35, 0]: 0.23 x 2^-24 off in exact arithmetic.
 __device__ __forceinline__ float one_minus_exp(float y, float e) {
-    float s = 1.0f / 40320.0f;
-    s = fmaf(s, y, 1.0f / 5040.0f);
-    s = fmaf(s, y, 1.0f / 720.0f);
-    s = fmaf(s, y, 1.0f / 120.0f);
-    s = fmaf(s, y, 1.0f / 24.0f);
-    s = fmaf(s, y, 1.0f / 6.0f);
-    s = fmaf(s, y, 0.5f);
+    float s = 0.00720365811f;
+    s = fmaf(s, y, 0.0413265228f);
+    s = fmaf(s, y, 0.166624129f);
+    s = fmaf(s, y, 0.499998122f);
     s = fmaf(s, y, 1.0f);
-    return y < -0.5f ? 1.0f - e : -y * s;
+    return y < -0.35f ? 1.0f - e : -y * s;
 }
 
 template <int GAIN>
@@ -195,134 +223,138 @@ __device__ __forceinline__ float gain_slope(float a, float g) {
     return 0.0f;
 }
 
-// Inclusive scan over a wave's eight token groups (lanes 8 apart), forward
-// (each lane's run after the lower lanes') or backward (after the higher ones').
-template <bool REVERSE>
-__device__ __forceinline__ void scan_groups(float (&A)[8], float (&H)[8], int lane) {
-#pragma unroll
-    for (int off = 8; off < 64; off *= 2) {
-        const bool has = REVERSE ? lane + off < 64 : lane >= off;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float a = REVERSE ? __shfl_down(A[j], off, 64) : __shfl_up(A[j], off, 64);
-            const float h = REVERSE ? __shfl_down(H[j], off, 64) : __shfl_up(H[j], off, 64);
-            H[j] = has ? apply(A[j], h, H[j]) : H[j];
-            A[j] = has ? join(a, A[j]) : A[j];
-        }
+// Two neighbouring channels of a row, as they lie in memory.
+template <bool BF16>
+struct Raw2;
+template <>
+struct Raw2<true> {
+    uint32_t v;
+    __device__ __forceinline__ void load(const void* p, long row, int i) {
+        v = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + row + i);
     }
+    __device__ __forceinline__ void zero() { v = 0u; }
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(i ? v & 0xffff0000u : v << 16); }
+    static __device__ __forceinline__ void store(void* p, long row, int i, f32x2 f) {
+        typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        *reinterpret_cast<bf16x2*>(static_cast<uint16_t*>(p) + row + i) = __builtin_convertvector(f, bf16x2);
+    }
+};
+template <>
+struct Raw2<false> {
+    f32x2 v;
+    __device__ __forceinline__ void load(const void* p, long row, int i) {
+        v = *reinterpret_cast<const f32x2*>(static_cast<const float*>(p) + row + i);
+    }
+    __device__ __forceinline__ void zero() { v = f32x2{0.f, 0.f}; }
+    __device__ __forceinline__ float get(int i) const { return v[i]; }
+    static __device__ __forceinline__ void store(void* p, long row, int i, f32x2 f) {
+        *reinterpret_cast<f32x2*>(static_cast<float*>(p) + row + i) = f;
+    }
+};
+
+// What waves 0 and 1 do for the tile, a channel to a lane: join the waves'
+// runs (totA, totH, in processing order), publish, look back, publish; the
+// state before the tile's first run, and through `behind` that behind its last.
+template <int WAVES>
+__device__ __forceinline__ float meet(const ScanParams& p, const float (&totA)[WAVES][kCols],
+                                      const float (&totH)[WAVES][kCols], int column, int at, int ch, float start,
+                                      float& behind) {
+    const long word = static_cast<long>(column) * p.tiles * kCols + ch;
+    const long mine = word + static_cast<long>(at) * kCols;
+    const bool last = at + 1 == p.tiles;
+    Window inc_words;
+    if (at > 0) inc_words.load(p.chain.inc + word, at - 1);
+    float tA = totA[0][ch], tH = totH[0][ch];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) {
+        tH = apply(totA[w][ch], tH, totH[w][ch]);
+        tA = join(tA, totA[w][ch]);
+    }
+    float h = start;
+    if (at > 0) {
+        if (!last) publish(p.chain.agg + mine, pair_word(tA, tH));
+        h = look_back(p.chain.agg + word, p.chain.inc + word, inc_words, at);
+    }
+    behind = apply(tA, h, tH);
+    if (!last) publish(p.chain.inc + mine, pair_word(0.0f, behind));
+    return h;
 }
 
 template <bool XBF, bool LBF, int GAIN, bool WRITE_H>
-__global__ void __launch_bounds__(kThreads) scan_fwd_kernel(ScanParams p) {
-    constexpr int R = kFwdR;
+__global__ void __launch_bounds__(64 * kFwdWaves) scan_fwd_kernel(ScanParams p) {
+    constexpr int R = kFwdR, W = kFwdWaves;
     __shared__ int slot;
-    __shared__ float totA[kWaves][kCols], totH[kWaves][kCols];
-    __shared__ float before[kWaves][kCols];  // the state before each wave's tokens
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    __shared__ float totA[W][kCols], totH[W][kCols];
+    __shared__ float before[W][kCols];  // the state before each wave's tokens
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int column, at;
     deal(p, &slot, column, at);
     const int b = column / p.strips, c0 = (column - b * p.strips) * kCols;
-    const int c8 = (lane & 7) * 8, c = c0 + c8;
-    const long t0 = static_cast<long>(at) * kFwdTile + (tid >> 3) * R;
+    const int c2 = 2 * lane, c = c0 + c2;
+    const int cc = c < p.D ? c : 0;  // lanes past the last channel read another's
+    const int t0 = at * kFwdTile + wave * R;
 
-    Raw8<XBF> x[R];
-    Raw8<LBF> la[R];
-    {
-        const int cc = c < p.D ? c : 0;
-        const long xb = b * p.x.sb + cc, lb = b * p.la.sb + cc;
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            const long t = t0 + j < p.T ? t0 + j : p.T - 1;
-            x[j].load(p.x.p, xb + t * p.x.st);
-            la[j].load(p.la.p, lb + t * p.la.st);
-        }
-        if (static_cast<long>(at + 1) * kFwdTile > p.T) {
-            // past the end: a = 1 and nothing added, so the state passes through
-#pragma unroll
-            for (int j = 0; j < R; ++j)
-                if (t0 + j >= p.T) {
-                    x[j].zero();
-                    la[j].zero();
-                }
-        }
-    }
-
-    float A[8], H[8];
+    Raw2<XBF> x[R];
+    Raw2<LBF> la[R];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-        float xf[8], lf[8];
-        x[j].get(xf);
-        la[j].get(lf);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float a = decay(lf[i]);
-            const float v = xf[i] * gain<GAIN>(lf[i], a);
-            H[i] = j ? apply(a, H[i], v) : v;
-            A[i] = j ? join(A[i], a) : a;
-        }
+        const long t = min(t0 + j, p.T - 1);
+        x[j].load(p.x.p, b * p.x.sb + t * p.x.st, cc);
+        la[j].load(p.la.p, b * p.la.sb + t * p.la.st, cc);
     }
-    scan_groups<false>(A, H, lane);
-    if (lane >= 56) {
+    if (t0 + R > p.T) {
+        // past the end: a = 1 and nothing added, so the state passes through
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            totA[wave][c8 + i] = A[i];
-            totH[wave][c8 + i] = H[i];
-        }
-    }
-    __syncthreads();
-    if (wave == 0) {
-        const int ch = c0 + lane;  // one channel to a lane here
-        const bool in = ch < p.D;
-        float tA = totA[0][lane], tH = totH[0][lane];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) {
-            tH = apply(totA[w][lane], tH, totH[w][lane]);
-            tA = join(tA, totA[w][lane]);
-        }
-        const long word = (static_cast<long>(column) * p.tiles) * kCols + lane;
-        float h;
-        if (at == 0) {
-            h = p.h0 && in ? p.h0[static_cast<long>(b) * p.D + ch] : 0.0f;
-        } else {
-            if (at + 1 < p.tiles) publish(p.chain.agg + word + static_cast<long>(at) * kCols, pair_word(tA, tH));
-            h = look_back(p.chain.agg + word, p.chain.inc + word, at);
-        }
-        const float behind = apply(tA, h, tH);
-        if (at + 1 < p.tiles) publish(p.chain.inc + word + static_cast<long>(at) * kCols, pair_word(0.0f, behind));
-        else if (p.hT && in) p.hT[static_cast<long>(b) * p.D + ch] = behind;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            before[w][lane] = h;
-            const int t = w * 8 * R;  // of the tile
-            if (p.marks_out && t % PDN_SCAN_MARK == 0) {
-                const long tt = static_cast<long>(at) * kFwdTile + t;
-                const long marks = (p.T + PDN_SCAN_MARK - 1) / PDN_SCAN_MARK;
-                if (tt < p.T && in) p.marks_out[(b * marks + tt / PDN_SCAN_MARK) * p.D + ch] = h;
+        for (int j = 0; j < R; ++j)
+            if (t0 + j >= p.T) {
+                x[j].zero();
+                la[j].zero();
             }
-            h = apply(totA[w][lane], h, totH[w][lane]);
+    }
+
+    float a[R][2], v[R][2], A[2], H[2];
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float l = la[j].get(i);
+            a[j][i] = decay(l);
+            v[j][i] = x[j].get(i) * gain<GAIN>(l, a[j][i]);
+            H[i] = j ? apply(a[j][i], H[i], v[j][i]) : v[j][i];
+            A[i] = j ? join(A[i], a[j][i]) : a[j][i];
         }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        totA[wave][c2 + i] = A[i];
+        totH[wave][c2 + i] = H[i];
     }
     __syncthreads();
-    if constexpr (WRITE_H) {
-        float h[8];
+    if (wave < 2) {
+        const int k = wave * 64 + lane, ch = c0 + k;
+        const bool in = ch < p.D;
+        const long state = static_cast<long>(b) * p.D + ch;
+        float behind;
+        float h = meet<W>(p, totA, totH, column, at, k, at == 0 && p.h0 && in ? p.h0[state] : 0.0f, behind);
+        if (at + 1 == p.tiles && p.hT && in) p.hT[state] = behind;
+        const int marks = (p.T + PDN_SCAN_MARK - 1) / PDN_SCAN_MARK;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float a = __shfl_up(A[i], 8, 64), v = __shfl_up(H[i], 8, 64);
-            h[i] = before[wave][c8 + i];
-            if (lane >= 8) h[i] = apply(a, h[i], v);
+        for (int w = 0; w < W; ++w) {
+            before[w][k] = h;
+            const int t = at * kFwdTile + w * R;
+            if (p.marks_out && t % PDN_SCAN_MARK == 0 && t < p.T && in)
+                p.marks_out[(static_cast<long>(b) * marks + t / PDN_SCAN_MARK) * p.D + ch] = h;
+            h = apply(totA[w][k], h, totH[w][k]);
         }
-        const long hb = b * p.h.sb + c;
+    }
+    if constexpr (WRITE_H) {
+        __syncthreads();
+        f32x2 h = {before[wave][c2], before[wave][c2 + 1]};
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            float xf[8], lf[8];
-            x[j].get(xf);
-            la[j].get(lf);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float a = decay(lf[i]);
-                h[i] = apply(a, h[i], xf[i] * gain<GAIN>(lf[i], a));
-            }
-            if (t0 + j < p.T && c < p.D) store8<XBF>(p.h.p, hb + (t0 + j) * p.h.st, h);
+            for (int i = 0; i < 2; ++i) h[i] = apply(a[j][i], h[i], v[j][i]);
+            if (t0 + j < p.T && c < p.D)
+                Raw2<XBF>::store(p.h.p, b * p.h.sb + static_cast<long>(t0 + j) * p.h.st, c, h);
         }
     }
 }
@@ -333,164 +365,117 @@ __global__ void __launch_bounds__(kThreads) scan_fwd_kernel(ScanParams p) {
 // kind of map, run right to left.  The states h_{t-1} inside a tile come from
 // the kept state before it.
 template <bool XBF, bool LBF, int GAIN>
-__global__ void __launch_bounds__(kThreads) scan_bwd_kernel(ScanParams p) {
-    constexpr int R = kBwdR;
+__global__ void __launch_bounds__(64 * kBwdWaves, 4) scan_bwd_kernel(ScanParams p) {
+    constexpr int R = kBwdR, W = kBwdWaves;
     __shared__ int slot;
-    __shared__ float totA[kWaves][kCols], totH[kWaves][kCols];  // the waves' runs, forward
-    __shared__ float totB[kWaves][kCols], totG[kWaves][kCols];  // and backward
-    __shared__ float before[kWaves][kCols];  // the state before each wave's tokens
-    __shared__ float behind[kWaves][kCols];  // what reaches them from the right
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    __shared__ float totA[W][kCols], totH[W][kCols];  // the waves' runs, forward
+    __shared__ float totB[W][kCols], totG[W][kCols];  // and backward, the last wave's first
+    __shared__ float before[W][kCols];  // the state before each wave's tokens
+    __shared__ float behind[W][kCols];  // what reaches them from the right
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int column, at;
     deal(p, &slot, column, at);
     const int tile = p.tiles - 1 - at;
     const int b = column / p.strips, c0 = (column - b * p.strips) * kCols;
-    const int c8 = (lane & 7) * 8, c = c0 + c8;
-    const long t0 = static_cast<long>(tile) * kBwdTile + (tid >> 3) * R;
+    const int c2 = 2 * lane, c = c0 + c2;
+    const int cc = c < p.D ? c : 0;
+    const int t0 = tile * kBwdTile + wave * R;
 
-    Raw8<XBF> x[R], dh[R];
-    Raw8<LBF> la[R];
-    {
-        const int cc = c < p.D ? c : 0;
-        const long xb = b * p.x.sb + cc, lb = b * p.la.sb + cc, gb = b * p.dh.sb + cc;
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            const long t = t0 + j < p.T ? t0 + j : p.T - 1;
-            x[j].load(p.x.p, xb + t * p.x.st);
-            la[j].load(p.la.p, lb + t * p.la.st);
-            dh[j].load(p.dh.p, gb + t * p.dh.st);
-        }
-        if (at == 0) {
-#pragma unroll
-            for (int j = 0; j < R; ++j)
-                if (t0 + j >= p.T) {
-                    x[j].zero();
-                    la[j].zero();
-                    dh[j].zero();
-                }
-        }
-    }
-
-    float A[8], H[8], AG[8], G[8];
+    Raw2<XBF> x[R], dh[R];
+    Raw2<LBF> la[R];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-        float xf[8], lf[8];
-        x[j].get(xf);
-        la[j].get(lf);
+        const long t = min(t0 + j, p.T - 1);
+        x[j].load(p.x.p, b * p.x.sb + t * p.x.st, cc);
+        la[j].load(p.la.p, b * p.la.sb + t * p.la.st, cc);
+        dh[j].load(p.dh.p, b * p.dh.sb + t * p.dh.st, cc);
+    }
+    if (t0 + R > p.T) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float a = decay(lf[i]);
-            const float v = xf[i] * gain<GAIN>(lf[i], a);
-            H[i] = j ? apply(a, H[i], v) : v;
-            A[i] = j ? join(A[i], a) : a;
-        }
+        for (int j = 0; j < R; ++j)
+            if (t0 + j >= p.T) {
+                x[j].zero();
+                la[j].zero();
+                dh[j].zero();
+            }
+    }
+
+    float a[R][2], g[R][2], A[2], H[2], B[2], G[2];
+    {
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float l = la[j].get(i);
+                a[j][i] = decay(l);
+                g[j][i] = gain<GAIN>(l, a[j][i]);
+                const float v = x[j].get(i) * g[j][i];
+                H[i] = j ? apply(a[j][i], H[i], v) : v;
+                A[i] = j ? join(A[i], a[j][i]) : a[j][i];
+            }
+#pragma unroll
+        for (int j = R - 1; j >= 0; --j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float full = j < R - 1 ? dh[j].get(i) + G[i] : dh[j].get(i);
+                G[i] = join(full, a[j][i]);
+                B[i] = j < R - 1 ? join(B[i], a[j][i]) : a[j][i];
+            }
     }
 #pragma unroll
-    for (int j = R - 1; j >= 0; --j) {
-        float gf[8], lf[8];
-        dh[j].get(gf);
-        la[j].get(lf);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float a = decay(lf[i]);
-            const float g = j < R - 1 ? gf[i] + G[i] : gf[i];
-            G[i] = join(g, a);
-            AG[i] = j < R - 1 ? join(AG[i], a) : a;
-        }
-    }
-    scan_groups<false>(A, H, lane);
-    scan_groups<true>(AG, G, lane);
-    if (lane >= 56) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            totA[wave][c8 + i] = A[i];
-            totH[wave][c8 + i] = H[i];
-        }
-    }
-    if (lane < 8) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            totB[wave][c8 + i] = AG[i];
-            totG[wave][c8 + i] = G[i];
-        }
+    for (int i = 0; i < 2; ++i) {
+        totA[wave][c2 + i] = A[i];
+        totH[wave][c2 + i] = H[i];
+        totB[W - 1 - wave][c2 + i] = B[i];
+        totG[W - 1 - wave][c2 + i] = G[i];
     }
     __syncthreads();
-    if (wave == 0) {
-        const int ch = c0 + lane;
+    if (wave < 2) {
+        const int k = wave * 64 + lane, ch = c0 + k;
         const bool in = ch < p.D;
         const long state = static_cast<long>(b) * p.D + ch;
-        float tA = totB[kWaves - 1][lane], tG = totG[kWaves - 1][lane];
-#pragma unroll
-        for (int w = kWaves - 2; w >= 0; --w) {
-            tG = apply(totB[w][lane], tG, totG[w][lane]);
-            tA = join(tA, totB[w][lane]);
-        }
-        const long word = (static_cast<long>(column) * p.tiles) * kCols + lane;
-        float h = 0.0f, g;
+        float h = 0.0f, out;
         if (in && p.marks) h = p.marks[(static_cast<long>(b) * p.tiles + tile) * p.D + ch];
         else if (in && p.h0) h = p.h0[state];
-        if (at == 0) {
-            g = p.dhT && in ? p.dhT[state] : 0.0f;
-        } else {
-            if (at + 1 < p.tiles) publish(p.chain.agg + word + static_cast<long>(at) * kCols, pair_word(tA, tG));
-            g = look_back(p.chain.agg + word, p.chain.inc + word, at);
-        }
-        const float out = apply(tA, g, tG);
-        if (at + 1 < p.tiles) publish(p.chain.inc + word + static_cast<long>(at) * kCols, pair_word(0.0f, out));
-        else if (p.dh0 && in) p.dh0[state] = out;
+        float r = meet<W>(p, totB, totG, column, at, k, at == 0 && p.dhT && in ? p.dhT[state] : 0.0f, out);
+        if (at + 1 == p.tiles && p.dh0 && in) p.dh0[state] = out;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            before[w][lane] = h;
-            h = apply(totA[w][lane], h, totH[w][lane]);
-        }
-#pragma unroll
-        for (int w = kWaves - 1; w >= 0; --w) {
-            behind[w][lane] = g;
-            g = apply(totB[w][lane], g, totG[w][lane]);
+        for (int w = 0; w < W; ++w) {
+            before[w][k] = h;
+            h = apply(totA[w][k], h, totH[w][k]);
+            behind[W - 1 - w][k] = r;
+            r = apply(totB[w][k], r, totG[w][k]);
         }
     }
     __syncthreads();
-    float h[8], g[8], prev[R][8];
+    // dlog_a = G (a h_{t-1} + g' x): the bracket forward, then G backward
+    float q[R][2];
+    {
+        float h[2] = {before[wave][c2], before[wave][c2 + 1]};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float a = __shfl_up(A[i], 8, 64), v = __shfl_up(H[i], 8, 64);
-        const float ag = __shfl_down(AG[i], 8, 64), vg = __shfl_down(G[i], 8, 64);
-        h[i] = before[wave][c8 + i];
-        if (lane >= 8) h[i] = apply(a, h[i], v);
-        g[i] = behind[wave][c8 + i];
-        if (lane < 56) g[i] = apply(ag, g[i], vg);
-    }
+        for (int j = 0; j < R; ++j) {
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-        float xf[8], lf[8];
-        x[j].get(xf);
-        la[j].get(lf);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float a = decay(lf[i]);
-            prev[j][i] = h[i];
-            if (j + 1 < R) h[i] = apply(a, h[i], xf[i] * gain<GAIN>(lf[i], a));
+            for (int i = 0; i < 2; ++i) {
+                const float xf = x[j].get(i), kept = join(h[i], a[j][i]);
+                q[j][i] = GAIN == PDN_GAIN_NONE ? kept : fmaf(gain_slope<GAIN>(a[j][i], g[j][i]), xf, kept);
+                h[i] = fmaf(xf, g[j][i], kept);
+            }
         }
     }
-    const long xb = b * p.dx.sb + c, lb = b * p.dla.sb + c;
+    float r[2] = {behind[wave][c2], behind[wave][c2 + 1]};
 #pragma unroll
     for (int j = R - 1; j >= 0; --j) {
-        float xf[8], lf[8], gf[8], dx[8], dl[8];
-        x[j].get(xf);
-        la[j].get(lf);
-        dh[j].get(gf);
+        f32x2 dx, dl;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float a = decay(lf[i]), k = gain<GAIN>(lf[i], a);
-            const float full = gf[i] + g[i];
-            dx[i] = GAIN == PDN_GAIN_NONE ? full : k * full;
-            dl[i] = join(prev[j][i], a) * full;
-            if constexpr (GAIN != PDN_GAIN_NONE) dl[i] = fmaf(gain_slope<GAIN>(a, k) * xf[i], full, dl[i]);
-            g[i] = join(full, a);
+        for (int i = 0; i < 2; ++i) {
+            const float full = dh[j].get(i) + r[i];
+            dx[i] = GAIN == PDN_GAIN_NONE ? full : g[j][i] * full;
+            dl[i] = q[j][i] * full;
+            r[i] = join(full, a[j][i]);
         }
         if (t0 + j < p.T && c < p.D) {
-            store8<XBF>(p.dx.p, xb + (t0 + j) * p.dx.st, dx);
-            store8<LBF>(p.dla.p, lb + (t0 + j) * p.dla.st, dl);
+            Raw2<XBF>::store(p.dx.p, b * p.dx.sb + static_cast<long>(t0 + j) * p.dx.st, c, dx);
+            Raw2<LBF>::store(p.dla.p, b * p.dla.sb + static_cast<long>(t0 + j) * p.dla.st, c, dl);
         }
     }
 }
@@ -520,10 +505,9 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(pdn_scan_step_args 
     store8<XBF>(a.h, b * a.h_sb + c, h);
 }
 
-// Before the tiles: counters to zero, every word to "not there yet".
-__global__ void __launch_bounds__(kThreads) scan_reset_kernel(unsigned* counters, u32x4* words, long n) {
+// Before the tiles: every word to "not there yet", every counter below 0.
+__global__ void __launch_bounds__(kThreads) scan_reset_kernel(u32x4* words, long n) {
     const long step = static_cast<long>(gridDim.x) * kThreads;
-    if (blockIdx.x == 0 && threadIdx.x < 2) counters[threadIdx.x] = 0u;
     for (long i = static_cast<long>(blockIdx.x) * kThreads + threadIdx.x; i < n; i += step)
         words[i] = u32x4{~0u, ~0u, ~0u, ~0u};
 }
@@ -534,15 +518,13 @@ __global__ void __launch_bounds__(kThreads) scan_state_kernel(float* dst, const 
     if (i < n) dst[i] = src ? src[i] : 0.0f;
 }
 
-// Workspace: two counters in the first 256 bytes, then the words of the
-// forward's tiles, then those of the backward's, then the backward's marks.
-constexpr size_t kCounterBytes = 256;
-
+// Workspace: the chain of a backward's tiles, then that of a forward's (each
+// its counters, then its words), then the marks that a backward forms.
 long strips(const pdn_scan_args& a) { return (a.D + kCols - 1L) / kCols; }
 long tiles(const pdn_scan_args& a, int tile) { return (a.T + tile - 1L) / tile; }
-size_t chain_words(const pdn_scan_args& a, int tile) {
-    const long n = tiles(a, tile);
-    return n > 1 ? static_cast<size_t>(a.B) * strips(a) * n * kCols * 2 : 0;
+size_t chain_bytes(const pdn_scan_args& a, int tile) {
+    const size_t n = tiles(a, tile), columns = a.B * strips(a);
+    return n > 1 ? columns * (kCounterStep * sizeof(unsigned) + n * kCols * 2 * sizeof(u64)) : 0;
 }
 
 ScanParams params(const pdn_scan_args& a) {
@@ -557,27 +539,25 @@ ScanParams params(const pdn_scan_args& a) {
     return p;
 }
 
-void set_chain(ScanParams& p, unsigned* counter, u64* words) {
-    p.chain.counter = counter;
-    p.chain.agg = words;
-    p.chain.inc = words + static_cast<long>(p.columns) * p.tiles * kCols;
+void set_chain(ScanParams& p, char* at) {
+    p.chain.counters = reinterpret_cast<unsigned*>(at);
+    p.chain.agg = reinterpret_cast<u64*>(at + sizeof(unsigned) * kCounterStep * p.columns);
+    p.chain.inc = p.chain.agg + static_cast<long>(p.columns) * p.tiles * kCols;
 }
 
-hipError_t reset(void* workspace, size_t words, hipStream_t st) {
-    const long n = static_cast<long>(words / 2);  // 16 bytes each
-    long blocks = (n + kThreads - 1) / kThreads;
-    if (blocks > 2048) blocks = 2048;
-    if (blocks < 1) blocks = 1;
-    scan_reset_kernel<<<dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st>>>(
-        static_cast<unsigned*>(workspace), reinterpret_cast<u32x4*>(static_cast<char*>(workspace) + kCounterBytes), n);
+hipError_t reset(void* workspace, size_t bytes, hipStream_t st) {
+    const long n = static_cast<long>(bytes / sizeof(u32x4));
+    const long blocks = (n + kThreads - 1) / kThreads;
+    scan_reset_kernel<<<dim3(static_cast<unsigned>(blocks < 2048 ? blocks : 2048)), dim3(kThreads), 0, st>>>(
+        static_cast<u32x4*>(workspace), n);
     return hipGetLastError();
 }
 
 template <bool XBF, bool LBF, int GAIN>
 void launch_tiles(const ScanParams& p, int kind, dim3 grid, hipStream_t st) {
-    if (kind == 0) scan_fwd_kernel<XBF, LBF, GAIN, true><<<grid, dim3(kThreads), 0, st>>>(p);
-    else if (kind == 1) scan_fwd_kernel<XBF, LBF, GAIN, false><<<grid, dim3(kThreads), 0, st>>>(p);
-    else scan_bwd_kernel<XBF, LBF, GAIN><<<grid, dim3(kThreads), 0, st>>>(p);
+    if (kind == 0) scan_fwd_kernel<XBF, LBF, GAIN, true><<<grid, dim3(64 * kFwdWaves), 0, st>>>(p);
+    else if (kind == 1) scan_fwd_kernel<XBF, LBF, GAIN, false><<<grid, dim3(64 * kFwdWaves), 0, st>>>(p);
+    else scan_bwd_kernel<XBF, LBF, GAIN><<<grid, dim3(64 * kBwdWaves), 0, st>>>(p);
 }
 
 // kind: 0 forward, 1 forward for the marks alone, 2 backward
@@ -606,20 +586,15 @@ hipError_t copy_state(float* dst, const float* src, const pdn_scan_args& a, hipS
 
 }  // namespace
 
-long scan_blocks(const pdn_scan_args& a) { return a.B * strips(a) * tiles(a, kBwdTile); }
+long scan_blocks(const pdn_scan_args& a) { return a.B * strips(a) * tiles(a, kFwdTile < kBwdTile ? kFwdTile : kBwdTile); }
 
-size_t scan_fwd_workspace_bytes(const pdn_scan_args& a) {
-    const size_t words = chain_words(a, kFwdTile);
-    return words ? kCounterBytes + words * sizeof(u64) : 0;
-}
+size_t scan_fwd_workspace_bytes(const pdn_scan_args& a) { return chain_bytes(a, kFwdTile); }
 
 size_t scan_bwd_workspace_bytes(const pdn_scan_bwd_args& b) {
     const pdn_scan_args& a = b.fwd;
-    const size_t words = chain_words(a, kBwdTile);
-    if (!words) return 0;  // one tile: from h0 to dhT
-    size_t n = kCounterBytes + words * sizeof(u64);
-    if (!a.marks) n += chain_words(a, kFwdTile) * sizeof(u64) + sizeof(float) * a.B * static_cast<size_t>(tiles(a, kBwdTile)) * a.D;
-    return n;
+    const size_t n = chain_bytes(a, kBwdTile);
+    if (n == 0 || a.marks) return n;  // one tile runs from h0 to dhT
+    return n + chain_bytes(a, kFwdTile) + sizeof(float) * a.B * static_cast<size_t>(tiles(a, kBwdTile)) * a.D;
 }
 
 hipError_t launch_scan_fwd(const pdn_scan_args& a, hipStream_t st) {
@@ -630,9 +605,9 @@ hipError_t launch_scan_fwd(const pdn_scan_args& a, hipStream_t st) {
     p.marks_out = a.marks;
     p.tiles = static_cast<int>(tiles(a, kFwdTile));
     if (p.tiles > 1) {
-        const hipError_t e = reset(a.workspace, chain_words(a, kFwdTile), st);
+        const hipError_t e = reset(a.workspace, chain_bytes(a, kFwdTile), st);
         if (e != hipSuccess) return e;
-        set_chain(p, static_cast<unsigned*>(a.workspace), reinterpret_cast<u64*>(static_cast<char*>(a.workspace) + kCounterBytes));
+        set_chain(p, static_cast<char*>(a.workspace));
     }
     return launch_kind(p, a, 0, st);
 }
@@ -649,21 +624,20 @@ hipError_t launch_scan_bwd(const pdn_scan_bwd_args& b, hipStream_t st) {
     p.marks = a.marks;
     p.tiles = static_cast<int>(tiles(a, kBwdTile));
     if (p.tiles > 1) {
-        unsigned* counters = static_cast<unsigned*>(b.workspace);
-        u64* words = reinterpret_cast<u64*>(static_cast<char*>(b.workspace) + kCounterBytes);
-        const size_t fwd = a.marks ? 0 : chain_words(a, kFwdTile), bwd = chain_words(a, kBwdTile);
-        hipError_t e = reset(b.workspace, fwd + bwd, st);
+        char* ws = static_cast<char*>(b.workspace);
+        const size_t bwd = chain_bytes(a, kBwdTile), fwd = a.marks ? 0 : chain_bytes(a, kFwdTile);
+        hipError_t e = reset(ws, bwd + fwd, st);
         if (e != hipSuccess) return e;
+        set_chain(p, ws);
         if (!a.marks) {
             ScanParams f = params(a);
-            f.marks_out = reinterpret_cast<float*>(words + fwd + bwd);
+            f.marks_out = reinterpret_cast<float*>(ws + bwd + fwd);
             f.tiles = static_cast<int>(tiles(a, kFwdTile));
-            set_chain(f, counters + 1, words);
+            set_chain(f, ws + bwd);
             e = launch_kind(f, a, 1, st);
             if (e != hipSuccess) return e;
             p.marks = f.marks_out;
         }
-        set_chain(p, counters, words + fwd);
     }
     return launch_kind(p, a, 2, st);
 }

@@ -486,7 +486,7 @@ typedef struct pdn_out_norm_bwd_args {
 #define PDN_GAIN_NORM 2
 
 /* Tokens between two of the scan's kept states (see marks). */
-#define PDN_SCAN_MARK 128
+#define PDN_SCAN_MARK 96
 
 /*
  * The gated linear recurrence with a vector state, per channel:

@@ -214,9 +214,9 @@ def test_what_is_not_read_is_not_checked(lib):
     a.x_st, a.x_sb, a.log_a_sb = 0, 0, 0         # inputs may repeat
     assert _check(lib, "pdn_scan_fwd", a) == pdn.PDN_OK
     a = _scan()
-    a.T, a.workspace, a.workspace_bytes = 256, None, 0
+    a.T, a.workspace, a.workspace_bytes = 1, None, 0     # one workgroup's span
     assert _check(lib, "pdn_scan_fwd", a) == pdn.PDN_OK
-    a.T = 257
+    a.T = 1000
     assert _check(lib, "pdn_scan_fwd", a) == pdn.PDN_EWORKSPACE
 
 
@@ -232,7 +232,8 @@ def test_calls_without_a_gpu_tensor_are_refused():
 
 
 def test_marks():
-    assert [pdn.pdn_scan_marks(t) for t in (0, 1, 128, 129, 1000)] == [0, 1, 1, 2, 8]
+    m = pdn.PDN_SCAN_MARK
+    assert [pdn.pdn_scan_marks(t) for t in (0, 1, m, m + 1, 10 * m - 1)] == [0, 1, 1, 2, 10]
 
 
 def test_inverse_frequencies():

@@ -359,7 +359,7 @@ def test_scan(case):
     _close("scan h", h, want, bound, dt)
     _close("scan hT", hT, want[:, -1], bound[:, -1])
     assert bool((wide[:, :, :8] == 7.0).all()) and bool((wide[:, :, 8 + D:] == 7.0).all())
-    at = np.arange(0, T, 128)
+    at = np.arange(0, T, pdn.PDN_SCAN_MARK)
     first = np.zeros((B, 1, D)) if h0 is None else f64(h0)[:, None]
     before, beforeb = (np.concatenate([f, v[:, :-1]], 1)[:, at] for f, v in ((first, want), (0 * first, bound)))
     _close("scan marks", marks, before, beforeb)
