@@ -583,13 +583,22 @@ def pdn_decode_step(q, k, v, o, S, log_alpha=None, beta=None, gamma=None,
 # the operators around the recurrence
 # ---------------------------------------------------------------------------
 
-def _dtype_of(t, name):
+_torch = None   # torch and its types' codes, from the first call on: a single-token call is
+_CODES = {}     # mostly host time, and an import statement in each of its functions is part of it
+
+
+def _use_torch():
+    global _torch
     import torch
-    if t.dtype == torch.bfloat16:
-        return PDN_BF16
-    if t.dtype == torch.float32:
-        return PDN_F32
-    raise ValueError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
+    _CODES.update({torch.float32: PDN_F32, torch.bfloat16: PDN_BF16})
+    _torch = torch
+
+
+def _dtype_of(t, name):
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise ValueError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
+    return code
 
 
 class _Call:
@@ -602,6 +611,8 @@ class _Call:
     __slots__ = ("a", "index")
 
     def __init__(self, struct, first):
+        if _torch is None:
+            _use_torch()
         index = first.get_device() if hasattr(first, "get_device") else -1
         if index < 0:
             raise ValueError("the first argument must be a tensor in device memory")
@@ -648,26 +659,25 @@ class _Call:
         device, with that device current.  A workspace that the caller does not
         give comes from torch's caching allocator, allocated on the launch's own
         stream, whose order then protects its reuse."""
-        import torch
-        if self.index != torch.cuda.current_device():
-            with torch.cuda.device(self.index):
+        if self.index != _torch.cuda.current_device():
+            with _torch.cuda.device(self.index):
                 return self.launch(name, stream, workspace)
         a, size = self.a, _AROUND[name][2]
         if size:
             if workspace is None:
                 n = self.size(size)
                 if n and stream is not None:
-                    own = torch.cuda.ExternalStream(stream, device=self.index) if isinstance(stream, int) else stream
-                    with torch.cuda.stream(own):
-                        workspace = torch.empty(n, dtype=torch.uint8, device="cuda")
+                    own = _torch.cuda.ExternalStream(stream, device=self.index) if isinstance(stream, int) else stream
+                    with _torch.cuda.stream(own):
+                        workspace = _torch.empty(n, dtype=_torch.uint8, device="cuda")
                 elif n:
-                    workspace = torch.empty(n, dtype=torch.uint8, device="cuda")
+                    workspace = _torch.empty(n, dtype=_torch.uint8, device="cuda")
             elif workspace.get_device() != self.index:
                 raise ValueError("workspace must be on cuda:%d" % self.index)
             if workspace is not None:
                 a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
         if stream is None:
-            stream = torch._C._cuda_getCurrentRawStream(self.index)
+            stream = _torch._C._cuda_getCurrentRawStream(self.index)
         elif not isinstance(stream, int):
             stream = stream.cuda_stream
         rc = getattr(load_library(), name)(ctypes.byref(a), stream)
@@ -676,7 +686,6 @@ class _Call:
 
 
 def _qk_norm(c, a, xq, xk, H, norm, eps, wq, wk, q_scale, k_scale, inv_freq, positions, rope_layout, rope_scale):
-    import torch
     if xq.dim() != 4 or xk.dim() != 4:
         raise ValueError("xq and xk must be [B,T,heads,d]")
     B, T, Hq, d = xq.shape
@@ -686,12 +695,12 @@ def _qk_norm(c, a, xq, xk, H, norm, eps, wq, wk, q_scale, k_scale, inv_freq, pos
     a.xq, a.xk = c.rows(xq, "xq", (B, T, Hq, d), dtype), c.rows(xk, "xk", (B, T, Hk, d), dtype)
     a.xq_sb, a.xq_st, a.xq_sh, _ = xq.stride()
     a.xk_sb, a.xk_st, a.xk_sh, _ = xk.stride()
-    a.wq, a.wk = c.plain(wq, "wq", (d,), torch.float32), c.plain(wk, "wk", (d,), torch.float32)
+    a.wq, a.wk = c.plain(wq, "wq", (d,), _torch.float32), c.plain(wk, "wk", (d,), _torch.float32)
     if inv_freq is not None:
         half = inv_freq.shape[0]
         a.rot_dim, a.rope_layout, a.rope_scale = 2 * half, rope_layout, rope_scale
-        a.inv_freq = c.plain(inv_freq, "inv_freq", (half,), torch.float64)
-        a.positions = c.plain(positions, "positions", (B, T), torch.int64)
+        a.inv_freq = c.plain(inv_freq, "inv_freq", (half,), _torch.float64)
+        a.positions = c.plain(positions, "positions", (B, T), _torch.int64)
     elif positions is not None:
         raise ValueError("positions need inv_freq")
     return B, T, d
@@ -718,13 +727,12 @@ def pdn_qk_norm_fwd(xq, xk, q, k, norm=PDN_NORM_L2, eps=1e-6, wq=None, wk=None, 
 
 def _qk_norm_bwd(xq, xk, dq, dk, dxq, dxk, dwq, dwk, norm, eps, wq, wk, q_scale, k_scale, inv_freq, positions,
                  rope_layout, rope_scale):
-    import torch
     c = _Call(QkNormBwdArgs, xq)
     if dq.dim() != 4:
         raise ValueError("dq and dk must be [B,H,T,d]")
     a, H = c.a, dq.shape[1]
     B, T, d = _qk_norm(c, a.fwd, xq, xk, H, norm, eps, wq, wk, q_scale, k_scale, inv_freq, positions, rope_layout, rope_scale)
-    f32 = torch.float32
+    f32 = _torch.float32
     a.dq, a.dk = c.plain(dq, "dq", (B, H, T, d), f32), c.plain(dk, "dk", (B, H, T, d), f32)
     a.dxq, a.dxk = c.rows(dxq, "dxq", xq.shape, xq.dtype), c.rows(dxk, "dxk", xk.shape, xq.dtype)
     a.dxq_sb, a.dxq_st, a.dxq_sh, _ = dxq.stride()
@@ -760,7 +768,6 @@ def _strides(a, field, t):
 
 
 def _out_norm(c, a, o, z, w, like, act, eps):
-    import torch
     if o.dim() != 4:
         raise ValueError("o must be [B,H,T,dv]")
     B, H, T, dv = o.shape
@@ -770,7 +777,7 @@ def _out_norm(c, a, o, z, w, like, act, eps):
     a.o = c.plain(o, "o", (B, H, T, dv), o.dtype)
     a.z = c.rows(z, "z", (B, T, H, dv), like.dtype)
     _strides(a, "z", z)
-    a.w = c.plain(w, "w", (dv,), torch.float32)
+    a.w = c.plain(w, "w", (dv,), _torch.float32)
     return B, T, H, dv
 
 
@@ -787,15 +794,14 @@ def pdn_out_norm_fwd(o, y, z=None, w=None, act=None, eps=1e-6, stream=None) -> N
 
 
 def _out_norm_bwd(o, dy, do, z, dz, w, dw, act, eps):
-    import torch
     c = _Call(OutNormBwdArgs, o)
     a = c.a
     shape = _out_norm(c, a.fwd, o, z, w, dy, act, eps)
     a.dy, a.dz = c.rows(dy, "dy", shape, dy.dtype), c.rows(dz, "dz", shape, dy.dtype)
     _strides(a, "dy", dy)
     _strides(a, "dz", dz)
-    a.d_o = c.plain(do, "do", o.shape, torch.float32)
-    a.dw = c.plain(dw, "dw", shape[-1:], torch.float32)
+    a.d_o = c.plain(do, "do", o.shape, _torch.float32)
+    a.dw = c.plain(dw, "dw", shape[-1:], _torch.float32)
     return c
 
 
@@ -817,7 +823,6 @@ def pdn_scan_marks(T: int) -> int:
 
 
 def _scan(c, a, x, log_a, h0, marks, gain):
-    import torch
     if x.dim() != 3:
         raise ValueError("x must be [B,T,D]")
     B, T, D = x.shape
@@ -826,19 +831,18 @@ def _scan(c, a, x, log_a, h0, marks, gain):
     a.x, a.log_a = c.rows(x, "x", (B, T, D), x.dtype), c.rows(log_a, "log_a", (B, T, D), log_a.dtype)
     a.x_sb, a.x_st, _ = x.stride()
     a.log_a_sb, a.log_a_st, _ = log_a.stride()
-    a.h0 = c.plain(h0, "h0", (B, D), torch.float32)
-    a.marks = c.plain(marks, "marks", (B, pdn_scan_marks(T), D), torch.float32)
+    a.h0 = c.plain(h0, "h0", (B, D), _torch.float32)
+    a.marks = c.plain(marks, "marks", (B, pdn_scan_marks(T), D), _torch.float32)
     return B, T, D
 
 
 def _scan_fwd(x, log_a, h, h0, hT, marks, gain):
-    import torch
     c = _Call(ScanArgs, x)
     a = c.a
     B, T, D = _scan(c, a, x, log_a, h0, marks, gain)
     a.h = c.rows(h, "h", (B, T, D), x.dtype)
     a.h_sb, a.h_st, _ = h.stride()
-    a.hT = c.plain(hT, "hT", (B, D), torch.float32)
+    a.hT = c.plain(hT, "hT", (B, D), _torch.float32)
     return c
 
 
@@ -856,7 +860,6 @@ def pdn_scan_fwd(x, log_a, h, h0=None, hT=None, marks=None, gain=PDN_GAIN_NONE, 
 
 
 def _scan_bwd(x, log_a, dh, dx, dlog_a, h0, dhT, dh0, marks, gain):
-    import torch
     c = _Call(ScanBwdArgs, x)
     a = c.a
     B, T, D = _scan(c, a.fwd, x, log_a, h0, marks, gain)
@@ -865,7 +868,7 @@ def _scan_bwd(x, log_a, dh, dx, dlog_a, h0, dhT, dh0, marks, gain):
     a.dh_sb, a.dh_st, _ = dh.stride()
     a.dx_sb, a.dx_st, _ = dx.stride()
     a.dlog_a_sb, a.dlog_a_st, _ = dlog_a.stride()
-    a.dhT, a.dh0 = c.plain(dhT, "dhT", (B, D), torch.float32), c.plain(dh0, "dh0", (B, D), torch.float32)
+    a.dhT, a.dh0 = c.plain(dhT, "dhT", (B, D), _torch.float32), c.plain(dh0, "dh0", (B, D), _torch.float32)
     return c
 
 
@@ -884,7 +887,6 @@ def pdn_scan_bwd(x, log_a, dh, dx, dlog_a, h0=None, dhT=None, dh0=None, marks=No
 def pdn_scan_step(x, log_a, h, h_prev, h_next, gain=PDN_GAIN_NONE, stream=None) -> None:
     """One token of the recurrence for every sequence: x, log_a, h [B,D]
     (views are fine), h_prev and h_next fp32 [B,D], which may be one tensor."""
-    import torch
     c = _Call(ScanStepArgs, x)
     if x.dim() != 2:
         raise ValueError("x must be [B,D]")
@@ -894,7 +896,7 @@ def pdn_scan_step(x, log_a, h, h_prev, h_next, gain=PDN_GAIN_NONE, stream=None) 
     a.dtype, a.log_dtype, a.gain = _dtype_of(x, "x"), _dtype_of(log_a, "log_a"), gain
     a.x, a.log_a, a.h = c.rows(x, "x", (B, D), x.dtype), c.rows(log_a, "log_a", (B, D), log_a.dtype), c.rows(h, "h", (B, D), x.dtype)
     a.x_sb, a.log_a_sb, a.h_sb = x.stride(0), log_a.stride(0), h.stride(0)
-    a.h_prev, a.h_next = c.plain(h_prev, "h_prev", (B, D), torch.float32), c.plain(h_next, "h_next", (B, D), torch.float32)
+    a.h_prev, a.h_next = c.plain(h_prev, "h_prev", (B, D), _torch.float32), c.plain(h_next, "h_next", (B, D), _torch.float32)
     c.launch("pdn_scan_step", stream)
 
 
