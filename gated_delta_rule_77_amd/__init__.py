@@ -168,7 +168,7 @@ _AROUND = {"pdn_qk_norm_fwd": (QkNormArgs, "pdn_qk_norm_check", None),
 EXPORTED = ("pdn_abi_version", "pdn_strerror", "pdn_chunk_fwd_workspace_size",
             "pdn_chunk_fwd_check", "pdn_chunk_fwd", "pdn_chunk_fwd_noalloc", "pdn_decode_check",
             "pdn_decode_step", "pdn_chunk_bwd_workspace_size", "pdn_chunk_bwd_check",
-            "pdn_chunk_bwd", "pdn_rope_freqs",
+            "pdn_chunk_bwd", "pdn_rope_freqs", "pdn_scan_marks",
             *(n for call, (_, check, size) in _AROUND.items() for n in (call, check, size) if n))
 
 _lib = None
@@ -225,6 +225,8 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
             for n in (name, check, size):
                 if n:
                     getattr(lib, n).restype = ctypes.c_int
+        lib.pdn_scan_marks.argtypes = [_I]
+        lib.pdn_scan_marks.restype = ctypes.c_int
         lib.pdn_rope_freqs.argtypes = [_I, ctypes.c_double, _I, ctypes.c_double, _L,
                                        ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_F)]
         lib.pdn_rope_freqs.restype = ctypes.c_int
@@ -819,7 +821,10 @@ def pdn_out_norm_bwd(o, dy, do, z=None, dz=None, w=None, dw=None, act=None, eps=
 
 def pdn_scan_marks(T: int) -> int:
     """How many states a scan over T tokens keeps in `marks`."""
-    return -(-int(T) // PDN_SCAN_MARK)
+    n = load_library().pdn_scan_marks(int(T))
+    if n < 0:
+        raise PdnError(n, "pdn_scan_marks")
+    return n
 
 
 def _scan(c, a, x, log_a, h0, marks, gain):

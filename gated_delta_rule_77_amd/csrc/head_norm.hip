@@ -59,52 +59,49 @@ struct QkParams {
     int norm;
 };
 
-// cos and sin of the angles of this lane's eight elements, times rope_scale:
-// out_i = n_i c_i + n_partner s_i, so s carries the sign of its element; (1, 0)
-// behind the rotated part.  The angle is formed in turns in 64 bits: position
-// times frequency keeps its fraction to 1e-9 turns at positions of millions,
-// where 32 bits would leave 1e-1.
-template <int ROPE>
-__device__ __forceinline__ void angles(const QkParams& p, int b, int t, int n, int e, float (&c)[8],
-                                       float (&s)[8]) {
-    const double pos = p.positions ? static_cast<double>(p.positions[n]) : static_cast<double>(t);
-    const int half = p.rot >> 1;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int i = 8 * e + j;
-        c[j] = 1.0f;
-        s[j] = 0.0f;
-        if (i < p.rot) {
-            int pair;
-            bool first;
-            if constexpr (ROPE == ROPE_HALF) {
-                first = i < half;
-                pair = first ? i : i - half;
-            } else {
-                first = !(i & 1);
-                pair = i >> 1;
-            }
-            if (ROPE == ROPE_PAIRS && (j & 1)) {  // the pair's second element: the same angle
-                c[j] = c[j - 1];
-                s[j] = -s[j - 1];
-                continue;
-            }
-            const double turns = pos * p.inv_freq[pair] * 0.15915494309189535;  // 1 / (2 pi)
-            const float f = static_cast<float>(turns - rint(turns));
-            float sn, cn;
-            sincospif(2.0f * f, &sn, &cn);
-            c[j] = cn * p.rope_scale;
-            s[j] = (first ? -sn : sn) * p.rope_scale;
-        }
-    }
-}
-
 // The lane that holds this lane's partner elements in the half layout (rot is
 // a multiple of 16, so that a lane's eight elements have theirs in one lane);
 // itself behind the rotated part.
 __device__ __forceinline__ int half_partner(int lane, int e, int rot) {
     const int h8 = rot >> 4;
     return e < h8 ? lane + h8 : e < 2 * h8 ? lane - h8 : lane;
+}
+
+// cos and sin of the angles of this lane's eight elements, times rope_scale:
+// out_i = n_i c_i + n_partner s_i, so s carries the sign of its element; (1, 0)
+// behind the rotated part.  The angle is formed in turns in 64 bits: position
+// times frequency keeps its fraction to 1e-9 turns at positions of millions,
+// where 32 bits would leave 1e-1.  Two elements share each angle: in the half
+// layout the lane `pl` holds the others, and each of the two lanes forms four.
+template <int ROPE>
+__device__ __forceinline__ void angles(const QkParams& p, int t, int n, int e, int pl, float (&c)[8], float (&s)[8]) {
+    const double pos = p.positions ? static_cast<double>(p.positions[n]) : static_cast<double>(t);
+    const bool rotated = 8 * e < p.rot;  // rot is a multiple of 16: all of a lane's elements, or none
+    const bool second = ROPE == ROPE_HALF && 16 * e >= p.rot;
+    const int pair0 = ROPE == ROPE_HALF ? 8 * e - (second ? (p.rot >> 1) - 4 : 0) : 4 * e;
+    float cn[4], sn[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const double f = rotated ? p.inv_freq[pair0 + j] : 0.0;
+        const double turns = pos * f * 0.15915494309189535;  // 1 / (2 pi)
+        sincospif(2.0f * static_cast<float>(turns - rint(turns)), &sn[j], &cn[j]);
+        cn[j] = rotated ? cn[j] * p.rope_scale : 1.0f;
+        sn[j] = rotated ? sn[j] * p.rope_scale : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (ROPE == ROPE_HALF) {
+            const float co = __shfl(cn[j], pl, 64), so = __shfl(sn[j], pl, 64);
+            c[j] = second ? co : cn[j];
+            c[4 + j] = second ? cn[j] : co;
+            s[j] = second ? so : -sn[j];
+            s[4 + j] = second ? sn[j] : -so;
+        } else {
+            c[2 * j] = c[2 * j + 1] = cn[j];
+            s[2 * j] = -sn[j];
+            s[2 * j + 1] = sn[j];
+        }
+    }
 }
 
 template <int ROPE>
@@ -122,26 +119,38 @@ template <bool BF16, int D, int ROPE>
 __global__ void __launch_bounds__(kThreads) qk_norm_fwd_kernel(QkParams p) {
     constexpr int LPR = D / 8, SLOTS = kThreads / LPR;
     const int tid = threadIdx.x, lane = tid & 63, e = tid % LPR;
-    const long want = static_cast<long>(blockIdx.x) * SLOTS + tid / LPR;
+    const long want = static_cast<long>(by_xcd(blockIdx.x, gridDim.x)) * SLOTS + tid / LPR;
     const bool valid = want < p.tokens;
     const int n = valid ? static_cast<int>(want) : p.tokens - 1;  // idle lanes repeat the last token, unstored
     const int b = n / p.T, t = n - b * p.T;
 
-    float c[8], s[8];
-    int pl = lane;
-    if constexpr (ROPE != ROPE_NONE) {
-        angles<ROPE>(p, b, t, n, e, c, s);
-        if constexpr (ROPE == ROPE_HALF) pl = half_partner(lane, e, p.rot);
-    }
-
     const int first = blockIdx.y * p.heads_per_block;
     const int last = min(first + p.heads_per_block, p.side[0].heads + p.side[1].heads);
+    // a side's heads in this workgroup, and the loads of its first ones ahead of the angles
+    int h0[2], h1[2];
+    long row[2];
+    Raw8<BF16> raw[2][kUnroll];
+    auto load = [&](int k, int h) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) raw[k][u].stream(p.side[k].x.p, row[k] + min(h + u, h1[k] - 1) * p.side[k].x.sh);
+    };
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int skip = k ? p.side[0].heads : 0;
+        h0[k] = max(first - skip, 0);
+        h1[k] = min(last - skip, p.side[k].heads);
+        row[k] = b * p.side[k].x.sb + t * p.side[k].x.st + 8 * e;
+        if (h0[k] < h1[k]) load(k, h0[k]);
+    }
+    float c[8], s[8];
+    int pl = lane;
+    if constexpr (ROPE == ROPE_HALF) pl = half_partner(lane, e, p.rot);
+    if constexpr (ROPE != ROPE_NONE) angles<ROPE>(p, t, n, e, pl, c, s);
+
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const QkSide& q = p.side[k];
-        const int skip = k ? p.side[0].heads : 0;
-        const int h0 = max(first - skip, 0), h1 = min(last - skip, q.heads);
-        if (h0 >= h1) continue;
+        if (h0[k] >= h1[k]) continue;
         float wc[8], ws[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) wc[j] = (q.w ? q.w[8 * e + j] : 1.0f) * q.scale;
@@ -153,17 +162,16 @@ __global__ void __launch_bounds__(kThreads) qk_norm_fwd_kernel(QkParams p) {
                 ws[j] *= s[j];
             }
         }
-        const long row = b * q.x.sb + t * q.x.st + 8 * e;
-        for (int h = h0; h < h1; h += kUnroll) {
-            Raw8<BF16> raw[kUnroll];
+        for (int h = h0[k]; h < h1[k]; h += kUnroll) {
+            Raw8<BF16> now[kUnroll];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-                raw[u].load(q.x.p, row + min(h + u, h1 - 1) * q.x.sh);
+            for (int u = 0; u < kUnroll; ++u) now[u] = raw[k][u];
+            if (h + kUnroll < h1[k]) load(k, h + kUnroll);
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                if (h + u >= h1) break;
+                if (h + u >= h1[k]) break;
                 float x[8], y[8];
-                raw[u].get(x);
+                now[u].get(x);
                 float r = 1.0f;
                 if (p.norm) {
                     float sum = 0.0f;
@@ -176,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_fwd_kernel(QkParams p) {
                     for (int j = 0; j < 8; ++j) y[j] = x[j] * wc[j] * r;
                 } else {
                     float xp[8];
-                    if constexpr (ROPE == ROPE_HALF) raw[u].from_lane(pl).get(xp);
+                    if constexpr (ROPE == ROPE_HALF) now[u].from_lane(pl).get(xp);
                     else partners<ROPE>(x, pl, xp);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) y[j] = fmaf(x[j], wc[j], xp[j] * ws[j]) * r;
@@ -228,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(QkParams p) {
         const int n = valid ? static_cast<int>(want) : p.tokens - 1;
         const int b = n / p.T, t = n - b * p.T;
         float c[8], s[8];
-        if constexpr (ROPE != ROPE_NONE) angles<ROPE>(p, b, t, n, e, c, s);
+        if constexpr (ROPE != ROPE_NONE) angles<ROPE>(p, t, n, e, pl, c, s);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const QkSide& q = p.side[k];
@@ -246,14 +254,14 @@ __global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(QkParams p) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int hu = min(h + u, h1 - 1);
-                    raw[u].load(q.x.p, row + hu * q.x.sh);
+                    raw[u].stream(q.x.p, row + hu * q.x.sh);
                     const long o = ((static_cast<long>(b) * p.H + static_cast<long>(hu) * q.rep) * p.T + t) * D + 8 * e;
                     Raw8<false> gr;
-                    gr.load(q.g, o);
+                    gr.stream(q.g, o);
                     gr.get(g[u]);
                     for (int m = 1; m < q.rep; ++m) {
                         float more[8];
-                        gr.load(q.g, o + static_cast<long>(m) * p.T * D);
+                        gr.stream(q.g, o + static_cast<long>(m) * p.T * D);
                         gr.get(more);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) g[u][j] += more[j];
@@ -345,9 +353,9 @@ __global__ void __launch_bounds__(kThreads) out_norm_fwd_kernel(OutParams p) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int hu = min(h + u, h1 - 1);
-            if (valid) o[u].load(p.o, orow + hu * step);
+            if (valid) o[u].stream(p.o, orow + hu * step);
             else o[u].zero();
-            if (p.act && valid) z[u].load(p.z.p, zrow + hu * p.z.sh);
+            if (p.act && valid) z[u].stream(p.z.p, zrow + hu * p.z.sh);
             else z[u].zero();
         }
 #pragma unroll

@@ -610,6 +610,10 @@ int pdn_scan_step(const pdn_scan_step_args* args, void* stream) {
     return call(args, stream, [](auto* a) { return check_scan_step(a); }, pdn::launch_scan_step);
 }
 
+int pdn_scan_marks(int32_t T) {
+    return T < 0 ? PDN_EINVAL : static_cast<int>((static_cast<long>(T) + PDN_SCAN_MARK - 1) / PDN_SCAN_MARK);
+}
+
 int pdn_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, int64_t original_context,
                    double* inv_freq, float* rope_scale) {
     if (!inv_freq || !rope_scale || rot_dim < 2 || rot_dim % 2 != 0) return PDN_EINVAL;

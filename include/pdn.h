@@ -510,7 +510,8 @@ typedef struct pdn_out_norm_bwd_args {
  *   hT                [B,D] fp32 state after the last; NULL = not written;
  *                     may be h0.
  *   marks             NULL, or [B, ceil(T / PDN_SCAN_MARK), D] fp32, written:
- *                     the states before tokens 0, PDN_SCAN_MARK, ..  A
+ *                     (pdn_scan_marks() of them) the states before tokens
+ *                     0, PDN_SCAN_MARK, ..  A
  *                     backward that is given them need not scan forward again.
  *   workspace, workspace_bytes   at least pdn_scan_fwd_workspace_size() bytes
  *                     (0 where one workgroup's span covers T).  It holds
@@ -608,6 +609,10 @@ int pdn_out_norm_bwd(const pdn_out_norm_bwd_args *args, void *stream);
 int pdn_scan_fwd(const pdn_scan_args *args, void *stream);
 int pdn_scan_bwd(const pdn_scan_bwd_args *args, void *stream);
 int pdn_scan_step(const pdn_scan_step_args *args, void *stream);
+
+/* How many states `marks` holds for each sequence of T tokens:
+ * ceil(T / PDN_SCAN_MARK), by the library's own spacing.  T < 0: PDN_EINVAL. */
+int pdn_scan_marks(int32_t T);
 
 /* How inverse frequencies are changed for contexts `factor` times as long as
  * the original one. */

@@ -232,6 +232,8 @@ def test_calls_without_a_gpu_tensor_are_refused():
 
 
 def test_marks():
+    with pytest.raises(pdn.PdnError):
+        pdn.pdn_scan_marks(-1)
     m = pdn.PDN_SCAN_MARK
     assert [pdn.pdn_scan_marks(t) for t in (0, 1, m, m + 1, 10 * m - 1)] == [0, 1, 1, 2, 10]
 
