@@ -154,7 +154,7 @@ int check_decode(const pdn_decode_args* a) {
 // ---- the operators around the recurrence ----
 
 // B * T of the strided operators: their kernels index tokens in 32 bits.
-constexpr long kMaxRows = (1L << 31) - 1;
+constexpr long kMaxRows = 1L << 30;
 
 int elt_bytes(int32_t dtype) { return dtype == PDN_BF16 ? 2 : 4; }
 

@@ -343,7 +343,9 @@ int pdn_chunk_bwd(const pdn_chunk_bwd_args *args, void *stream);
  * only have their last dimension contiguous.  Their strides are given in
  * elements, are >= 0, and keep every row 16-byte aligned; the stride of a
  * dimension of size 1 is not read.  Inputs may overlap or repeat (stride 0);
- * the rows of a strided output must not overlap (PDN_EINVAL).
+ * the rows of a strided output must not overlap each other (PDN_EINVAL).  No
+ * output may overlap an input, another output or the workspace, except where
+ * two arguments may be one buffer.
  * ---------------------------------------------------------------------- */
 
 /* Norm of a head's row x[0..d): r = (c sum x^2 + eps)^(-1/2), with c = 1/d
