@@ -30,6 +30,10 @@
 // device scope: the word is its own flag (all ones = not there yet, which no
 // published word is), so no fence, and no write-back of an L2, is needed.
 //
+// With few columns each has a carrier besides: its first workgroup, which takes
+// the tiles' (A, H) as they come and publishes the states behind them, the same
+// chain of operations in one place.
+//
 // A decay that is zero drops the state before it, infinities and NaN included:
 // every "a h + b" below selects b, and every product of decays 0, where the
 // later factor is zero.
@@ -54,6 +58,14 @@ constexpr int kBwdTile = kBwdWaves * kBwdR;
 // Predecessors looked at together: 2 and 8 measured 1 to 5% slower (rounds, and
 // registers and traffic).
 constexpr int kWindow = 4;
+// Runs that a carrier takes a round (8, 16 and 32 at one column of 512 tiles:
+// 125, 86 and 65 us), and the columns up to which they have carriers.  With few
+// columns many of a column's tiles are in flight, and each would look far back;
+// with many, the carriers' places are worth more.  Forward without and with
+// them, bf16, T = 65536: 1 column 88 and 65 us, 4 columns 90 and 71, 8 columns
+// 110 and 98, 16 columns 177 and 191.
+constexpr int kCarry = 32;
+constexpr int kCarried = 8;
 constexpr u64 kEmpty = ~0ull;
 constexpr unsigned kPolls = 1u << 21;  // loads before a tile gives up: seconds, where thousands are the most that is needed
 
@@ -90,6 +102,7 @@ struct ScanParams {
     int strips;          // kCols-channel strips of a row
     int columns;         // B * strips
     int tiles;           // along T
+    int carrier;         // 1: each column's first workgroup carries its state (see carry)
     Chain chain;
 };
 
@@ -191,7 +204,36 @@ __device__ __forceinline__ void deal(const ScanParams& p, int* slot, int& column
         *slot = static_cast<int>(1u + __hip_atomic_fetch_add(p.chain.counters + static_cast<long>(column) * kCounterStep, 1u,
                                                              __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
     __syncthreads();
-    at = __builtin_amdgcn_readfirstlane(*slot);
+    at = __builtin_amdgcn_readfirstlane(*slot) - p.carrier;  // -1: this workgroup is the carrier
+}
+
+// The carrier's work, a channel to a lane of its first two waves: from the
+// state `h` before the column's first tile, the state behind each tile but the
+// last, as their runs come in, up to kCarry of them a round.  It waits only for
+// tiles that started after it, and every one that has started publishes its run
+// before it waits, so all started tiles come to an end, and the next ones start.
+__device__ void carry(const ScanParams& p, int column, int ch, float h) {
+    const long word = static_cast<long>(column) * p.tiles * kCols + ch;
+    const int n = p.tiles - 1;
+    unsigned polls = kPolls;
+    for (int next = 0; next < n && polls;) {
+        u64 r[kCarry];
+#pragma unroll
+        for (int k = 0; k < kCarry; ++k) r[k] = peek(p.chain.agg + word + static_cast<long>(min(next + k, n - 1)) * kCols);
+        int done = 0;
+#pragma unroll
+        for (int k = 0; k < kCarry; ++k)
+            if (done == k && next + k < n && __all(r[k] != kEmpty)) {
+                h = apply(word_A(r[k]), h, word_H(r[k]));
+                publish(p.chain.inc + word + static_cast<long>(next + k) * kCols, pair_word(0.0f, h));
+                done = k + 1;
+            }
+        next += done;
+        if (!done) {
+            --polls;
+            __builtin_amdgcn_s_sleep(1);
+        }
+    }
 }
 
 __device__ __forceinline__ float decay(float la) { return __builtin_amdgcn_exp2f(la * kLog2e); }
@@ -264,7 +306,7 @@ __device__ __forceinline__ float meet(const ScanParams& p, const float (&totA)[W
     const long mine = word + static_cast<long>(at) * kCols;
     const bool last = at + 1 == p.tiles;
     Window inc_words;
-    if (at > 0) inc_words.load(p.chain.inc + word, at - 1);
+    if (at > 0 && !p.carrier) inc_words.load(p.chain.inc + word, at - 1);
     float tA = totA[0][ch], tH = totH[0][ch];
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) {
@@ -272,12 +314,20 @@ __device__ __forceinline__ float meet(const ScanParams& p, const float (&totA)[W
         tA = join(tA, totA[w][ch]);
     }
     float h = start;
-    if (at > 0) {
+    if (p.carrier) {
+        if (!last) publish(p.chain.agg + mine, pair_word(tA, tH));
+        if (at > 0) {
+            unsigned polls = kPolls;
+            const u64* from = p.chain.inc + mine - kCols;
+            const u64 w = settled(from, peek(from), polls);
+            h = polls ? word_H(w) : __uint_as_float(0x7fc00000u);
+        }
+    } else if (at > 0) {
         if (!last) publish(p.chain.agg + mine, pair_word(tA, tH));
         h = look_back(p.chain.agg + word, p.chain.inc + word, inc_words, at);
     }
     behind = apply(tA, h, tH);
-    if (!last) publish(p.chain.inc + mine, pair_word(0.0f, behind));
+    if (!last && !p.carrier) publish(p.chain.inc + mine, pair_word(0.0f, behind));
     return h;
 }
 
@@ -291,6 +341,11 @@ __global__ void __launch_bounds__(64 * kFwdWaves) scan_fwd_kernel(ScanParams p) 
     int column, at;
     deal(p, &slot, column, at);
     const int b = column / p.strips, c0 = (column - b * p.strips) * kCols;
+    if (at < 0) {
+        const int ch = c0 + tid;
+        if (wave < 2) carry(p, column, tid, p.h0 && ch < p.D ? p.h0[static_cast<long>(b) * p.D + ch] : 0.0f);
+        return;
+    }
     const int c2 = 2 * lane, c = c0 + c2;
     const int cc = c < p.D ? c : 0;  // lanes past the last channel read another's
     const int t0 = at * kFwdTile + wave * R;
@@ -378,6 +433,11 @@ __global__ void __launch_bounds__(64 * kBwdWaves, 4) scan_bwd_kernel(ScanParams 
     deal(p, &slot, column, at);
     const int tile = p.tiles - 1 - at;
     const int b = column / p.strips, c0 = (column - b * p.strips) * kCols;
+    if (at < 0) {
+        const int ch = c0 + tid;
+        if (wave < 2) carry(p, column, tid, p.dhT && ch < p.D ? p.dhT[static_cast<long>(b) * p.D + ch] : 0.0f);
+        return;
+    }
     const int c2 = 2 * lane, c = c0 + c2;
     const int cc = c < p.D ? c : 0;
     const int t0 = tile * kBwdTile + wave * R;
@@ -541,6 +601,7 @@ ScanParams params(const pdn_scan_args& a) {
 }
 
 void set_chain(ScanParams& p, char* at) {
+    p.carrier = p.columns <= kCarried;
     p.chain.counters = reinterpret_cast<unsigned*>(at);
     p.chain.agg = reinterpret_cast<u64*>(at + sizeof(unsigned) * kCounterStep * p.columns);
     p.chain.inc = p.chain.agg + static_cast<long>(p.columns) * p.tiles * kCols;
@@ -563,7 +624,7 @@ void launch_tiles(const ScanParams& p, int kind, dim3 grid, hipStream_t st) {
 
 // kind: 0 forward, 1 forward for the marks alone, 2 backward
 hipError_t launch_kind(const ScanParams& p, const pdn_scan_args& a, int kind, hipStream_t st) {
-    const dim3 grid(static_cast<unsigned>(static_cast<long>(p.columns) * p.tiles));
+    const dim3 grid(static_cast<unsigned>(static_cast<long>(p.columns) * (p.tiles + p.carrier)));
     const bool xb = a.dtype == PDN_BF16, lb = a.log_dtype == PDN_BF16;
 #define PDN_GAINS(X, L)                                                              \
     switch (a.gain) {                                                                \

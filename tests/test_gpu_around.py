@@ -304,6 +304,8 @@ SCAN = [  # B, T, D, type, type of log_a, gain, h0 / dhT, resets
     (5, 515, 64, "bf16", "fp32", 1, False, False),
     (1, 20011, 64, "bf16", "bf16", 2, True, False),
     (2, 9000, 24, "fp32", "fp32", 0, True, True),
+    (3, 700, 520, "bf16", "fp32", 1, True, True),      # more columns than have carriers
+    (9, 3001, 72, "fp32", "fp32", 2, True, False),
 ]
 
 
