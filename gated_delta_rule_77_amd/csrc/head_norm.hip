@@ -15,7 +15,7 @@
 // 8 pairs at most), and the rotation folds into two factors per element,
 //   out_i = r (x_i wc_i + x_partner(i) ws_i).
 // Heads go four at a time, loads first.
-#include "kernels.h"
+#include "layer.h"
 #include "rows.h"
 
 namespace pdn {

@@ -53,22 +53,4 @@ size_t chunk_fwd_workspace_bytes(const pdn_chunk_fwd_args& a);
 size_t chunk_bwd_workspace_bytes(const pdn_chunk_bwd_args& a);
 hipError_t launch_chunk_bwd(const pdn_chunk_bwd_args& a, hipStream_t stream);
 
-// Norm and rotation of q and k into the recurrence's layout, and the gated
-// norm of its output, with their gradients (head_norm.hip).
-hipError_t launch_qk_norm(const pdn_qk_norm_args& a, hipStream_t stream);
-size_t qk_norm_bwd_workspace_bytes(const pdn_qk_norm_bwd_args& a);
-hipError_t launch_qk_norm_bwd(const pdn_qk_norm_bwd_args& a, hipStream_t stream);
-hipError_t launch_out_norm(const pdn_out_norm_args& a, hipStream_t stream);
-size_t out_norm_bwd_workspace_bytes(const pdn_out_norm_bwd_args& a);
-hipError_t launch_out_norm_bwd(const pdn_out_norm_bwd_args& a, hipStream_t stream);
-
-// The recurrence with a vector state (scan.hip).  scan_blocks: the most
-// workgroups that a call of these sizes launches.
-long scan_blocks(const pdn_scan_args& a);
-size_t scan_fwd_workspace_bytes(const pdn_scan_args& a);
-size_t scan_bwd_workspace_bytes(const pdn_scan_bwd_args& a);
-hipError_t launch_scan_fwd(const pdn_scan_args& a, hipStream_t stream);
-hipError_t launch_scan_bwd(const pdn_scan_bwd_args& a, hipStream_t stream);
-hipError_t launch_scan_step(const pdn_scan_step_args& a, hipStream_t stream);
-
 }  // namespace pdn

@@ -1,4 +1,5 @@
-// Host layer of libpdn.so: the extern "C" entry points declared in pdn.h.
+// Host layer of libpdn.so: the extern "C" entry points declared in pdn.h and
+// pdn_layer.h.
 // Every entry point validates its arguments before touching the GPU, maps
 // HIP errors to PDN_EHIP, and lets no exception escape.
 #include <hip/hip_runtime.h>
@@ -9,6 +10,7 @@
 #include <mutex>
 
 #include "kernels.h"
+#include "layer.h"
 #include "pdn.h"
 
 namespace {
@@ -566,6 +568,8 @@ int pdn_decode_step(const pdn_decode_args* args, void* stream) {
         return PDN_EHIP;
     }
 }
+
+int pdn_layer_version(void) { return PDN_LAYER_VERSION; }
 
 int pdn_qk_norm_check(const pdn_qk_norm_args* args) { return answer([&] { return check_qk_norm(args); }); }
 int pdn_qk_norm_bwd_check(const pdn_qk_norm_bwd_args* args) { return answer([&] { return check_qk_norm_bwd(args); }); }

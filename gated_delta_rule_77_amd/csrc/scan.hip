@@ -37,7 +37,7 @@
 // A decay that is zero drops the state before it, infinities and NaN included:
 // every "a h + b" below selects b, and every product of decays 0, where the
 // later factor is zero.
-#include "kernels.h"
+#include "layer.h"
 #include "rows.h"
 
 namespace pdn {

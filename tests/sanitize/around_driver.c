@@ -9,7 +9,7 @@
 #include <stdio.h>
 #include <string.h>
 
-#include "pdn.h"
+#include "pdn_layer.h"
 
 #define FAKE ((void *)(uintptr_t)0x10000)
 

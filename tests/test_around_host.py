@@ -4,6 +4,7 @@ and the references' own consistency."""
 import ctypes
 import math
 import os
+import re
 import subprocess
 
 import numpy as np
@@ -30,12 +31,20 @@ STRUCTS = {"pdn_qk_norm_args": pdn.QkNormArgs, "pdn_qk_norm_bwd_args": pdn.QkNor
            "pdn_scan_step_args": pdn.ScanStepArgs}
 
 
+def test_exports_every_declared_symbol(lib):
+    src = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "pdn_layer.h")).read(), flags=re.S)
+    names = set(re.findall(r"\b(pdn_[a-z_0-9]+)\s*\(", src))
+    assert names == set(pdn.EXPORTED_LAYER)
+    out = subprocess.run(["nm", "-D", "--defined-only", pdn.LIB_PATH], capture_output=True, text=True, check=True).stdout
+    assert names <= set(re.findall(r"\bT (pdn_[a-z_0-9]+)", out))
+
+
 def test_struct_layouts_match_the_header(tmp_path):
-    lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "pdn.h"', "int main(void){"]
+    lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "pdn_layer.h"', "int main(void){"]
     for c, m in STRUCTS.items():
         lines.append('printf("%s %%zu\\n", sizeof(%s));' % (c, c))
         lines += ['printf("%s.%s %%zu\\n", offsetof(%s, %s));' % (c, f, c, f) for f, _ in m._fields_]
-    lines += ['printf("mark %d\\n", PDN_SCAN_MARK);', "return 0;}"]
+    lines += ['printf("mark %d\\nversion %d\\n", PDN_SCAN_MARK, PDN_LAYER_VERSION);', "return 0;}"]
     (tmp_path / "l.c").write_text("\n".join(lines))
     subprocess.check_call(["gcc", "-std=c99", "-I", os.path.join(ROOT, "include"), str(tmp_path / "l.c"), "-o", str(tmp_path / "l")])
     got = dict(l.split() for l in subprocess.check_output([str(tmp_path / "l")], text=True).splitlines())
@@ -44,6 +53,21 @@ def test_struct_layouts_match_the_header(tmp_path):
         for f, _ in m._fields_:
             assert int(got[c + "." + f]) == getattr(m, f).offset, (c, f)
     assert int(got["mark"]) == pdn.PDN_SCAN_MARK
+    assert int(got["version"]) == pdn.PDN_LAYER_VERSION == pdn.load_library().pdn_layer_version()
+
+
+def test_binding_refuses_a_library_of_another_layer_version(tmp_path):
+    for layer in ("", "int pdn_layer_version(void) { return %d; }" % (pdn.PDN_LAYER_VERSION + 1)):
+        stub = tmp_path / "stub.c"
+        stub.write_text("\n".join(
+            ["int pdn_abi_version(void) { return %d; }" % pdn.PDN_ABI_VERSION,
+             "const char *pdn_strerror(int c) { (void)c; return \"stub\"; }", layer] +
+            ["int %s(void *a, void *b) { (void)a; (void)b; return -1; }" % n
+             for n in pdn.EXPORTED if n not in ("pdn_abi_version", "pdn_strerror")]))
+        so = tmp_path / ("libstub%d.so" % len(layer))
+        subprocess.check_call(["gcc", "-shared", "-fPIC", str(stub), "-o", str(so)])
+        with pytest.raises(RuntimeError, match="pdn_layer.h"):
+            pdn.load_library(str(so))
 
 
 def _qk():
