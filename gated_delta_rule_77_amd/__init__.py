@@ -657,7 +657,7 @@ class _Call:
 
     def size(self, name):
         n = ctypes.c_size_t(0)
-        rc = getattr(load_library(), name)(ctypes.byref(self.a), ctypes.byref(n))
+        rc = getattr(_lib or load_library(), name)(ctypes.byref(self.a), ctypes.byref(n))
         if rc != PDN_OK:
             raise PdnError(rc, name)
         return n.value
@@ -671,6 +671,7 @@ class _Call:
             with _torch.cuda.device(self.index):
                 return self.launch(name, stream, workspace)
         a, size = self.a, _AROUND[name][2]
+        lib = _lib or load_library()
         if size:
             if workspace is None:
                 n = self.size(size)
@@ -688,7 +689,7 @@ class _Call:
             stream = _torch._C._cuda_getCurrentRawStream(self.index)
         elif not isinstance(stream, int):
             stream = stream.cuda_stream
-        rc = getattr(load_library(), name)(ctypes.byref(a), stream)
+        rc = getattr(lib, name)(ctypes.byref(a), stream)
         if rc != PDN_OK:
             raise PdnError(rc, name)
 

@@ -34,6 +34,17 @@
 // the tiles' (A, H) as they come and publishes the states behind them, the same
 // chain of operations in one place.
 //
+// Measured on an MI355X, whose large copies reach 5.3 TB/s (counters: 1.03 to
+// 1.06 times the bytes that the call cannot do without, the published words
+// among them), with the reset of the words (6 us) before it:
+//   forward   B4 T8192 D2048, bf16, fp32 decays       98 us   5.5 TB/s
+//             B1 T65536 D2048, bf16                  176 us   4.6 TB/s
+//             B2 T8192 D4096, bf16, normed gain       84 us   4.8 TB/s
+//   backward  of the last, kept states given         140 us   4.8 TB/s
+// A tile lives for 8 to 11 us, of which it loads for 3 to 4, waits for its state
+// for 2 to 5 and stores for 2; two workgroups to a compute unit cover most of
+// that, and what is left is the first round's fill and the last one's drain.
+//
 // A decay that is zero drops the state before it, infinities and NaN included:
 // every "a h + b" below selects b, and every product of decays 0, where the
 // later factor is zero.
