@@ -596,8 +596,11 @@ _CODES = {}     # mostly host time, and an import statement in each of its funct
 
 
 def _use_torch():
-    global _torch
+    global _torch, _current_stream
     import torch
+    # the stream's handle without an object around it (3 us less), where torch has that
+    _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
     _CODES.update({torch.float32: PDN_F32, torch.bfloat16: PDN_BF16})
     _torch = torch
 
@@ -686,7 +689,7 @@ class _Call:
             if workspace is not None:
                 a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
         if stream is None:
-            stream = _torch._C._cuda_getCurrentRawStream(self.index)
+            stream = _current_stream(self.index)
         elif not isinstance(stream, int):
             stream = stream.cuda_stream
         rc = getattr(lib, name)(ctypes.byref(a), stream)

@@ -233,8 +233,8 @@ __device__ __forceinline__ void sum_slots(const float (&acc)[8], float* red, flo
 
 // A workgroup takes token groups in strides of the grid, so that a lane's
 // weight gradients add up in registers over all its tokens and heads; one
-// partial sum per workgroup goes to the workspace (kFill of them: the kernel
-// that adds them up takes 6 us).  Its loads stay behind the angles: ahead of
+// partial sum per workgroup goes to the workspace (kBwdFill of them: the kernel
+// that adds them up takes 5 us).  Its loads stay behind the angles: ahead of
 // them they cost the registers of a fourth wave (205 -> 212 us).
 template <bool BF16, int D, int ROPE>
 __global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(QkParams p) {
@@ -520,8 +520,10 @@ int heads_per_block(long groups, int heads) {
     return static_cast<int>((heads + parts - 1) / parts);
 }
 
-// Grid of a backward: at most kFill workgroups, each with a partial sum of the
-// weight gradients.
+// Grid of a backward: at most four workgroups to a compute unit (what its
+// registers allow), each with a partial sum of the weight gradients; twice as
+// many measured 1% slower, most of it the partial sums'.
+constexpr long kBwdFill = 1024;
 struct BwdGrid {
     int x, y, per;
 };
@@ -530,7 +532,7 @@ BwdGrid bwd_grid(long tokens, int slots, int heads) {
     BwdGrid g;
     g.per = heads_per_block(groups, heads);
     g.y = (heads + g.per - 1) / g.per;
-    const long cap = kFill / g.y;
+    const long cap = kBwdFill / g.y;
     g.x = static_cast<int>(groups < cap ? groups : cap < 1 ? 1 : cap);
     return g;
 }

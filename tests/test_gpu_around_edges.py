@@ -192,3 +192,112 @@ def test_positions_in_any_order():
     for t in (q, k):
         sel = np.broadcast_to(small[:, None, :], (B, H, T))
         _close("q/k at any position", t[torch_mod().from_numpy(sel.copy()).to("cuda")], want[sel], bound[sel])
+
+
+@pytest.mark.parametrize("which", ["q", "k"])
+def test_weights_on_one_side(which):
+    pdn = _pdn()
+    B, T, H, d = 2, 40, 3, 64
+    rng = np.random.default_rng(307)
+    x = {n: _draw(rng, (B, T, H, d), "fp32") for n in "qk"}
+    g = {n: rng.standard_normal((B, H, T, d)).astype(np.float32) for n in "qk"}
+    w = (1 + 0.2 * rng.standard_normal(d)).astype(np.float32)
+    out = {n: _nan((B, H, T, d)) for n in "qk"}
+    kw = {"w" + which: _up(w), "norm": 1}
+    pdn.pdn_qk_norm_fwd(_up(x["q"]), _up(x["k"]), out["q"], out["k"], **kw)
+    dx, dw = {n: _nan((B, T, H, d)) for n in "qk"}, _nan((d,))
+    pdn.pdn_qk_norm_bwd(_up(x["q"]), _up(x["k"]), _up(g["q"]), _up(g["k"]), dx["q"], dx["k"], **{"dw" + which: dw}, **kw)
+    eps = float(np.float32(1e-6))
+    for n in "qk":
+        wn = f64(w) if n == which else None
+        want, bound = ref.qk_one(f64(x[n]), wn, 1.0, H, 1, eps, None)
+        _close("one side " + n, out[n], want, bound)
+        want, bound, dww, dwb = ref.qk_one_bwd(f64(x[n]), wn, 1.0, f64(g[n]), 1, eps, None)
+        _close("one side dx" + n, dx[n], want, bound)
+        if n == which:
+            _close("one side dw" + n, dw, dww, dwb)
+
+
+def test_heads_before_tokens():
+    """Strided tensors in the other order: [B,H,T,d] memory seen as [B,T,H,d]."""
+    pdn = _pdn()
+    torch = torch_mod()
+    B, T, H, d = 2, 37, 3, 128
+    gen = torch.Generator(device="cuda").manual_seed(308)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    x, z, o, g = rnd(B, H, T, d), rnd(B, H, T, d), rnd(B, H, T, d), rnd(B, H, T, d)
+    got, want = [], []
+    for order, out in ((lambda t: t.transpose(1, 2), got), (lambda t: t.transpose(1, 2).contiguous(), want)):
+        new = lambda: _nan((B, H, T, d)).transpose(1, 2) if order(x).stride(1) == d else _nan((B, T, H, d))
+        q, k, y, dx, dz, dg, do = _nan((B, H, T, d)), _nan((B, H, T, d)), new(), new(), new(), new(), _nan((B, H, T, d))
+        pdn.pdn_qk_norm_fwd(order(x), order(z), q, k)
+        pdn.pdn_out_norm_fwd(o, y, z=order(z))
+        pdn.pdn_qk_norm_bwd(order(x), order(z), g, g, dx, dz)
+        pdn.pdn_out_norm_bwd(o, order(x), do, z=order(z), dz=dg)
+        out += [q, k, y, dx, dz, dg, do]
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_captured_with_workspaces_made_inside():
+    pdn = _pdn()
+    torch = torch_mod()
+    x, la, h0, dh, dhT = _scan_case((2, 1100, 1160, "bf16", "bf16", 0, True, True), 309)
+    ins = [_up(x, "bf16"), _up(la, "bf16"), _up(dh, "bf16")]
+    outs = [torch.zeros_like(ins[0]) for _ in range(3)]
+
+    def run():
+        pdn.pdn_scan_fwd(ins[0], ins[1], outs[0])
+        pdn.pdn_scan_bwd(ins[0], ins[1], ins[2], outs[1], outs[2])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in outs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(3):
+        for t in outs:
+            t.zero_()
+        junk = torch.full((1 << 22,), 5.0, device="cuda")
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b)
+        del junk
+
+
+def test_calls_from_two_threads():
+    import threading
+    pdn = _pdn()
+    torch = torch_mod()
+    cases = [_scan_case((2, 1500, 264, "fp32", "fp32", 1, True, False), s) for s in (310, 311)]
+    ins = [(_up(x), _up(la), _up(h0)) for x, la, h0, _, _ in cases]
+    want = []
+    for x, la, h0 in ins:
+        want.append(torch.empty_like(x))
+        pdn.pdn_scan_fwd(x, la, want[-1], h0=h0, gain=1)
+    torch.cuda.synchronize()
+    got = [[] for _ in ins]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                h = torch.zeros_like(ins[i][0])
+                pdn.pdn_scan_fwd(ins[i][0], ins[i][1], h, h0=ins[i][2], gain=1)
+                got[i].append(h)
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert len(got[i]) == 20 and all(torch.equal(h, want[i]) for h in got[i])
