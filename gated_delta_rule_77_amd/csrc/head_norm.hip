@@ -233,9 +233,11 @@ __device__ __forceinline__ void sum_slots(const float (&acc)[8], float* red, flo
 
 // A workgroup takes token groups in strides of the grid, so that a lane's
 // weight gradients add up in registers over all its tokens and heads; one
-// partial sum per workgroup goes to the workspace (kBwdFill of them: the kernel
-// that adds them up takes 5 us).  Its loads stay behind the angles: ahead of
-// them they cost the registers of a fourth wave (205 -> 212 us).
+// partial sum per workgroup goes to the workspace (at most kBwdFill of them: the
+// kernel that adds them up takes 6 us).  Its loads stay behind the angles: ahead of
+// them they cost the registers of a fourth wave (205 -> 212 us).  They go through
+// the caches, where a recurrence's backward has just left some of what they read:
+// the same at B2 T8192 H32, 32 us instead of 40 for 6725 tokens of 12 fp32 heads.
 template <bool BF16, int D, int ROPE>
 __global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(QkParams p) {
     constexpr int LPR = D / 8, SLOTS = kThreads / LPR;
@@ -272,14 +274,14 @@ __global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(QkParams p) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int hu = min(h + u, h1 - 1);
-                    raw[u].stream(q.x.p, row + hu * q.x.sh);
+                    raw[u].load(q.x.p, row + hu * q.x.sh);
                     const long o = ((static_cast<long>(b) * p.H + static_cast<long>(hu) * q.rep) * p.T + t) * D + 8 * e;
                     Raw8<false> gr;
-                    gr.stream(q.g, o);
+                    gr.load(q.g, o);
                     gr.get(g[u]);
                     for (int m = 1; m < q.rep; ++m) {
                         float more[8];
-                        gr.stream(q.g, o + static_cast<long>(m) * p.T * D);
+                        gr.load(q.g, o + static_cast<long>(m) * p.T * D);
                         gr.get(more);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) g[u][j] += more[j];
@@ -520,20 +522,22 @@ int heads_per_block(long groups, int heads) {
     return static_cast<int>((heads + parts - 1) / parts);
 }
 
-// Grid of a backward: at most four workgroups to a compute unit (what its
-// registers allow), each with a partial sum of the weight gradients; twice as
-// many measured 1% slower, most of it the partial sums'.
-constexpr long kBwdFill = 1024;
+// Grid of a backward.  With weight gradients each workgroup leaves a partial sum
+// of them, and takes several token groups so that those stay few, the groups
+// dealt evenly.  1024, 2048 and 4096 workgroups at B2 T8192 H32: 229, 223 and
+// 222 us with the sum of the partial ones.
+constexpr long kBwdFill = 2048;
 struct BwdGrid {
     int x, y, per;
 };
-BwdGrid bwd_grid(long tokens, int slots, int heads) {
+BwdGrid bwd_grid(long tokens, int slots, int heads, bool weights) {
     const long groups = (tokens + slots - 1) / slots;
     BwdGrid g;
     g.per = heads_per_block(groups, heads);
     g.y = (heads + g.per - 1) / g.per;
-    const long cap = kBwdFill / g.y;
-    g.x = static_cast<int>(groups < cap ? groups : cap < 1 ? 1 : cap);
+    const long cap = kBwdFill / g.y > 0 ? kBwdFill / g.y : 1;
+    const long each = weights && groups > cap ? (groups + cap - 1) / cap : 1;
+    g.x = static_cast<int>((groups + each - 1) / each);
     return g;
 }
 
@@ -649,7 +653,7 @@ hipError_t launch_qk_norm(const pdn_qk_norm_args& a, hipStream_t st) {
 
 size_t qk_norm_bwd_workspace_bytes(const pdn_qk_norm_bwd_args& a) {
     if (!a.dwq && !a.dwk) return 0;
-    const BwdGrid g = bwd_grid(static_cast<long>(a.fwd.B) * a.fwd.T, kThreads / (a.fwd.d / 8), a.fwd.Hq + a.fwd.Hk);
+    const BwdGrid g = bwd_grid(static_cast<long>(a.fwd.B) * a.fwd.T, kThreads / (a.fwd.d / 8), a.fwd.Hq + a.fwd.Hk, true);
     return sizeof(float) * 2 * a.fwd.d * static_cast<size_t>(g.x) * g.y;
 }
 
@@ -665,7 +669,7 @@ hipError_t launch_qk_norm_bwd(const pdn_qk_norm_bwd_args& a, hipStream_t st) {
         p.side[0].dx = StridedOut{a.dxq, a.dxq_sb, a.dxq_st, a.dxq_sh};
         p.side[1].dx = StridedOut{a.dxk, a.dxk_sb, a.dxk_st, a.dxk_sh};
         p.partial = partial;
-        const BwdGrid g = bwd_grid(p.tokens, kThreads / (f.d / 8), f.Hq + f.Hk);
+        const BwdGrid g = bwd_grid(p.tokens, kThreads / (f.d / 8), f.Hq + f.Hk, weights);
         p.heads_per_block = g.per;
         blocks = g.x * g.y;
         const hipError_t e = qk_dispatch(p, f, true, dim3(g.x, g.y), st);
@@ -687,7 +691,7 @@ hipError_t launch_out_norm(const pdn_out_norm_args& a, hipStream_t st) {
 
 size_t out_norm_bwd_workspace_bytes(const pdn_out_norm_bwd_args& a) {
     if (!a.dw) return 0;
-    const BwdGrid g = bwd_grid(static_cast<long>(a.fwd.B) * a.fwd.T, kThreads / out_lanes(a.fwd.dv), a.fwd.H);
+    const BwdGrid g = bwd_grid(static_cast<long>(a.fwd.B) * a.fwd.T, kThreads / out_lanes(a.fwd.dv), a.fwd.H, true);
     return sizeof(float) * a.fwd.dv * static_cast<size_t>(g.x) * g.y;
 }
 
@@ -701,7 +705,7 @@ hipError_t launch_out_norm_bwd(const pdn_out_norm_bwd_args& a, hipStream_t st) {
         p.d_o = a.d_o;
         p.dz = StridedOut{a.dz, a.dz_sb, a.dz_st, a.dz_sh};
         p.partial = partial;
-        const BwdGrid g = bwd_grid(p.tokens, kThreads / out_lanes(f.dv), f.H);
+        const BwdGrid g = bwd_grid(p.tokens, kThreads / out_lanes(f.dv), f.H, a.dw != nullptr);
         p.heads_per_block = g.per;
         blocks = g.x * g.y;
         const hipError_t e = out_dispatch(p, f, true, dim3(g.x, g.y), st);
