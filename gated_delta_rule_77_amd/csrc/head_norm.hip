@@ -19,7 +19,7 @@
 // kernel moves within 3% of the bytes it cannot do without):
 //   q/k norm      B4 T8192 H16 d128 bf16, no rotation      82 us   6.5 TB/s (*)
 //                 B1 T65536 Hq16 Hk4 H16, half rotated    165 us   5.3 TB/s
-//   its backward  B2 T8192 H32, all rotated, weights      205 us   5.2 TB/s
+//   its backward  B2 T8192 H32, all rotated, weights      206 us   5.2 TB/s
 //   output norm   B4 T8192 H16 dv128, fp32 o, bf16 z, y   100 us   5.4 TB/s
 //   its backward  B2 T8192 H32                            186 us   5.1 TB/s
 // (*) over the copy's rate: part of the 268 MB written stays in the 256 MB
@@ -527,13 +527,21 @@ int heads_per_block(long groups, int heads) {
 // dealt evenly.  1024, 2048 and 4096 workgroups at B2 T8192 H32: 229, 223 and
 // 222 us with the sum of the partial ones.
 constexpr long kBwdFill = 2048;
+// Heads that a workgroup of the q/k norm's backward takes at most: its streams
+// are many (x, its gradient, the heads' gradients), and 8 heads' stay closer
+// together than 32's: 215 against 228 us there, 4 heads 221.  The output norm's
+// backward does not care.
+constexpr int kQkBwdHeads = 8;
 struct BwdGrid {
     int x, y, per;
 };
-BwdGrid bwd_grid(long tokens, int slots, int heads, bool weights) {
+BwdGrid bwd_grid(long tokens, int slots, int heads, int most, bool weights) {
     const long groups = (tokens + slots - 1) / slots;
     BwdGrid g;
     g.per = heads_per_block(groups, heads);
+    // (but never over kBwdFill parts, whatever the heads)
+    const int least = static_cast<int>((heads + kBwdFill - 1) / kBwdFill);
+    if (g.per > most) g.per = most > least ? most : least;
     g.y = (heads + g.per - 1) / g.per;
     const long cap = kBwdFill / g.y > 0 ? kBwdFill / g.y : 1;
     const long each = weights && groups > cap ? (groups + cap - 1) / cap : 1;
@@ -653,7 +661,7 @@ hipError_t launch_qk_norm(const pdn_qk_norm_args& a, hipStream_t st) {
 
 size_t qk_norm_bwd_workspace_bytes(const pdn_qk_norm_bwd_args& a) {
     if (!a.dwq && !a.dwk) return 0;
-    const BwdGrid g = bwd_grid(static_cast<long>(a.fwd.B) * a.fwd.T, kThreads / (a.fwd.d / 8), a.fwd.Hq + a.fwd.Hk, true);
+    const BwdGrid g = bwd_grid(static_cast<long>(a.fwd.B) * a.fwd.T, kThreads / (a.fwd.d / 8), a.fwd.Hq + a.fwd.Hk, kQkBwdHeads, true);
     return sizeof(float) * 2 * a.fwd.d * static_cast<size_t>(g.x) * g.y;
 }
 
@@ -669,7 +677,7 @@ hipError_t launch_qk_norm_bwd(const pdn_qk_norm_bwd_args& a, hipStream_t st) {
         p.side[0].dx = StridedOut{a.dxq, a.dxq_sb, a.dxq_st, a.dxq_sh};
         p.side[1].dx = StridedOut{a.dxk, a.dxk_sb, a.dxk_st, a.dxk_sh};
         p.partial = partial;
-        const BwdGrid g = bwd_grid(p.tokens, kThreads / (f.d / 8), f.Hq + f.Hk, weights);
+        const BwdGrid g = bwd_grid(p.tokens, kThreads / (f.d / 8), f.Hq + f.Hk, kQkBwdHeads, weights);
         p.heads_per_block = g.per;
         blocks = g.x * g.y;
         const hipError_t e = qk_dispatch(p, f, true, dim3(g.x, g.y), st);
@@ -691,7 +699,7 @@ hipError_t launch_out_norm(const pdn_out_norm_args& a, hipStream_t st) {
 
 size_t out_norm_bwd_workspace_bytes(const pdn_out_norm_bwd_args& a) {
     if (!a.dw) return 0;
-    const BwdGrid g = bwd_grid(static_cast<long>(a.fwd.B) * a.fwd.T, kThreads / out_lanes(a.fwd.dv), a.fwd.H, true);
+    const BwdGrid g = bwd_grid(static_cast<long>(a.fwd.B) * a.fwd.T, kThreads / out_lanes(a.fwd.dv), a.fwd.H, a.fwd.H, true);
     return sizeof(float) * a.fwd.dv * static_cast<size_t>(g.x) * g.y;
 }
 
@@ -705,7 +713,7 @@ hipError_t launch_out_norm_bwd(const pdn_out_norm_bwd_args& a, hipStream_t st) {
         p.d_o = a.d_o;
         p.dz = StridedOut{a.dz, a.dz_sb, a.dz_st, a.dz_sh};
         p.partial = partial;
-        const BwdGrid g = bwd_grid(p.tokens, kThreads / out_lanes(f.dv), f.H, a.dw != nullptr);
+        const BwdGrid g = bwd_grid(p.tokens, kThreads / out_lanes(f.dv), f.H, f.H, a.dw != nullptr);
         p.heads_per_block = g.per;
         blocks = g.x * g.y;
         const hipError_t e = out_dispatch(p, f, true, dim3(g.x, g.y), st);

@@ -120,9 +120,10 @@ def test_repeated_gradients():
     assert torch.equal(a, b)
 
 
-def test_very_many_heads():
+@pytest.mark.parametrize("T,H", [(3, 4096), (1, 70000)])
+def test_very_many_heads(T, H):
     pdn = _pdn()
-    B, T, H, d = 1, 3, 4096, 64
+    B, d = 1, 64
     rng = np.random.default_rng(304)
     x = _draw(rng, (B, T, H, d), "bf16")
     q, k = _nan((B, H, T, d), "bf16"), _nan((B, H, T, d), "bf16")
