@@ -679,7 +679,10 @@ class _Call:
             if workspace is None:
                 n = self.size(size)
                 if n and stream is not None:
-                    own = _torch.cuda.ExternalStream(stream, device=self.index) if isinstance(stream, int) else stream
+                    own = stream
+                    if isinstance(stream, int):   # a handle; 0 is the default stream's
+                        own = (_torch.cuda.ExternalStream(stream, device=self.index) if stream
+                               else _torch.cuda.default_stream(self.index))
                     with _torch.cuda.stream(own):
                         workspace = _torch.empty(n, dtype=_torch.uint8, device="cuda")
                 elif n:

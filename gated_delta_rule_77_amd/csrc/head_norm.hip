@@ -128,7 +128,7 @@ __device__ __forceinline__ void partners(const float (&x)[8], int lane, float (&
 
 // A workgroup takes SLOTS tokens and (unless tokens are few) all their heads:
 // splitting the heads costs the angles once more for each part (B1 T65536,
-// half rotated: 186, 227 and 299 us in 2, 4 and 8 parts).  The next heads' loads
+// half rotated: 227 and 299 us in 4 and 8 parts, where one took 199).  The next heads' loads
 // are issued ahead of the present ones' arithmetic, the first ones' ahead of the
 // angles.
 template <bool BF16, int D, int ROPE>

@@ -542,7 +542,7 @@ def test_another_stream_and_its_workspace():
     pdn.pdn_scan_bwd(xd, lad, dhd, want[1], want[2], h0=h0d, gain=2)
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
-    for stream in (side, side.cuda_stream):
+    for stream in (side, side.cuda_stream, 0, torch.cuda.default_stream()):
         got = [torch.zeros_like(t) for t in want]
         side.wait_stream(torch.cuda.current_stream())
         pdn.pdn_scan_fwd(xd, lad, got[0], h0=h0d, gain=2, stream=stream)
