@@ -649,6 +649,16 @@ OutParams out_params(const pdn_out_norm_args& a) {
 
 }  // namespace
 
+bool qk_norm_fits(const pdn_qk_norm_args& a) {
+    const int slots = kThreads / (a.d / 8);
+    return (static_cast<long>(a.B) * a.T + slots - 1) / slots <= kMaxGridThreads / kThreads;
+}
+
+bool out_norm_fits(const pdn_out_norm_args& a) {
+    const int slots = kThreads / out_lanes(a.dv);
+    return (static_cast<long>(a.B) * a.T + slots - 1) / slots <= kMaxGridThreads / kThreads;
+}
+
 hipError_t launch_qk_norm(const pdn_qk_norm_args& a, hipStream_t st) {
     if (a.T == 0) return hipSuccess;
     QkParams p = qk_params(a);

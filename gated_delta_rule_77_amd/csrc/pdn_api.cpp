@@ -229,7 +229,7 @@ int check_qk_norm(const pdn_qk_norm_args* a, bool backward = false) {
     if (a->norm != PDN_NORM_NONE && a->norm != PDN_NORM_RMS && a->norm != PDN_NORM_L2) return PDN_EINVAL;
     if (a->norm != PDN_NORM_NONE ? !valid_eps(a->eps) : (a->wq || a->wk)) return PDN_EINVAL;
     if (!std::isfinite(a->q_scale) || !std::isfinite(a->k_scale)) return PDN_EINVAL;
-    if (a->d != 64 && a->d != 128) return PDN_EUNSUPPORTED;
+    if ((a->d != 64 && a->d != 128) || !pdn::qk_norm_fits(*a)) return PDN_EUNSUPPORTED;
     if (a->rot_dim < 0 || a->rot_dim > a->d) return PDN_EINVAL;
     if (a->rot_dim % 16 != 0) return PDN_EUNSUPPORTED;
     if (a->rot_dim > 0) {
@@ -277,7 +277,7 @@ int check_out_norm(const pdn_out_norm_args* a, bool backward = false) {
     if (rc != PDN_OK) return rc;
     if (!valid_dtype(a->o_dtype) || !valid_dtype(a->dtype) || !valid_eps(a->eps) || a->dv < 1) return PDN_EINVAL;
     if (a->act != PDN_ACT_NONE && a->act != PDN_ACT_SILU && a->act != PDN_ACT_SIGMOID) return PDN_EINVAL;
-    if (a->dv % 16 != 0 || a->dv > 256) return PDN_EUNSUPPORTED;
+    if (a->dv % 16 != 0 || a->dv > 256 || !pdn::out_norm_fits(*a)) return PDN_EUNSUPPORTED;
     if (a->w && !aligned16(a->w)) return PDN_EINVAL;
     if (a->T == 0) return PDN_OK;
     if (!a->o || !aligned16(a->o) || (a->z != nullptr) != (a->act != PDN_ACT_NONE)) return PDN_EINVAL;
@@ -324,7 +324,7 @@ int check_scan(const pdn_scan_args* a, bool backward = false, bool check_ws = tr
     if (!a) return PDN_EINVAL;
     int rc = check_scan_kind(a->B, a->T, a->D, a->dtype, a->log_dtype, a->gain);
     if (rc != PDN_OK) return rc;
-    if (pdn::scan_blocks(*a) > kMaxRows) return PDN_EUNSUPPORTED;
+    if (!pdn::scan_fits(*a)) return PDN_EUNSUPPORTED;
     const void* ptrs[] = {a->h0, a->marks, backward ? nullptr : a->hT};
     for (const void* p : ptrs)
         if (p && !aligned16(p)) return PDN_EINVAL;

@@ -687,7 +687,10 @@ hipError_t copy_state(float* dst, const float* src, const pdn_scan_args& a, hipS
 
 }  // namespace
 
-long scan_blocks(const pdn_scan_args& a) { return a.B * strips(a) * tiles(a, kFwdTile < kBwdTile ? kFwdTile : kBwdTile); }
+bool scan_fits(const pdn_scan_args& a) {
+    static_assert(kFwdWaves == kBwdWaves && kBwdTile <= kFwdTile, "the backward has the more threads");
+    return a.B * strips(a) * (tiles(a, kBwdTile) + 1) <= kMaxGridThreads / (64 * kBwdWaves);
+}
 
 size_t scan_fwd_workspace_bytes(const pdn_scan_args& a) { return chain_bytes(a, kFwdTile); }
 

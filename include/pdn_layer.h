@@ -26,7 +26,10 @@ int pdn_layer_version(void);
  * aligned; the stride of a dimension of size 1 is not read.  Inputs may overlap
  * or repeat (stride 0); the rows of a strided output must not overlap each
  * other (PDN_EINVAL).  No output may overlap an input, another output or the
- * workspace, except where two arguments may be one buffer. */
+ * workspace, except where two arguments may be one buffer.
+ * PDN_EUNSUPPORTED where B * T or B * D passes 2^30, or a launch's 2^32 threads
+ * do not suffice (B * T past some 10^8, a scan past some 10^11 channels' tokens,
+ * channels rounded up to 128). */
 
 /* Norm of a head's row x[0..d): r = (c sum x^2 + eps)^(-1/2), with c = 1/d
  * (RMS) or 1 (L2, which the delta rule's keys are commonly given). */

@@ -184,6 +184,11 @@ REFUSED = [
     ("pdn_qk_norm_fwd", {"xq_st": 2300}, E), ("pdn_qk_norm_fwd", {"xk_sh": -128}, E), ("pdn_qk_norm_fwd", {"xq_sb": 1 << 60}, E),
     ("pdn_qk_norm_fwd", {"wq": FAKE + 4}, E), ("pdn_qk_norm_fwd", {"B": 1 << 22, "H": 8}, N),
     ("pdn_qk_norm_fwd", {"B": 1 << 16, "T": 1 << 15}, N),
+    # more workgroups than a launch has room for
+    ("pdn_qk_norm_fwd", {"B": 1 << 14, "T": 1 << 15, "H": 1, "Hq": 1, "Hk": 1}, N),
+    ("pdn_out_norm_fwd", {"B": 1 << 14, "T": 1 << 14, "H": 1, "dv": 256}, N),
+    ("pdn_scan_fwd", {"B": 1 << 20, "T": 1000, "D": 8}, N),
+    ("pdn_scan_bwd", {"fwd.B": 1 << 20, "fwd.T": 1000, "fwd.D": 8}, N),
     ("pdn_qk_norm_bwd", {"fwd.Hk": 5}, E), ("pdn_qk_norm_bwd", {"dq": None}, E), ("pdn_qk_norm_bwd", {"dxk": None}, E),
     ("pdn_qk_norm_bwd", {"dwq": None}, E), ("pdn_qk_norm_bwd", {"fwd.wk": None}, E), ("pdn_qk_norm_bwd", {"dxq_sh": 64}, E),
     ("pdn_qk_norm_bwd", {"dxk_st": 0}, E), ("pdn_qk_norm_bwd", {"dxq_sb": 1280}, E), ("pdn_qk_norm_bwd", {"dk": FAKE + 8}, E),

@@ -302,3 +302,18 @@ def test_calls_from_two_threads():
         t.join()
     for i in range(2):
         assert len(got[i]) == 20 and all(torch.equal(h, want[i]) for h in got[i])
+
+
+def test_very_many_tokens():
+    """40 million rows of 16, some of them looked at."""
+    pdn = _pdn()
+    torch = torch_mod()
+    n, d = 40_000_003, 16
+    gen = torch.Generator(device="cuda").manual_seed(312)
+    o = torch.randn((1, 1, n, d), generator=gen, device="cuda", dtype=torch.float32)
+    y = torch.full((1, n, 1, d), float("nan"), device="cuda")
+    pdn.pdn_out_norm_fwd(o, y)
+    at = torch.cat([torch.arange(100), torch.randint(0, n, (5000,)), torch.arange(n - 100, n)]).to("cuda")
+    want, bound = ref.out_fwd(o[:, :, at].double().cpu().numpy(), None, None, 0, float(np.float32(1e-6)))
+    _close("many tokens", y[:, at], want, bound)
+    assert bool(torch.isfinite(y).all())
