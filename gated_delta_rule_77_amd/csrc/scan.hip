@@ -37,8 +37,8 @@
 // 1.06 times the bytes that the call cannot do without, the published words
 // among them), with the reset of the words (6 us) before it:
 //   forward   B4 T8192 D2048, bf16, fp32 decays       98 us   5.5 TB/s
-//             B1 T65536 D2048, bf16                  176 us   4.6 TB/s
-//             B2 T8192 D4096, bf16, normed gain       84 us   4.8 TB/s
+//             B1 T65536 D2048, bf16                  155 us   5.2 TB/s
+//             B2 T8192 D4096, bf16, normed gain       87 us   4.7 TB/s
 //   backward  of the last, kept states given         140 us   4.8 TB/s
 // A tile lives for 8 to 11 us, of which it loads for 3 to 4, waits for its state
 // for 2 to 5 and stores for 2; two workgroups to a compute unit cover most of
@@ -61,26 +61,31 @@ constexpr int kCols = 128;     // channels of a tile
 // (two workgroups to a compute unit).  Measured at B2 T8192 D4096 bf16, forward
 // 8 x 16 93 us, 16 x 16 101, 4 x 32 104, 8 x 8 108; backward 8 x 12 144, 4 x 16
 // 150, 16 x 8 154, 8 x 8 157, 8 x 16 (one workgroup to a compute unit) 177.
-constexpr int kFwdWaves = 8, kFwdR = 16;
-constexpr int kBwdWaves = 8, kBwdR = 12;
-constexpr int kFwdTile = kFwdWaves * kFwdR;
-constexpr int kBwdTile = kBwdWaves * kBwdR;
+// Forward in bf16 24 tokens: 1% slower there, 161 us instead of 176 over 65536 x
+// 2048 and 49 instead of 66 over 65536 x 128, where longer tiles mean fewer in a
+// chain; in fp32 16: 24 took 77 us instead of 72 at B16 T2048 D1024, 154 instead
+// of 147 at B4 T8192 D2048 (159 instead of 169 over 65536 x 1024).
+constexpr int kWaves = 8;
+constexpr int fwd_r(bool bf16) { return bf16 ? 24 : 16; }
+constexpr int kBwdR = 12;
+constexpr int kBwdTile = kWaves * kBwdR;
 // Predecessors looked at together: 2 and 8 measured 1 to 5% slower (rounds, and
 // registers and traffic).
 constexpr int kWindow = 4;
 // Runs that a carrier takes a round (8, 16 and 32 at one column of 512 tiles:
 // 125, 86 and 65 us), and the columns up to which they have carriers.  With few
 // columns many of a column's tiles are in flight, and each would look far back;
-// with many, the carriers' places are worth more.  Forward without and with
-// them, bf16, T = 65536: 1 column 88 and 65 us, 4 columns 90 and 71, 8 columns
-// 110 and 98, 16 columns 177 and 191.
+// with many, the carriers' places are worth more.  Without and with them, bf16,
+// T = 65536: forward on tiles of 128 tokens 1 column 88 and 65 us, 4 columns 90
+// and 71; as it stands 8 columns 90 and 89 (backward 160 and 142), 16 columns
+// 158 and 165 (backward 269 and 279).
 constexpr int kCarry = 32;
 constexpr int kCarried = 8;
 constexpr u64 kEmpty = ~0ull;
 constexpr unsigned kPolls = 1u << 21;  // loads before a tile gives up: seconds, where thousands are the most that is needed
 
 static_assert(kBwdTile == PDN_SCAN_MARK, "the backward's tiles start at the marks");
-static_assert(PDN_SCAN_MARK % kFwdR == 0, "marks lie at the boundaries of the forward's waves");
+static_assert(PDN_SCAN_MARK % fwd_r(true) == 0 && PDN_SCAN_MARK % fwd_r(false) == 0, "marks lie at the boundaries of the forward's waves");
 
 struct Rows {
     const void* p;
@@ -277,7 +282,7 @@ __device__ __forceinline__ float gain_slope(float a, float g) {
 
 // Two neighbouring channels of a row, as they lie in memory.  What is read once
 // is loaded past the caches (STREAM) where rows begin at 128-byte lines: scan
-// over 65536 tokens by 2048 channels 185 -> 175 us, B16 T2048 D1024 in fp32 86 ->
+// over 65536 tokens by 2048 channels (128 to a tile) 185 -> 175 us, B16 T2048 D1024 in fp32 86 ->
 // 73 us.  Other rows share lines at the strips' borders, which the caches then
 // spare: backward of B11 T2346 D2600 in fp32 307 us past them, 288 us through.
 // (A template argument: the compiler makes one load of two alike.)
@@ -355,8 +360,8 @@ __device__ __forceinline__ float meet(const ScanParams& p, const float (&totA)[W
 }
 
 template <bool XBF, bool LBF, int GAIN, bool LINES, bool WRITE_H>
-__global__ void __launch_bounds__(64 * kFwdWaves) scan_fwd_kernel(ScanParams p) {
-    constexpr int R = kFwdR, W = kFwdWaves;
+__global__ void __launch_bounds__(64 * kWaves, 4) scan_fwd_kernel(ScanParams p) {
+    constexpr int R = fwd_r(XBF), W = kWaves, TILE = W * R;
     __shared__ int slot;
     __shared__ float totA[W][kCols], totH[W][kCols];
     __shared__ float before[W][kCols];  // the state before each wave's tokens
@@ -371,7 +376,7 @@ __global__ void __launch_bounds__(64 * kFwdWaves) scan_fwd_kernel(ScanParams p) 
     }
     const int c2 = 2 * lane, c = c0 + c2;
     const int cc = c < p.D ? c : 0;  // lanes past the last channel read another's
-    const int t0 = at * kFwdTile + wave * R;
+    const int t0 = at * TILE + wave * R;
 
     Raw2<XBF> x[R];
     Raw2<LBF> la[R];
@@ -419,7 +424,7 @@ __global__ void __launch_bounds__(64 * kFwdWaves) scan_fwd_kernel(ScanParams p) 
 #pragma unroll
         for (int w = 0; w < W; ++w) {
             before[w][k] = h;
-            const int t = at * kFwdTile + w * R;
+            const int t = at * TILE + w * R;
             if (p.marks_out && t % PDN_SCAN_MARK == 0 && t < p.T && in)
                 p.marks_out[(static_cast<long>(b) * marks + t / PDN_SCAN_MARK) * p.D + ch] = h;
             h = apply(totA[w][k], h, totH[w][k]);
@@ -444,8 +449,8 @@ __global__ void __launch_bounds__(64 * kFwdWaves) scan_fwd_kernel(ScanParams p) 
 // kind of map, run right to left.  The states h_{t-1} inside a tile come from
 // the kept state before it.
 template <bool XBF, bool LBF, int GAIN, bool LINES>
-__global__ void __launch_bounds__(64 * kBwdWaves, 4) scan_bwd_kernel(ScanParams p) {
-    constexpr int R = kBwdR, W = kBwdWaves;
+__global__ void __launch_bounds__(64 * kWaves, 4) scan_bwd_kernel(ScanParams p) {
+    constexpr int R = kBwdR, W = kWaves;
     __shared__ int slot;
     __shared__ float totA[W][kCols], totH[W][kCols];  // the waves' runs, forward
     __shared__ float totB[W][kCols], totG[W][kCols];  // and backward, the last wave's first
@@ -605,6 +610,7 @@ __global__ void __launch_bounds__(kThreads) scan_state_kernel(float* dst, const 
 // Workspace: the chain of a backward's tiles, then that of a forward's (each
 // its counters, then its words), then the marks that a backward forms.
 long strips(const pdn_scan_args& a) { return (a.D + kCols - 1L) / kCols; }
+int fwd_tile(const pdn_scan_args& a) { return kWaves * fwd_r(a.dtype == PDN_BF16); }
 long tiles(const pdn_scan_args& a, int tile) { return (a.T + tile - 1L) / tile; }
 size_t chain_bytes(const pdn_scan_args& a, int tile) {
     const size_t n = tiles(a, tile), columns = a.B * strips(a);
@@ -640,9 +646,9 @@ hipError_t reset(void* workspace, size_t bytes, hipStream_t st) {
 
 template <bool XBF, bool LBF, int GAIN, bool LINES>
 void launch_tiles(const ScanParams& p, int kind, dim3 grid, hipStream_t st) {
-    if (kind == 0) scan_fwd_kernel<XBF, LBF, GAIN, LINES, true><<<grid, dim3(64 * kFwdWaves), 0, st>>>(p);
-    else if (kind == 1) scan_fwd_kernel<XBF, LBF, GAIN, LINES, false><<<grid, dim3(64 * kFwdWaves), 0, st>>>(p);
-    else scan_bwd_kernel<XBF, LBF, GAIN, LINES><<<grid, dim3(64 * kBwdWaves), 0, st>>>(p);
+    if (kind == 0) scan_fwd_kernel<XBF, LBF, GAIN, LINES, true><<<grid, dim3(64 * kWaves), 0, st>>>(p);
+    else if (kind == 1) scan_fwd_kernel<XBF, LBF, GAIN, LINES, false><<<grid, dim3(64 * kWaves), 0, st>>>(p);
+    else scan_bwd_kernel<XBF, LBF, GAIN, LINES><<<grid, dim3(64 * kWaves), 0, st>>>(p);
 }
 
 template <bool XBF, bool LBF>
@@ -688,17 +694,17 @@ hipError_t copy_state(float* dst, const float* src, const pdn_scan_args& a, hipS
 }  // namespace
 
 bool scan_fits(const pdn_scan_args& a) {
-    static_assert(kFwdWaves == kBwdWaves && kBwdTile <= kFwdTile, "the backward has the more threads");
-    return a.B * strips(a) * (tiles(a, kBwdTile) + 1) <= kMaxGridThreads / (64 * kBwdWaves);
+    static_assert(kBwdR <= fwd_r(false) && kBwdR <= fwd_r(true), "the backward has the most tiles");
+    return a.B * strips(a) * (tiles(a, kBwdTile) + 1) <= kMaxGridThreads / (64 * kWaves);
 }
 
-size_t scan_fwd_workspace_bytes(const pdn_scan_args& a) { return chain_bytes(a, kFwdTile); }
+size_t scan_fwd_workspace_bytes(const pdn_scan_args& a) { return chain_bytes(a, fwd_tile(a)); }
 
 size_t scan_bwd_workspace_bytes(const pdn_scan_bwd_args& b) {
     const pdn_scan_args& a = b.fwd;
     const size_t n = chain_bytes(a, kBwdTile);
     if (n == 0 || a.marks) return n;  // one tile runs from h0 to dhT
-    return n + chain_bytes(a, kFwdTile) + sizeof(float) * a.B * static_cast<size_t>(tiles(a, kBwdTile)) * a.D;
+    return n + chain_bytes(a, fwd_tile(a)) + sizeof(float) * a.B * static_cast<size_t>(tiles(a, kBwdTile)) * a.D;
 }
 
 hipError_t launch_scan_fwd(const pdn_scan_args& a, hipStream_t st) {
@@ -707,9 +713,9 @@ hipError_t launch_scan_fwd(const pdn_scan_args& a, hipStream_t st) {
     p.h = RowsOut{a.h, a.h_sb, a.h_st};
     p.hT = a.hT;
     p.marks_out = a.marks;
-    p.tiles = static_cast<int>(tiles(a, kFwdTile));
+    p.tiles = static_cast<int>(tiles(a, fwd_tile(a)));
     if (p.tiles > 1) {
-        const hipError_t e = reset(a.workspace, chain_bytes(a, kFwdTile), st);
+        const hipError_t e = reset(a.workspace, chain_bytes(a, fwd_tile(a)), st);
         if (e != hipSuccess) return e;
         set_chain(p, static_cast<char*>(a.workspace));
     }
@@ -729,14 +735,14 @@ hipError_t launch_scan_bwd(const pdn_scan_bwd_args& b, hipStream_t st) {
     p.tiles = static_cast<int>(tiles(a, kBwdTile));
     if (p.tiles > 1) {
         char* ws = static_cast<char*>(b.workspace);
-        const size_t bwd = chain_bytes(a, kBwdTile), fwd = a.marks ? 0 : chain_bytes(a, kFwdTile);
+        const size_t bwd = chain_bytes(a, kBwdTile), fwd = a.marks ? 0 : chain_bytes(a, fwd_tile(a));
         hipError_t e = reset(ws, bwd + fwd, st);
         if (e != hipSuccess) return e;
         set_chain(p, ws);
         if (!a.marks) {
             ScanParams f = params(a);
             f.marks_out = reinterpret_cast<float*>(ws + bwd + fwd);
-            f.tiles = static_cast<int>(tiles(a, kFwdTile));
+            f.tiles = static_cast<int>(tiles(a, fwd_tile(a)));
             set_chain(f, ws + bwd);
             e = launch_kind(f, a, 1, st);
             if (e != hipSuccess) return e;

@@ -306,6 +306,12 @@ SCAN = [  # B, T, D, type, type of log_a, gain, h0 / dhT, resets
     (2, 9000, 24, "fp32", "fp32", 0, True, True),
     (3, 700, 520, "bf16", "fp32", 1, True, True),      # more columns than have carriers
     (9, 3001, 72, "fp32", "fp32", 2, True, False),
+    # a bf16 forward tile, one token less and more, and lengths that are multiples of both directions'
+    (1, 191, 64, "bf16", "bf16", 1, True, False),
+    (2, 192, 136, "bf16", "fp32", 2, True, True),
+    (1, 193, 72, "bf16", "bf16", 0, True, False),
+    (3, 576, 520, "bf16", "bf16", 2, True, True),
+    (1, 6145, 64, "bf16", "fp32", 0, True, False),     # 32 whole tiles and a token: a carrier's round and one more
 ]
 
 
