@@ -15,23 +15,7 @@
 // lane; its row addresses are scalars.  The waves' runs meet in LDS.  What is
 // left is the state before the tile:
 //
-// each tile publishes its (A, H) as soon as it has it, then looks back along
-// its column for the nearest tile whose state behind it is known, applies the
-// (A, H) of the tiles between in their order, and publishes the state behind
-// itself.  Whichever tile it starts from, that is the same chain of operations
-// h_{j+1} = A_j h_j + H_j, so results are the same bits whatever the timing.
-// A column's tiles are dealt by a counter of its own, in the order of their
-// tokens: a tile waits only for tiles that started before it, so every wait
-// ends.  (The waits are bounded all the same: a call whose workspace another
-// call overwrites gives NaN instead of hanging.)
-//
-// A published pair is one 64-bit word, stored and loaded by relaxed atomics at
-// device scope: the word is its own flag (all ones = not there yet, which no
-// published word is), so no fence, and no write-back of an L2, is needed.
-//
-// With few columns each has a carrier besides: its first workgroup, which takes
-// the tiles' (A, H) as they come and publishes the states behind them, the same
-// chain of operations in one place.
+// the tiles hand it on along their column as scan_chain.h says.
 //
 // Measured on an MI355X, whose large copies reach 5.3 TB/s (counters: 1.03 to
 // 1.06 times the bytes that the call cannot do without, the published words
@@ -49,14 +33,12 @@
 // later factor is zero.
 #include "layer.h"
 #include "rows.h"
+#include "scan_chain.h"
 
 namespace pdn {
 namespace {
 
-typedef unsigned long long u64;
-
 constexpr int kThreads = 256;  // of the step, reset and copy kernels
-constexpr int kCols = 128;     // channels of a tile
 // Waves of a workgroup and tokens of a wave.  Both directions fit 128 registers
 // (two workgroups to a compute unit).  Measured at B2 T8192 D4096 bf16, forward
 // 8 x 16 93 us, 16 x 16 101, 4 x 32 104, 8 x 8 108; backward 8 x 12 144, 4 x 16
@@ -69,21 +51,6 @@ constexpr int kWaves = 8;
 constexpr int fwd_r(bool bf16) { return bf16 ? 24 : 16; }
 constexpr int kBwdR = 12;
 constexpr int kBwdTile = kWaves * kBwdR;
-// Predecessors looked at together: 2 and 8 measured 1 to 5% slower (rounds, and
-// registers and traffic).
-constexpr int kWindow = 4;
-// Runs that a carrier takes a round (8, 16 and 32 at one column of 512 tiles:
-// 125, 86 and 65 us), and the columns up to which they have carriers.  With few
-// columns many of a column's tiles are in flight, and each would look far back;
-// with many, the carriers' places are worth more.  Without and with them, bf16,
-// T = 65536: forward on tiles of 128 tokens 1 column 88 and 65 us, 4 columns 90
-// and 71; as it stands 8 columns 90 and 89 (backward 160 and 142), 16 columns
-// 158 and 165 (backward 269 and 279).
-constexpr int kCarry = 32;
-constexpr int kCarried = 8;
-constexpr u64 kEmpty = ~0ull;
-constexpr unsigned kPolls = 1u << 21;  // loads before a tile gives up: seconds, where thousands are the most that is needed
-
 static_assert(kBwdTile == PDN_SCAN_MARK, "the backward's tiles start at the marks");
 static_assert(PDN_SCAN_MARK % fwd_r(true) == 0 && PDN_SCAN_MARK % fwd_r(false) == 0, "marks lie at the boundaries of the forward's waves");
 
@@ -94,14 +61,6 @@ struct Rows {
 struct RowsOut {
     void* p;
     long sb, st;
-};
-
-// Where a launch's tiles meet: the counter that deals each column's, and, for
-// every column and tile in processing order, kCols words of each kind.
-struct Chain {
-    unsigned* counters;
-    u64* agg;   // (A, H) of a tile
-    u64* inc;   // the state behind it
 };
 
 struct ScanParams {
@@ -116,94 +75,8 @@ struct ScanParams {
     int T, D;
     int strips;          // kCols-channel strips of a row
     int columns;         // B * strips
-    int tiles;           // along T
-    int carrier;         // 1: each column's first workgroup carries its state (see carry)
     Chain chain;
 };
-
-__device__ __forceinline__ float apply(float A, float h, float H) { return A == 0.0f ? H : fmaf(A, h, H); }
-// the decay of a run `first` followed by one of decay `then`
-__device__ __forceinline__ float join(float first, float then) { return then == 0.0f ? 0.0f : first * then; }
-
-__device__ __forceinline__ u64 pair_word(float A, float H) {
-    // a NaN from the inputs could have all bits set, and with it the word
-    const uint32_t a = A != A ? 0x7fc00000u : __float_as_uint(A);
-    return (static_cast<u64>(__float_as_uint(H)) << 32) | a;
-}
-__device__ __forceinline__ float word_A(u64 w) { return __uint_as_float(static_cast<uint32_t>(w)); }
-__device__ __forceinline__ float word_H(u64 w) { return __uint_as_float(static_cast<uint32_t>(w >> 32)); }
-
-template <class T>
-__device__ __forceinline__ T peek(const T* p) {
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-template <class T>
-__device__ __forceinline__ void publish(T* p, T w) {
-    __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-
-// The word at p, once it is there; `polls` counts down over all of a wave's waits.
-__device__ __forceinline__ u64 settled(const u64* p, u64 w, unsigned& polls) {
-    while (!__all(w != kEmpty) && polls) {
-        --polls;
-        __builtin_amdgcn_s_sleep(1);
-        w = peek(p);
-    }
-    return w;
-}
-
-// The published states behind the kWindow tiles up to `from`.
-struct Window {
-    u64 w[kWindow];
-    __device__ __forceinline__ void load(const u64* first, int from) {
-#pragma unroll
-        for (int k = 0; k < kWindow; ++k) w[k] = peek(first + static_cast<long>(max(from - k, 0)) * kCols);
-    }
-};
-
-// The state before tile `at` of this column (at > 0), one channel to a lane of
-// one wave; agg and inc point at this lane's word of the column's first tile,
-// `inc_words` holds the states behind the tiles up to at - 1.
-//
-// A load from where other workgroups publish takes 1.5 to 2 us here under the
-// tiles' own traffic, so what counts is how many of them follow one another:
-// one for the known states, one for the runs behind the nearest of them.  (The
-// first is issued before the tile's own run is published: the memory counter is
-// in order, so a load behind a store waits for both.)
-__device__ __forceinline__ float look_back(const u64* agg, const u64* inc, Window& inc_words, int at) {
-    unsigned polls = kPolls;
-    int known = -1;
-    float h = 0.0f;
-    for (int from = at - 1;;) {
-#pragma unroll
-        for (int k = 0; k < kWindow; ++k)
-            if (known < 0 && from - k >= 0 && __all(inc_words.w[k] != kEmpty)) {
-                known = from - k;
-                h = word_H(inc_words.w[k]);
-            }
-        if (known >= 0) break;
-        if (!--polls) return __uint_as_float(0x7fc00000u);
-        if (from >= kWindow) {
-            from -= kWindow;
-        } else {
-            from = at - 1;
-            __builtin_amdgcn_s_sleep(1);
-        }
-        inc_words.load(inc, from);
-    }
-    for (int j = known + 1; j < at; j += kWindow) {
-        u64 r[kWindow];
-#pragma unroll
-        for (int k = 0; k < kWindow; ++k) r[k] = peek(agg + static_cast<long>(min(j + k, at - 1)) * kCols);
-#pragma unroll
-        for (int k = 0; k < kWindow; ++k) {
-            if (j + k >= at) break;
-            r[k] = settled(agg + static_cast<long>(j + k) * kCols, r[k], polls);
-            h = apply(word_A(r[k]), h, word_H(r[k]));
-        }
-    }
-    return polls ? h : __uint_as_float(0x7fc00000u);
-}
 
 // The counters lie a 128-byte line apart and start at all ones, one below 0.
 constexpr int kCounterStep = 32;
@@ -214,41 +87,12 @@ constexpr int kCounterStep = 32;
 __device__ __forceinline__ void deal(const ScanParams& p, int* slot, int& column, int& at) {
     column = by_xcd(blockIdx.x % p.columns, p.columns);
     at = 0;
-    if (p.tiles == 1) return;
+    if (p.chain.tiles == 1) return;
     if (threadIdx.x == 0)
         *slot = static_cast<int>(1u + __hip_atomic_fetch_add(p.chain.counters + static_cast<long>(column) * kCounterStep, 1u,
                                                              __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
     __syncthreads();
-    at = __builtin_amdgcn_readfirstlane(*slot) - p.carrier;  // -1: this workgroup is the carrier
-}
-
-// The carrier's work, a channel to a lane of its first two waves: from the
-// state `h` before the column's first tile, the state behind each tile but the
-// last, as their runs come in, up to kCarry of them a round.  It waits only for
-// tiles that started after it, and every one that has started publishes its run
-// before it waits, so all started tiles come to an end, and the next ones start.
-__device__ void carry(const ScanParams& p, int column, int ch, float h) {
-    const long word = static_cast<long>(column) * p.tiles * kCols + ch;
-    const int n = p.tiles - 1;
-    unsigned polls = kPolls;
-    for (int next = 0; next < n && polls;) {
-        u64 r[kCarry];
-#pragma unroll
-        for (int k = 0; k < kCarry; ++k) r[k] = peek(p.chain.agg + word + static_cast<long>(min(next + k, n - 1)) * kCols);
-        int done = 0;
-#pragma unroll
-        for (int k = 0; k < kCarry; ++k)
-            if (done == k && next + k < n && __all(r[k] != kEmpty)) {
-                h = apply(word_A(r[k]), h, word_H(r[k]));
-                publish(p.chain.inc + word + static_cast<long>(next + k) * kCols, pair_word(0.0f, h));
-                done = k + 1;
-            }
-        next += done;
-        if (!done) {
-            --polls;
-            __builtin_amdgcn_s_sleep(1);
-        }
-    }
+    at = __builtin_amdgcn_readfirstlane(*slot) - p.chain.carrier;  // -1: this workgroup is the carrier
 }
 
 __device__ __forceinline__ float decay(float la) { return __builtin_amdgcn_exp2f(la * kLog2e); }
@@ -320,45 +164,6 @@ struct Raw2<false> {
     }
 };
 
-// What waves 0 and 1 do for the tile, a channel to a lane: join the waves'
-// runs (totA, totH, in processing order), publish, look back, publish; the
-// state before the tile's first run, and through `behind` that behind its last.
-template <int WAVES>
-__device__ __forceinline__ float meet(const ScanParams& p, const float (&totA)[WAVES][kCols],
-                                      const float (&totH)[WAVES][kCols], int column, int at, int ch, float start,
-                                      float& behind) {
-    const long word = static_cast<long>(column) * p.tiles * kCols + ch;
-    const long mine = word + static_cast<long>(at) * kCols;
-    const bool last = at + 1 == p.tiles;
-    Window inc_words;
-    if (at > 0 && !p.carrier) inc_words.load(p.chain.inc + word, at - 1);
-    float tA = totA[0][ch], tH = totH[0][ch];
-#pragma unroll
-    for (int w = 1; w < WAVES; ++w) {
-        tH = apply(totA[w][ch], tH, totH[w][ch]);
-        tA = join(tA, totA[w][ch]);
-    }
-    float h = start;
-    if (p.carrier) {
-        // the last tile may write over what `start` was read from, and here
-        // only this order keeps it behind that load
-        asm volatile("" : : "v"(start) : "memory");
-        if (!last) publish(p.chain.agg + mine, pair_word(tA, tH));
-        if (at > 0) {
-            unsigned polls = kPolls;
-            const u64* from = p.chain.inc + mine - kCols;
-            const u64 w = settled(from, peek(from), polls);
-            h = polls ? word_H(w) : __uint_as_float(0x7fc00000u);
-        }
-    } else if (at > 0) {
-        if (!last) publish(p.chain.agg + mine, pair_word(tA, tH));
-        h = look_back(p.chain.agg + word, p.chain.inc + word, inc_words, at);
-    }
-    behind = apply(tA, h, tH);
-    if (!last && !p.carrier) publish(p.chain.inc + mine, pair_word(0.0f, behind));
-    return h;
-}
-
 template <bool XBF, bool LBF, int GAIN, bool LINES, bool WRITE_H>
 __global__ void __launch_bounds__(64 * kWaves, 4) scan_fwd_kernel(ScanParams p) {
     constexpr int R = fwd_r(XBF), W = kWaves, TILE = W * R;
@@ -370,8 +175,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) scan_fwd_kernel(ScanParams p) 
     deal(p, &slot, column, at);
     const int b = column / p.strips, c0 = (column - b * p.strips) * kCols;
     if (at < 0) {
-        const int ch = c0 + tid;
-        if (wave < 2) carry(p, column, tid, p.h0 && ch < p.D ? p.h0[static_cast<long>(b) * p.D + ch] : 0.0f);
+        if (wave < 2) carry(p.chain, column, tid);
         return;
     }
     const int c2 = 2 * lane, c = c0 + c2;
@@ -418,8 +222,8 @@ __global__ void __launch_bounds__(64 * kWaves, 4) scan_fwd_kernel(ScanParams p) 
         const bool in = ch < p.D;
         const long state = static_cast<long>(b) * p.D + ch;
         float behind;
-        float h = meet<W>(p, totA, totH, column, at, k, at == 0 && p.h0 && in ? p.h0[state] : 0.0f, behind);
-        if (at + 1 == p.tiles && p.hT && in) p.hT[state] = behind;
+        float h = meet<W>(p.chain, totA, totH, column, at, k, at == 0 && p.h0 && in ? p.h0[state] : 0.0f, behind);
+        if (at + 1 == p.chain.tiles && p.hT && in) p.hT[state] = behind;
         const int marks = (p.T + PDN_SCAN_MARK - 1) / PDN_SCAN_MARK;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
@@ -459,11 +263,10 @@ __global__ void __launch_bounds__(64 * kWaves, 4) scan_bwd_kernel(ScanParams p) 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int column, at;
     deal(p, &slot, column, at);
-    const int tile = p.tiles - 1 - at;
+    const int tile = p.chain.tiles - 1 - at;
     const int b = column / p.strips, c0 = (column - b * p.strips) * kCols;
     if (at < 0) {
-        const int ch = c0 + tid;
-        if (wave < 2) carry(p, column, tid, p.dhT && ch < p.D ? p.dhT[static_cast<long>(b) * p.D + ch] : 0.0f);
+        if (wave < 2) carry(p.chain, column, tid);
         return;
     }
     const int c2 = 2 * lane, c = c0 + c2;
@@ -524,10 +327,10 @@ __global__ void __launch_bounds__(64 * kWaves, 4) scan_bwd_kernel(ScanParams p) 
         const bool in = ch < p.D;
         const long state = static_cast<long>(b) * p.D + ch;
         float h = 0.0f, out;
-        if (in && p.marks) h = p.marks[(static_cast<long>(b) * p.tiles + tile) * p.D + ch];
+        if (in && p.marks) h = p.marks[(static_cast<long>(b) * p.chain.tiles + tile) * p.D + ch];
         else if (in && p.h0) h = p.h0[state];
-        float r = meet<W>(p, totB, totG, column, at, k, at == 0 && p.dhT && in ? p.dhT[state] : 0.0f, out);
-        if (at + 1 == p.tiles && p.dh0 && in) p.dh0[state] = out;
+        float r = meet<W>(p.chain, totB, totG, column, at, k, at == 0 && p.dhT && in ? p.dhT[state] : 0.0f, out);
+        if (at + 1 == p.chain.tiles && p.dh0 && in) p.dh0[state] = out;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
             before[w][k] = h;
@@ -630,10 +433,10 @@ ScanParams params(const pdn_scan_args& a) {
 }
 
 void set_chain(ScanParams& p, char* at) {
-    p.carrier = p.columns <= kCarried;
+    p.chain.carrier = p.chain.tiles > 1 && p.columns <= kCarried;
     p.chain.counters = reinterpret_cast<unsigned*>(at);
     p.chain.agg = reinterpret_cast<u64*>(at + sizeof(unsigned) * kCounterStep * p.columns);
-    p.chain.inc = p.chain.agg + static_cast<long>(p.columns) * p.tiles * kCols;
+    p.chain.inc = p.chain.agg + static_cast<long>(p.columns) * p.chain.tiles * kCols;
 }
 
 hipError_t reset(void* workspace, size_t bytes, hipStream_t st) {
@@ -674,7 +477,7 @@ bool whole_lines(const void* p, long sb, long st, int32_t dtype, const pdn_scan_
 
 // kind: 0 forward, 1 forward for the marks alone, 2 backward
 hipError_t launch_kind(const ScanParams& p, const pdn_scan_args& a, int kind, hipStream_t st) {
-    const dim3 grid(static_cast<unsigned>(static_cast<long>(p.columns) * (p.tiles + p.carrier)));
+    const dim3 grid(static_cast<unsigned>(static_cast<long>(p.columns) * (p.chain.tiles + p.chain.carrier)));
     const bool xb = a.dtype == PDN_BF16, lb = a.log_dtype == PDN_BF16;
     const bool lines = whole_lines(p.x.p, p.x.sb, p.x.st, a.dtype, a) && whole_lines(p.la.p, p.la.sb, p.la.st, a.log_dtype, a) &&
                        (kind != 2 || whole_lines(p.dh.p, p.dh.sb, p.dh.st, a.dtype, a));
@@ -713,8 +516,8 @@ hipError_t launch_scan_fwd(const pdn_scan_args& a, hipStream_t st) {
     p.h = RowsOut{a.h, a.h_sb, a.h_st};
     p.hT = a.hT;
     p.marks_out = a.marks;
-    p.tiles = static_cast<int>(tiles(a, fwd_tile(a)));
-    if (p.tiles > 1) {
+    p.chain.tiles = static_cast<int>(tiles(a, fwd_tile(a)));
+    if (p.chain.tiles > 1) {
         const hipError_t e = reset(a.workspace, chain_bytes(a, fwd_tile(a)), st);
         if (e != hipSuccess) return e;
         set_chain(p, static_cast<char*>(a.workspace));
@@ -732,8 +535,8 @@ hipError_t launch_scan_bwd(const pdn_scan_bwd_args& b, hipStream_t st) {
     p.dhT = b.dhT;
     p.dh0 = b.dh0;
     p.marks = a.marks;
-    p.tiles = static_cast<int>(tiles(a, kBwdTile));
-    if (p.tiles > 1) {
+    p.chain.tiles = static_cast<int>(tiles(a, kBwdTile));
+    if (p.chain.tiles > 1) {
         char* ws = static_cast<char*>(b.workspace);
         const size_t bwd = chain_bytes(a, kBwdTile), fwd = a.marks ? 0 : chain_bytes(a, fwd_tile(a));
         hipError_t e = reset(ws, bwd + fwd, st);
@@ -742,7 +545,7 @@ hipError_t launch_scan_bwd(const pdn_scan_bwd_args& b, hipStream_t st) {
         if (!a.marks) {
             ScanParams f = params(a);
             f.marks_out = reinterpret_cast<float*>(ws + bwd + fwd);
-            f.tiles = static_cast<int>(tiles(a, fwd_tile(a)));
+            f.chain.tiles = static_cast<int>(tiles(a, fwd_tile(a)));
             set_chain(f, ws + bwd);
             e = launch_kind(f, a, 1, st);
             if (e != hipSuccess) return e;
