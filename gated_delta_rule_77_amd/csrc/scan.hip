@@ -110,10 +110,12 @@ __device__ __forceinline__ float one_minus_exp(float y, float e) {
     return y < -0.35f ? 1.0f - e : -y * s;
 }
 
+// The normed gain of a decay of one is +0, whichever zero la is (of la = +0 the
+// difference above is -0): the slope divides by it, and tends to -inf there.
 template <int GAIN>
 __device__ __forceinline__ float gain(float la, float a) {
     if constexpr (GAIN == PDN_GAIN_COMPLEMENT) return one_minus_exp(la, a);
-    if constexpr (GAIN == PDN_GAIN_NORM) return __builtin_amdgcn_sqrtf(one_minus_exp(2.0f * la, a * a));
+    if constexpr (GAIN == PDN_GAIN_NORM) return fabsf(__builtin_amdgcn_sqrtf(one_minus_exp(2.0f * la, a * a)));
     return 1.0f;
 }
 // its derivative by la, given the gain g

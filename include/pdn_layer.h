@@ -234,8 +234,9 @@ typedef struct pdn_scan_args {
  *   dh         strided [B,T,D] in dtype.     dhT: [B,D] fp32; NULL = zeros.
  *   dx, dlog_a strided [B,T,D] in dtype and log_dtype.
  *   dh0        [B,D] fp32; NULL = not written; may be dhT.
- * PDN_GAIN_NORM's derivative is unbounded at a = 1: such tokens give inf or
- * NaN in dlog_a.
+ * PDN_GAIN_NORM's derivative tends to -inf as log_a tends to 0: tokens with
+ * log_a = 0 (of either sign) give an infinity of the sign of -x_t G_t in dlog_a
+ * (NaN where that is 0).
  */
 typedef struct pdn_scan_bwd_args {
     pdn_scan_args fwd;
