@@ -87,7 +87,7 @@ __device__ __forceinline__ int half_partner(int lane, int e, int rot) {
 template <int ROPE>
 __device__ __forceinline__ void angles(const QkParams& p, int t, int n, int e, int pl, float (&c)[8], float (&s)[8]) {
     const double pos = p.positions ? static_cast<double>(p.positions[n]) : static_cast<double>(t);
-    const bool rotated = 8 * e < p.rot;  // rot is a multiple of 16: all of a lane's elements, or none
+    const bool rotated = 8 * e < p.rot;
     const bool second = ROPE == ROPE_HALF && 16 * e >= p.rot;
     const int pair0 = ROPE == ROPE_HALF ? 8 * e - (second ? (p.rot >> 1) - 4 : 0) : 4 * e;
     float cn[4], sn[4];
@@ -115,14 +115,14 @@ __device__ __forceinline__ void angles(const QkParams& p, int t, int n, int e, i
     }
 }
 
+// Zeros behind the rotated part: times a sine of zero an infinity there would
+// reach its neighbour, or turn itself into NaN.
 template <int ROPE>
-__device__ __forceinline__ void partners(const float (&x)[8], int lane, float (&xp)[8]) {
-    if constexpr (ROPE == ROPE_HALF) {
+__device__ __forceinline__ void partners(const float (&x)[8], int lane, bool rotated, float (&xp)[8]) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) xp[j] = __shfl(x[j], lane, 64);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) xp[j] = x[j ^ 1];
+    for (int j = 0; j < 8; ++j) {
+        const float other = ROPE == ROPE_HALF ? __shfl(x[j], lane, 64) : x[j ^ 1];
+        xp[j] = rotated ? other : 0.0f;
     }
 }
 
@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_fwd_kernel(QkParams p) {
     }
     float c[8], s[8];
     int pl = lane;
+    const bool rotated = 8 * e < p.rot;  // rot is a multiple of 16: all of a lane's elements, or none
     if constexpr (ROPE == ROPE_HALF) pl = half_partner(lane, e, p.rot);
     if constexpr (ROPE != ROPE_NONE) angles<ROPE>(p, t, n, e, pl, c, s);
 
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_fwd_kernel(QkParams p) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) wc[j] = (q.w ? q.w[8 * e + j] : 1.0f) * q.scale;
         if constexpr (ROPE != ROPE_NONE) {
-            partners<ROPE>(wc, pl, ws);
+            partners<ROPE>(wc, pl, rotated, ws);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 wc[j] *= c[j];
@@ -200,8 +201,13 @@ __global__ void __launch_bounds__(kThreads) qk_norm_fwd_kernel(QkParams p) {
                     for (int j = 0; j < 8; ++j) y[j] = x[j] * wc[j] * r;
                 } else {
                     float xp[8];
-                    if constexpr (ROPE == ROPE_HALF) now[u].from_lane(pl).get(xp);
-                    else partners<ROPE>(x, pl, xp);
+                    if constexpr (ROPE == ROPE_HALF) {
+                        Raw8<BF16> other = now[u].from_lane(pl);
+                        if (!rotated) other.zero();
+                        other.get(xp);
+                    } else {
+                        partners<ROPE>(x, pl, rotated, xp);
+                    }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) y[j] = fmaf(x[j], wc[j], xp[j] * ws[j]) * r;
                 }
@@ -248,6 +254,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(QkParams p) {
     const int groups = (p.tokens + SLOTS - 1) / SLOTS;
     float dw[2][8] = {};
     int pl = lane;
+    const bool rotated = 8 * e < p.rot;
     if constexpr (ROPE == ROPE_HALF) pl = half_partner(lane, e, p.rot);
 
     for (int grp = blockIdx.x; grp < groups; grp += gridDim.x) {
@@ -294,7 +301,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(QkParams p) {
                     raw[u].get(x);
                     if constexpr (ROPE != ROPE_NONE) {  // the rotation turned back: its transpose
                         float gp[8];
-                        partners<ROPE>(g[u], pl, gp);
+                        partners<ROPE>(g[u], pl, rotated, gp);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) g[u][j] = fmaf(g[u][j], c[j], -gp[j] * s[j]);
                     }

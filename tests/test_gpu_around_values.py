@@ -4,6 +4,7 @@ gates far from zero, slices of a longer buffer of positions."""
 import numpy as np
 import pytest
 
+import around_ref as ref
 from test_gpu_around import _down, _nan, _pdn, _up
 
 pytestmark = pytest.mark.gpu
@@ -35,3 +36,43 @@ def test_normed_gain_slope_at_a_decay_of_one(dtype, T):
     pdn.pdn_scan_fwd(xd, lad, h, gain=pdn.PDN_GAIN_NORM)
     h = _down(h)
     np.testing.assert_array_equal(h[:, at], h[:, at - 1] if at else 0 * h[:, 0])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("d,rot", [(64, 16), (128, 64), (128, 112)])
+@pytest.mark.parametrize("layout", [0, 1])
+def test_elements_behind_the_rotation_stay(layout, d, rot, dtype):
+    """Without a norm an element behind rot_dim is its input times the scale, and
+    no other element sees it: infinities and NaN there, forward and backward."""
+    pdn = _pdn()
+    rng = np.random.default_rng(401)
+    B, T, H = 2, 19, 3
+    x = rng.standard_normal((B, T, H, d)).astype(np.float32)
+    if dtype == "bf16":
+        x = ref.bf16(x)
+    g = rng.standard_normal((B, H, T, d)).astype(np.float32)
+    bad_x, bad_g = x.copy(), g.copy()
+    for bad in (bad_x, bad_g):
+        bad[0, 1, 2, rot + 3], bad[1, 2, 0, rot + 8], bad[1, 0, 1, d - 1] = np.inf, -np.inf, np.nan
+    kw = dict(norm=pdn.PDN_NORM_NONE, q_scale=0.5, k_scale=2.0, rope_layout=layout,
+              inv_freq=_up(10000.0 ** (-2.0 * np.arange(rot // 2) / rot)))
+
+    def both(xv, gv):
+        xd = _up(xv, dtype)
+        q, k = _nan((B, H, T, d), dtype), _nan((B, H, T, d), dtype)
+        pdn.pdn_qk_norm_fwd(xd, xd, q, k, **kw)
+        dxq, dxk = _nan((B, T, H, d), dtype), _nan((B, T, H, d), dtype)
+        pdn.pdn_qk_norm_bwd(xd, xd, _up(gv), _up(gv), dxq, dxk, **kw)
+        return [_down(t) for t in (q, k, dxq, dxk)]
+
+    for xv, gv in ((bad_x, g), (x, bad_g)):
+        good, bad = both(x, g), both(xv, gv)
+        for i, (a, b) in enumerate(zip(good, bad)):
+            source, given = (xv.transpose(0, 2, 1, 3), x.transpose(0, 2, 1, 3)) if i < 2 else (gv.transpose(0, 2, 1, 3), g.transpose(0, 2, 1, 3))
+            hit = ~np.isfinite(source)
+            np.testing.assert_array_equal(b[hit], source[hit])      # inf stays inf, NaN NaN
+            np.testing.assert_array_equal(b[~hit], a[~hit])
+            behind = given[..., rot:].astype(np.float64) * (0.5, 2.0)[i % 2]
+            if i >= 2 and dtype == "bf16":
+                behind = ref.bf16(behind.astype(np.float32)).astype(np.float64)
+            np.testing.assert_array_equal(a[..., rot:], behind)
