@@ -470,7 +470,9 @@ __global__ void __launch_bounds__(kThreads) out_norm_bwd_kernel(OutParams p) {
                             dz[j] = n1 * f * fmaf(zf[j], 1.0f - f, 1.0f);
                             g[j] *= f * zf[j];
                         } else {
-                            dz[j] = n1 * f * (1.0f - f);
+                            // 1 - f as it is for -z: where f is near one, the
+                            // difference would keep few of its digits
+                            dz[j] = n1 * f * sigmoid(-zf[j]);
                             g[j] *= f;
                         }
                     }

@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 
 import around_ref as ref
-from test_gpu_around import _down, _nan, _pdn, _up
+from around_ref import U
+from test_gpu_around import _close, _down, _nan, _pdn, _up
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +77,23 @@ def test_elements_behind_the_rotation_stay(layout, d, rot, dtype):
             if i >= 2 and dtype == "bf16":
                 behind = ref.bf16(behind.astype(np.float32)).astype(np.float64)
             np.testing.assert_array_equal(a[..., rot:], behind)
+
+
+def test_sigmoid_gate_gradient_far_from_zero():
+    """dz = n f (1 - f) w dy keeps its relative accuracy where f is near one:
+    2 |z| for the exponent's argument (its constant and its product), 12 for exp2,
+    add and reciprocal of f and of 1 - f, 13 for the row's norm, 5 products."""
+    pdn = _pdn()
+    rng = np.random.default_rng(402)
+    B, H, T, dv = 1, 2, 40, 32
+    o = rng.standard_normal((B, H, T, dv)).astype(np.float32)
+    z = rng.uniform(-80.0, 80.0, (B, T, H, dv)).astype(np.float32)
+    z[0, 0, 0, :4] = [17.5, 20.0, 60.0, -60.0]
+    dy = rng.choice([-1.0, 1.0], (B, T, H, dv)).astype(np.float32) * rng.uniform(0.5, 2.0, (B, T, H, dv)).astype(np.float32)
+    w = (1 + 0.2 * rng.standard_normal(dv)).astype(np.float32)
+    do, dz, dw = _nan((B, H, T, dv)), _nan((B, T, H, dv)), _nan((dv,))
+    pdn.pdn_out_norm_bwd(_up(o), _up(dy), do, z=_up(z), dz=dz, w=_up(w), dw=dw, act=pdn.PDN_ACT_SIGMOID)
+    x, z64 = o.astype(np.float64).transpose(0, 2, 1, 3), z.astype(np.float64)
+    r = ref.norm_factor(x, 1, float(np.float32(1e-6)))[0]
+    want = dy * x * r * w.astype(np.float64) / (1 + np.exp(-z64)) / (1 + np.exp(z64))
+    _close("sigmoid dz", dz, want, np.abs(want) * (32 + 2 * np.abs(z64)) * U)
