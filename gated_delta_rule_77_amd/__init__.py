@@ -619,7 +619,7 @@ class _Call:
     each is one comparison on the way through; the message is put together only
     when one fails."""
 
-    __slots__ = ("a", "index")
+    __slots__ = ("a", "index", "moved")
 
     def __init__(self, struct, first):
         if _torch is None:
@@ -627,7 +627,7 @@ class _Call:
         index = first.get_device() if hasattr(first, "get_device") else -1
         if index < 0:
             raise ValueError("the first argument must be a tensor in device memory")
-        self.a, self.index = struct(), index
+        self.a, self.index, self.moved = struct(), index, None
 
     def plain(self, t, name, shape, dtype):
         """Pointer of a contiguous tensor (None stays None)."""
@@ -637,6 +637,18 @@ class _Call:
             self._refuse(t, name, shape, dtype)
             raise ValueError("%s must be contiguous" % name)
         return t.data_ptr()
+
+    def table(self, a, t, name, shape, dtype):
+        """Sets a.<name> to a contiguous tensor of 8-byte numbers, which may be a
+        slice of a longer one and so begin 8 bytes off the library's alignment.
+        Such a slice is copied on the launch's stream, into memory that begins
+        where it has to; until then the field holds an address that only the
+        checks see."""
+        p = self.plain(t, name, shape, dtype)
+        if p and p % 16:
+            self.moved = (self.moved or []) + [(a, name, t)]
+            p -= p % 16
+        setattr(a, name, p)
 
     def rows(self, t, name, shape, dtype):
         """Pointer of a strided tensor; its last dimension must be contiguous."""
@@ -675,15 +687,20 @@ class _Call:
                 return self.launch(name, stream, workspace)
         a, size = self.a, _AROUND[name][2]
         lib = _lib or load_library()
+        if self.moved:
+            # a kernel (a sum with zero), as all that a captured call records
+            if stream is None:
+                copies = [t + 0 for _, _, t in self.moved]
+            else:
+                with _torch.cuda.stream(self._stream(stream)):
+                    copies = [t + 0 for _, _, t in self.moved]
+            for (struct, field, _), t in zip(self.moved, copies):
+                setattr(struct, field, t.data_ptr())
         if size:
             if workspace is None:
                 n = self.size(size)
                 if n and stream is not None:
-                    own = stream
-                    if isinstance(stream, int):   # a handle; 0 is the default stream's
-                        own = (_torch.cuda.ExternalStream(stream, device=self.index) if stream
-                               else _torch.cuda.default_stream(self.index))
-                    with _torch.cuda.stream(own):
+                    with _torch.cuda.stream(self._stream(stream)):
                         workspace = _torch.empty(n, dtype=_torch.uint8, device="cuda")
                 elif n:
                     workspace = _torch.empty(n, dtype=_torch.uint8, device="cuda")
@@ -698,6 +715,13 @@ class _Call:
         rc = getattr(lib, name)(ctypes.byref(a), stream)
         if rc != PDN_OK:
             raise PdnError(rc, name)
+
+    def _stream(self, stream):
+        """torch's object for a stream that the caller gave."""
+        if not isinstance(stream, int):
+            return stream
+        # a handle; 0 is the default stream's
+        return _torch.cuda.ExternalStream(stream, device=self.index) if stream else _torch.cuda.default_stream(self.index)
 
 
 def _qk_norm(c, a, xq, xk, H, norm, eps, wq, wk, q_scale, k_scale, inv_freq, positions, rope_layout, rope_scale):
@@ -714,8 +738,8 @@ def _qk_norm(c, a, xq, xk, H, norm, eps, wq, wk, q_scale, k_scale, inv_freq, pos
     if inv_freq is not None:
         half = inv_freq.shape[0]
         a.rot_dim, a.rope_layout, a.rope_scale = 2 * half, rope_layout, rope_scale
-        a.inv_freq = c.plain(inv_freq, "inv_freq", (half,), _torch.float64)
-        a.positions = c.plain(positions, "positions", (B, T), _torch.int64)
+        c.table(a, inv_freq, "inv_freq", (half,), _torch.float64)
+        c.table(a, positions, "positions", (B, T), _torch.int64)
     elif positions is not None:
         raise ValueError("positions need inv_freq")
     return B, T, d
@@ -730,7 +754,9 @@ def pdn_qk_norm_fwd(xq, xk, q, k, norm=PDN_NORM_L2, eps=1e-6, wq=None, wk=None, 
 
     norm is one of PDN_NORM_*, wq / wk its fp32 weights [d].  inv_freq
     (float64 [rot_dim / 2], see pdn_rope_freqs) turns the rotation on, at
-    positions (int64 [B,T]; None = 0, 1, .. in each sequence)."""
+    positions (int64 [B,T]; None = 0, 1, .. in each sequence).  Both may be
+    slices of longer tensors, as a generation loop's positions[:, t:t + 1] is: one
+    that begins off 16 bytes is copied first, a kernel more."""
     c = _Call(QkNormArgs, xq)
     if q.dim() != 4:
         raise ValueError("q and k must be [B,H,T,d]")

@@ -7,6 +7,8 @@
  * given stream of the current device, arguments validated before any launch,
  * its return codes, nothing allocated, kernels only (so that a call can be
  * captured into a HIP graph), and the caller's workspace where one is needed.
+ * Every pointer is 16-byte aligned (PDN_EINVAL otherwise), those to positions and
+ * inverse frequencies too: a slice of a longer buffer may have to be copied.
  */
 #ifndef PDN_LAYER_H
 #define PDN_LAYER_H

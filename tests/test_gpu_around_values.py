@@ -7,6 +7,7 @@ import pytest
 import around_ref as ref
 from around_ref import U
 from test_gpu_around import _close, _down, _nan, _pdn, _up
+from gpu_util import torch_mod
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +98,80 @@ def test_sigmoid_gate_gradient_far_from_zero():
     r = ref.norm_factor(x, 1, float(np.float32(1e-6)))[0]
     want = dy * x * r * w.astype(np.float64) / (1 + np.exp(-z64)) / (1 + np.exp(z64))
     _close("sigmoid dz", dz, want, np.abs(want) * (32 + 2 * np.abs(z64)) * U)
+
+
+@pytest.mark.parametrize("B,H,d,dtype", [(1, 4, 128, "bf16"), (1, 2, 64, "fp32")])
+def test_positions_sliced_from_a_longer_buffer(B, H, d, dtype):
+    """A generation loop takes positions[:, t:t + 1] of one buffer, a prefill in
+    parts positions[:, s:e]: such slices are contiguous and begin anywhere."""
+    pdn = _pdn()
+    torch = torch_mod()
+    gen = torch.Generator(device="cuda").manual_seed(403)
+    T = 9
+    x = torch.randn((B, T, 2, H, d), generator=gen, device="cuda").to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    g = torch.randn((2, B, H, T, d), generator=gen, device="cuda")
+    positions = 1000 + 7 * torch.arange(T, device="cuda")[None]
+    table = torch.tensor([0.0] + pdn.pdn_rope_freqs(d)[0], dtype=torch.float64, device="cuda")
+    w = torch.ones(d, device="cuda")
+
+    def run(s, e, inv, stream=None):
+        kw = dict(norm=pdn.PDN_NORM_RMS, inv_freq=inv, positions=positions[:, s:e], wq=w, wk=w)
+        xq, xk = x[:, s:e, 0], x[:, s:e, 1]
+        q, k = (torch.full((B, H, e - s, d), float("nan"), device="cuda", dtype=x.dtype) for _ in range(2))
+        dxq, dxk = (torch.full((B, e - s, H, d), float("nan"), device="cuda", dtype=x.dtype) for _ in range(2))
+        dq, dk = g[0][:, :, s:e].contiguous(), g[1][:, :, s:e].contiguous()
+        dwq, dwk = _nan((d,)), _nan((d,))
+        if stream is not None:
+            torch.cuda.synchronize()
+        pdn.pdn_qk_norm_fwd(xq, xk, q, k, stream=stream, **kw)
+        assert pdn.pdn_qk_norm_bwd_workspace_size(xq, xk, dq, dk, dxq, dxk, dwq=dwq, dwk=dwk, **kw) > 0
+        pdn.pdn_qk_norm_bwd(xq, xk, dq, dk, dxq, dxk, dwq=dwq, dwk=dwk, stream=stream, **kw)
+        if stream is not None:
+            junk = [torch.full((64,), -1, device="cuda", dtype=torch.int64) for _ in range(16)]  # nothing of the call's is free yet
+            torch.cuda.synchronize()
+            del junk
+        return q, k, dxq, dxk
+
+    inv = table[1:].clone()
+    whole = run(0, T, inv)
+    side = torch.cuda.Stream()
+    parts = [(t, t + 1) for t in range(T)] + [(1, 4), (3, T), (2, 8)]
+    for s, e in parts:
+        for iv, stream in ((inv, None), (table[1:], None), (inv, side), (inv, side.cuda_stream), (table[1:], 0)):
+            got = run(s, e, iv, stream)
+            for name, a, b in zip(("q", "k"), got, whole):
+                assert torch.equal(a, b[:, :, s:e]), (name, s, e)
+            for name, a, b in zip(("dxq", "dxk"), got[2:], whole[2:]):
+                assert torch.equal(a, b[:, s:e]), (name, s, e)
+
+
+def test_sliced_positions_captured():
+    """The call in a graph reads the slice at every replay."""
+    pdn = _pdn()
+    torch = torch_mod()
+    gen = torch.Generator(device="cuda").manual_seed(404)
+    H, d = 2, 64
+    x = torch.randn((1, 1, 2, H, d), generator=gen, device="cuda")
+    buf = torch.zeros((1, 4), dtype=torch.int64, device="cuda")
+    inv = torch.tensor(pdn.pdn_rope_freqs(d)[0], dtype=torch.float64, device="cuda")
+    q, k, wq, wk = (_nan((1, H, 1, d)) for _ in range(4))
+    call = lambda pos, a, b: pdn.pdn_qk_norm_fwd(x[:, :, 0], x[:, :, 1], a, b, inv_freq=inv, positions=pos)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(buf[:, 1:2], q, k)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(buf[:, 1:2], q, k)
+    for pos in (0, 5, 123456, 7):
+        buf.fill_(-3)
+        buf[0, 1] = pos
+        q.fill_(float("nan"))
+        k.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        call(torch.full((1, 1), pos, dtype=torch.int64, device="cuda"), wq, wk)
+        assert torch.equal(q, wq) and torch.equal(k, wk), pos
