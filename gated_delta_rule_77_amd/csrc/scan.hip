@@ -434,8 +434,10 @@ ScanParams params(const pdn_scan_args& a) {
     return p;
 }
 
+bool has_carriers(long columns, long tiles) { return tiles > 1 && columns <= kCarried; }
+
 void set_chain(ScanParams& p, char* at) {
-    p.chain.carrier = p.chain.tiles > 1 && p.columns <= kCarried;
+    p.chain.carrier = has_carriers(p.columns, p.chain.tiles);
     p.chain.counters = reinterpret_cast<unsigned*>(at);
     p.chain.agg = reinterpret_cast<u64*>(at + sizeof(unsigned) * kCounterStep * p.columns);
     p.chain.inc = p.chain.agg + static_cast<long>(p.columns) * p.chain.tiles * kCols;
@@ -500,7 +502,8 @@ hipError_t copy_state(float* dst, const float* src, const pdn_scan_args& a, hipS
 
 bool scan_fits(const pdn_scan_args& a) {
     static_assert(kBwdR <= fwd_r(false) && kBwdR <= fwd_r(true), "the backward has the most tiles");
-    return a.B * strips(a) * (tiles(a, kBwdTile) + 1) <= kMaxGridThreads / (64 * kWaves);
+    const long columns = a.B * strips(a), n = tiles(a, kBwdTile);
+    return columns * (n + has_carriers(columns, n)) <= kMaxGridThreads / (64 * kWaves);
 }
 
 size_t scan_fwd_workspace_bytes(const pdn_scan_args& a) { return chain_bytes(a, fwd_tile(a)); }

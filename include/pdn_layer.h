@@ -30,8 +30,8 @@ int pdn_layer_version(void);
  * other (PDN_EINVAL).  No output may overlap an input, another output or the
  * workspace, except where two arguments may be one buffer.
  * PDN_EUNSUPPORTED where B * T or B * D passes 2^30, or a launch's 2^32 threads
- * do not suffice (B * T past some 10^8, a scan past some 10^11 channels' tokens,
- * channels rounded up to 128). */
+ * do not suffice (B * T past some 10^8; a scan of 2^23 or more tiles of 128
+ * channels by PDN_SCAN_MARK tokens, B ceil(D / 128) ceil(T / PDN_SCAN_MARK)). */
 
 /* Norm of a head's row x[0..d): r = (c sum x^2 + eps)^(-1/2), with c = 1/d
  * (RMS) or 1 (L2, which the delta rule's keys are commonly given). */

@@ -6,7 +6,7 @@ import pytest
 
 import around_ref as ref
 from around_ref import U
-from test_gpu_around import _close, _down, _nan, _pdn, _up
+from test_gpu_around import TINY, _close, _down, _nan, _pdn, _up
 from gpu_util import torch_mod
 
 pytestmark = pytest.mark.gpu
@@ -175,3 +175,28 @@ def test_sliced_positions_captured():
         torch.cuda.synchronize()
         call(torch.full((1, 1), pos, dtype=torch.int64, device="cuda"), wq, wk)
         assert torch.equal(q, wq) and torch.equal(k, wk), pos
+
+
+@pytest.mark.parametrize("B", [5_000_000, (1 << 23) - 1])
+def test_scan_of_as_many_columns_as_a_launch_holds(B):
+    """One token of very many sequences: a workgroup each, and no other."""
+    pdn = _pdn()
+    torch = torch_mod()
+    gen = torch.Generator(device="cuda").manual_seed(406)
+    x, dh = (torch.randn((B, 1, 8), generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2))
+    la = -torch.rand((B, 1, 8), generator=gen, device="cuda")
+    h0, dhT = (torch.randn((B, 8), generator=gen, device="cuda") for _ in range(2))
+    h, hT = torch.full_like(x, float("nan")), torch.full_like(h0, float("nan"))
+    print("[around] scan of %d columns" % B, flush=True)
+    pdn.pdn_scan_fwd(x, la, h, h0=h0, hT=hT, gain=pdn.PDN_GAIN_NORM)
+    step_h, step = torch.empty_like(x[:, 0]), torch.empty_like(h0)
+    pdn.pdn_scan_step(x[:, 0], la[:, 0], step_h, h0, step, gain=pdn.PDN_GAIN_NORM)
+    assert torch.equal(hT, step) and torch.equal(h[:, 0], step_h)
+    dx, dla, dh0 = torch.full_like(x, float("nan")), torch.full_like(la, float("nan")), torch.full_like(h0, float("nan"))
+    pdn.pdn_scan_bwd(x, la, dh, dx, dla, h0=h0, dhT=dhT, dh0=dh0)
+    assert torch.equal(dx[:, 0], (dh[:, 0].float() + dhT).to(torch.bfloat16))     # one addition, one rounding
+    # dlog_a = h0 dh0.  dlog_a: a h0, dh + dhT and their product are rounded, 3 U |a h0 (dh + dhT)|; dh0:
+    # a dh is rounded before dhT joins it, U |a dh| whatever the sum cancels to, then their sum; a <= 1
+    h0, dh, dhT = h0.double(), dh[:, 0].double(), dhT.double()
+    room = U * h0.abs() * (5 * (dh + dhT).abs() + 2 * dh.abs()) + TINY
+    assert bool(((dla[:, 0].double() - dh0.double() * h0).abs() <= room).all())
