@@ -6,7 +6,7 @@ import pytest
 
 import around_ref as ref
 from around_ref import U
-from test_gpu_around import TINY, _close, _down, _nan, _pdn, _up
+from test_gpu_around import TINY, _close, _down, _nan, _pdn, _scan_case, _up
 from gpu_util import torch_mod
 
 pytestmark = pytest.mark.gpu
@@ -200,3 +200,31 @@ def test_scan_of_as_many_columns_as_a_launch_holds(B):
     h0, dh, dhT = h0.double(), dh[:, 0].double(), dhT.double()
     room = U * h0.abs() * (5 * (dh + dhT).abs() + 2 * dh.abs()) + TINY
     assert bool(((dla[:, 0].double() - dh0.double() * h0).abs() <= room).all())
+
+
+@pytest.mark.parametrize("D,lengths", [(72, [1, 255, 3, 600, 128]), (1160, [192, 96, 5, 700]), (8, [97, 1, 1, 400])])
+def test_packed_row_against_its_sequences_alone(D, lengths):
+    """A packed row's states are those of its sequences run one by one, each
+    within the bounds of the definition: forward and backward."""
+    pdn = _pdn()
+    T = sum(lengths)
+    x, la, _, dh, _ = _scan_case((1, T, D, "fp32", "fp32", 2, False, False), 405)
+    starts = np.cumsum([0] + lengths[:-1])
+    la[:, starts] = -np.inf
+    f64 = lambda v: v.astype(np.float64)
+    names = ("h", "dx", "dlog_a")
+
+    def run(s, e):
+        xd, lad = _up(x[:, s:e]), _up(la[:, s:e])
+        h, dx, dla = (_nan((1, e - s, D)) for _ in names)
+        pdn.pdn_scan_fwd(xd, lad, h, gain=2)
+        pdn.pdn_scan_bwd(xd, lad, _up(dh[:, s:e]), dx, dla, gain=2)
+        return h, dx, dla
+
+    packed = run(0, T)
+    bounds = (ref.scan_fwd(f64(x), f64(la), None, 2)[1],) + tuple(
+        b for _, b in ref.scan_bwd(f64(x), f64(la), None, f64(dh), None, 2)[:2])
+    for s, n in zip(starts, lengths):
+        for name, a, b, bound in zip(names, run(s, s + n), packed, bounds):
+            # each is off by its bound and its own rounding at most
+            _close("packed " + name, b[:, s:s + n], _down(a), 2 * bound[:, s:s + n] + U * (np.abs(_down(a)) + bound[:, s:s + n]))
