@@ -16,14 +16,15 @@
 //   out_i = r (x_i wc_i + x_partner(i) ws_i).
 //
 // Measured on an MI355X, whose large copies reach 5.3 TB/s (counters: each
-// kernel moves within 3% of the bytes it cannot do without):
+// of these moves within 3% of the bytes it cannot do without):
 //   q/k norm      B4 T8192 H16 d128 bf16, no rotation      82 us   6.5 TB/s (*)
 //                 B1 T65536 Hq16 Hk4 H16, half rotated    165 us   5.3 TB/s
-//   its backward  B2 T8192 H32, all rotated, weights      206 us   5.2 TB/s
+//   its backward  B2 T8192 H32, all rotated, weights      208 us   5.2 TB/s
 //   output norm   B4 T8192 H16 dv128, fp32 o, bf16 z, y   100 us   5.4 TB/s
 //   its backward  B2 T8192 H32                            186 us   5.1 TB/s
 // (*) over the copy's rate: part of the 268 MB written stays in the 256 MB
-// cache from one call to the next, where q and k are overwritten in place.
+// cache from one call to the next, where q and k are overwritten in place (109 us
+// into other memory each call).
 #include "layer.h"
 #include "rows.h"
 
@@ -128,7 +129,7 @@ __device__ __forceinline__ void partners(const float (&x)[8], int lane, bool rot
 
 // A workgroup takes SLOTS tokens and (unless tokens are few) all their heads:
 // splitting the heads costs the angles once more for each part (B1 T65536,
-// half rotated: 227 and 299 us in 4 and 8 parts, where one took 199).  The next heads' loads
+// half rotated: 169, 193 and 251 us in 2, 4 and 8 parts, one 165).  The next heads' loads
 // are issued ahead of the present ones' arithmetic, the first ones' ahead of the
 // angles.
 template <bool BF16, int D, int ROPE>
@@ -241,7 +242,8 @@ __device__ __forceinline__ void sum_slots(const float (&acc)[8], float* red, flo
 // weight gradients add up in registers over all its tokens and heads; one
 // partial sum per workgroup goes to the workspace (at most kBwdFill of them: the
 // kernel that adds them up takes 6 us).  Its loads stay behind the angles: ahead of
-// them they cost the registers of a fourth wave (205 -> 212 us).  They go through
+// them they cost the registers of a fourth wave (205 -> 212 us, interleaved; the
+// half layout takes 131 to 133 registers and has three, 225 us where that takes 217).  They go through
 // the caches, where a recurrence's backward has just left some of what they read:
 // the same at B2 T8192 H32, 32 us instead of 40 for 6725 tokens of 12 fp32 heads.
 template <bool BF16, int D, int ROPE>

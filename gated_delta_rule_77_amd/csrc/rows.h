@@ -13,8 +13,10 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 // Eight elements as they lie in memory: 16 bytes of bf16, 32 of fp32.
 //
 // `stream` loads what a call reads once without keeping it in the caches, which
-// then hold more of what the call writes, for the next call to read: q/k norm of
-// B4 T8192 H16 d128 111 -> 85 us, gated output norm of the same 106 -> 100 us.
+// then hold more of what the call writes, for the next call to read or to write
+// over: q/k norm of B4 T8192 H16 d128 113 -> 82 us and gated output norm of the
+// same 106 -> 100 us with the outputs in place, 112 -> 109 and 106 -> 105 us into
+// other memory each call.
 template <bool BF16>
 struct Raw8;
 

@@ -17,13 +17,13 @@
 //
 // the tiles hand it on along their column as scan_chain.h says.
 //
-// Measured on an MI355X, whose large copies reach 5.3 TB/s (counters: 1.03 to
-// 1.06 times the bytes that the call cannot do without, the published words
-// among them), with the reset of the words (6 us) before it:
+// Measured on an MI355X, whose large copies reach 5.3 TB/s (counters: 1.02 to
+// 1.04 times the bytes that the call cannot do without, the published words
+// among them), after the reset of the words (6 us):
 //   forward   B4 T8192 D2048, bf16, fp32 decays       98 us   5.5 TB/s
-//             B1 T65536 D2048, bf16                  155 us   5.2 TB/s
-//             B2 T8192 D4096, bf16, normed gain       87 us   4.7 TB/s
-//   backward  of the last, kept states given         140 us   4.8 TB/s
+//             B1 T65536 D2048, bf16                  160 us   5.0 TB/s
+//             B2 T8192 D4096, bf16, normed gain       86 us   4.7 TB/s
+//   backward  of the last, kept states given         142 us   4.7 TB/s
 // A tile lives for 8 to 11 us, of which it loads for 3 to 4, waits for its state
 // for 2 to 5 and stores for 2; two workgroups to a compute unit cover most of
 // that, and what is left is the first round's fill and the last one's drain.
@@ -40,7 +40,8 @@ namespace {
 
 constexpr int kThreads = 256;  // of the step, reset and copy kernels
 // Waves of a workgroup and tokens of a wave.  Both directions fit 128 registers
-// (two workgroups to a compute unit).  Measured at B2 T8192 D4096 bf16, forward
+// (two workgroups to a compute unit), but for the fp32 backward with the
+// complement gain, which spills 20 bytes a lane.  Measured at B2 T8192 D4096 bf16, forward
 // 8 x 16 93 us, 16 x 16 101, 4 x 32 104, 8 x 8 108; backward 8 x 12 144, 4 x 16
 // 150, 16 x 8 154, 8 x 8 157, 8 x 16 (one workgroup to a compute unit) 177.
 // Forward in bf16 24 tokens: 1% slower there, 161 us instead of 176 over 65536 x

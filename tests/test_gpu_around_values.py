@@ -1,6 +1,7 @@
-"""GPU checks of the operators around the recurrence at values and views that the
-other suites pass over: decays of exactly one, infinities beside a rotation,
-gates far from zero, slices of a longer buffer of positions."""
+"""GPU checks of the operators around the recurrence at values, views and sizes that
+the other suites pass over: decays of exactly one, infinities beside a rotation,
+gates far from zero, slices of a longer buffer of positions, as many columns as a
+launch holds, packed rows against their sequences alone."""
 import numpy as np
 import pytest
 
