@@ -2,7 +2,7 @@
 
 This layer only marshals arguments: it checks tensor placement, dtypes and
 shapes, passes raw device pointers and the current HIP stream to the C ABI
-(include/pdn.h, include/pdn_layer.h), and raises on a non-zero return code.  Every step of the
+(include/pdn.h, include/pdn_layer.h, include/pdn_block.h), and raises on a non-zero return code.  Every step of the
 computation runs in the HIP kernels of libpdn.so; there is no fallback, and
 loading fails loudly when the library is missing.
 
@@ -22,6 +22,11 @@ and the operators around the recurrence:
     pdn_scan_fwd / _bwd / _step(...)   the gated recurrence with a vector state, [B,T,D]
     pdn_scan_marks(T)                  kept states of a scan over T tokens
     pdn_rope_freqs(...)                inverse frequencies, scaled for long contexts
+and what a stack with attention layers needs besides:
+    pdn_add_norm_fwd / _bwd(...)       dropout, residual and norm between two sublayers, y in 8 bits too
+    pdn_attn_fwd / _bwd(...)           causal softmax attention over [B,H,T,d]
+    pdn_cache_append(...)              new tokens' keys and values into a paged cache
+    pdn_attn_paged(...)                attention of new tokens over that cache
 with pdn_*_workspace_size(...) for those that take scratch.
 """
 from __future__ import annotations
@@ -36,10 +41,11 @@ LIB_PATH = os.path.join(_HERE, "libpdn.so")
 # The argument structs below mirror this version of include/pdn.h.
 PDN_ABI_VERSION = 5
 PDN_LAYER_VERSION = 1   # and this one of include/pdn_layer.h
+PDN_BLOCK_VERSION = 1   # and of include/pdn_block.h
 
 PDN_OK, PDN_EINVAL, PDN_EUNSUPPORTED, PDN_EWORKSPACE, PDN_EHIP, PDN_ESCRATCH = 0, -1, -2, -3, -4, -5
 PDN_NOALLOC_SCRATCH_BYTES = 256 << 20   # static scratch of pdn_chunk_fwd_noalloc
-PDN_F32, PDN_BF16 = 0, 1
+PDN_F32, PDN_BF16, PDN_E4M3 = 0, 1, 2
 PDN_ALPHA_NONE, PDN_ALPHA_SCALAR, PDN_ALPHA_VEC = 0, 1, 2
 PDN_GATE_SCALAR, PDN_GATE_VEC, PDN_GAMMA_SAME_AS_BETA = 1, 2, 3
 PDN_KEY_SYMMETRIC, PDN_KEY_ERASE_GATE, PDN_KEY_WRITE_GATE = 0, 1, 2
@@ -156,6 +162,62 @@ class ScanStepArgs(ctypes.Structure):
                 ("h_prev", _P), ("h_next", _P), ("h", _P), ("h_sb", _L)]
 
 
+class AddNormArgs(ctypes.Structure):
+    """Mirror of ``pdn_add_norm_args``."""
+    _fields_ = [("B", _I), ("T", _I), ("D", _I), ("dtype", _I), ("s_dtype", _I), ("y_dtype", _I), ("group", _I),
+                ("eps", _F), ("drop_p", _F), ("seed", _P), ("w", _P),
+                ("x", _P), ("x_sb", _L), ("x_st", _L), ("res", _P), ("res_sb", _L), ("res_st", _L),
+                ("s", _P), ("s_sb", _L), ("s_st", _L), ("y", _P), ("y_sb", _L), ("y_st", _L), ("y_scale", _P)]
+
+
+class AddNormBwdArgs(ctypes.Structure):
+    """Mirror of ``pdn_add_norm_bwd_args``."""
+    _fields_ = [("B", _I), ("T", _I), ("D", _I), ("dtype", _I), ("s_dtype", _I), ("y_dtype", _I),
+                ("eps", _F), ("drop_p", _F), ("seed", _P), ("w", _P),
+                ("s", _P), ("s_sb", _L), ("s_st", _L), ("dy", _P), ("dy_sb", _L), ("dy_st", _L),
+                ("ds", _P), ("ds_sb", _L), ("ds_st", _L), ("dres", _P), ("dres_sb", _L), ("dres_st", _L),
+                ("dx", _P), ("dx_sb", _L), ("dx_st", _L), ("dw", _P),
+                ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class AttnArgs(ctypes.Structure):
+    """Mirror of ``pdn_attn_args``."""
+    _fields_ = [("B", _I), ("H", _I), ("Hk", _I), ("Tq", _I), ("Tk", _I), ("d", _I), ("dtype", _I), ("o_dtype", _I),
+                ("window", _I), ("scale", _F), ("first", _P),
+                ("q", _P), ("q_sb", _L), ("q_sh", _L), ("q_st", _L), ("k", _P), ("k_sb", _L), ("k_sh", _L), ("k_st", _L),
+                ("v", _P), ("v_sb", _L), ("v_sh", _L), ("v_st", _L), ("o", _P), ("o_sb", _L), ("o_sh", _L), ("o_st", _L),
+                ("lse", _P), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class AttnBwdArgs(ctypes.Structure):
+    """Mirror of ``pdn_attn_bwd_args``."""
+    _fields_ = [("fwd", AttnArgs), ("g_dtype", _I), ("d_o", _P), ("do_sb", _L), ("do_sh", _L), ("do_st", _L),
+                ("dq", _P), ("dq_sb", _L), ("dq_sh", _L), ("dq_st", _L), ("dk", _P), ("dk_sb", _L), ("dk_sh", _L), ("dk_st", _L),
+                ("dv", _P), ("dv_sb", _L), ("dv_sh", _L), ("dv_st", _L),
+                ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class Cache(ctypes.Structure):
+    """Mirror of ``pdn_cache``."""
+    _fields_ = [("B", _I), ("N", _I), ("max_new", _I), ("Hk", _I), ("d", _I), ("dtype", _I),
+                ("pages", _I), ("page_size", _I), ("table_width", _I),
+                ("k_pages", _P), ("k_sp", _L), ("k_st", _L), ("k_sh", _L),
+                ("v_pages", _P), ("v_sp", _L), ("v_st", _L), ("v_sh", _L),
+                ("table", _P), ("lens", _P), ("starts", _P)]
+
+
+class CacheAppendArgs(ctypes.Structure):
+    """Mirror of ``pdn_cache_append_args``."""
+    _fields_ = [("cache", Cache), ("k", _P), ("k_sn", _L), ("k_sh", _L), ("v", _P), ("v_sn", _L), ("v_sh", _L)]
+
+
+class AttnPagedArgs(ctypes.Structure):
+    """Mirror of ``pdn_attn_paged_args``."""
+    _fields_ = [("cache", Cache), ("H", _I), ("o_dtype", _I), ("window", _I), ("scale", _F),
+                ("q", _P), ("q_sn", _L), ("q_sh", _L), ("o", _P), ("o_sn", _L), ("o_sh", _L), ("lse", _P),
+                ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
 # the operators around the recurrence: their argument structs, and which of
 # them have a workspace size to ask for
 _AROUND = {"pdn_qk_norm_fwd": (QkNormArgs, "pdn_qk_norm_check", None),
@@ -166,6 +228,15 @@ _AROUND = {"pdn_qk_norm_fwd": (QkNormArgs, "pdn_qk_norm_check", None),
            "pdn_scan_bwd": (ScanBwdArgs, "pdn_scan_bwd_check", "pdn_scan_bwd_workspace_size"),
            "pdn_scan_step": (ScanStepArgs, "pdn_scan_step_check", None)}
 
+# and those of include/pdn_block.h
+_BLOCK = {"pdn_add_norm_fwd": (AddNormArgs, "pdn_add_norm_check", None),
+          "pdn_add_norm_bwd": (AddNormBwdArgs, "pdn_add_norm_bwd_check", "pdn_add_norm_bwd_workspace_size"),
+          "pdn_attn_fwd": (AttnArgs, "pdn_attn_check", "pdn_attn_fwd_workspace_size"),
+          "pdn_attn_bwd": (AttnBwdArgs, "pdn_attn_bwd_check", "pdn_attn_bwd_workspace_size"),
+          "pdn_cache_append": (CacheAppendArgs, "pdn_cache_append_check", None),
+          "pdn_attn_paged": (AttnPagedArgs, "pdn_attn_paged_check", "pdn_attn_paged_workspace_size")}
+_SIZES = {name: size for calls in (_AROUND, _BLOCK) for name, (_, _, size) in calls.items()}
+
 EXPORTED = ("pdn_abi_version", "pdn_strerror", "pdn_chunk_fwd_workspace_size",
             "pdn_chunk_fwd_check", "pdn_chunk_fwd", "pdn_chunk_fwd_noalloc", "pdn_decode_check",
             "pdn_decode_step", "pdn_chunk_bwd_workspace_size", "pdn_chunk_bwd_check",
@@ -173,6 +244,9 @@ EXPORTED = ("pdn_abi_version", "pdn_strerror", "pdn_chunk_fwd_workspace_size",
 # include/pdn_layer.h
 EXPORTED_LAYER = ("pdn_layer_version", "pdn_rope_freqs", "pdn_scan_marks",
                   *(n for call, (_, check, size) in _AROUND.items() for n in (call, check, size) if n))
+
+# include/pdn_block.h
+EXPORTED_BLOCK = ("pdn_block_version", *(n for call, (_, check, size) in _BLOCK.items() for n in (call, check, size) if n))
 
 _lib = None
 _lock = threading.Lock()
@@ -230,7 +304,10 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         if not hasattr(lib, "pdn_layer_version") or lib.pdn_layer_version() != PDN_LAYER_VERSION:
             raise RuntimeError("%s is of another version of include/pdn_layer.h than this binding (%d): "
                                "rebuild it with `python -m gated_delta_rule_77_amd.build`" % (p, PDN_LAYER_VERSION))
-        for name, (struct, check, size) in _AROUND.items():
+        if not hasattr(lib, "pdn_block_version") or lib.pdn_block_version() != PDN_BLOCK_VERSION:
+            raise RuntimeError("%s is of another version of include/pdn_block.h than this binding (%d): "
+                               "rebuild it with `python -m gated_delta_rule_77_amd.build`" % (p, PDN_BLOCK_VERSION))
+        for name, (struct, check, size) in (*_AROUND.items(), *_BLOCK.items()):
             getattr(lib, name).argtypes = [ctypes.POINTER(struct), _P]
             getattr(lib, check).argtypes = [ctypes.POINTER(struct)]
             if size:
@@ -685,7 +762,7 @@ class _Call:
         if self.index != _torch.cuda.current_device():
             with _torch.cuda.device(self.index):
                 return self.launch(name, stream, workspace)
-        a, size = self.a, _AROUND[name][2]
+        a, size = self.a, _SIZES[name]
         lib = _lib or load_library()
         if self.moved:
             # a kernel (a sum with zero), as all that a captured call records
@@ -955,3 +1032,225 @@ def pdn_rope_freqs(rot_dim, base=10000.0, scaling=PDN_ROPE_PLAIN, factor=1.0, or
     if rc != PDN_OK:
         raise PdnError(rc, "pdn_rope_freqs")
     return list(freqs), float(scale.value)
+
+
+# ---------------------------------------------------------------------------
+# what a stack with attention layers needs besides the recurrence
+# ---------------------------------------------------------------------------
+
+def _rows3(c, a, field, t, name, shape, dtype):
+    """A [B,T,D] tensor and its strides (None: as they are)."""
+    if t is not None:
+        setattr(a, field, c.rows(t, name, shape, dtype))
+        sb, st, _ = t.stride()
+        setattr(a, field + "_sb", sb)
+        setattr(a, field + "_st", st)
+
+
+def _seam(c, x, w, eps, drop_p, seed):
+    if x.dim() != 3:
+        raise ValueError("the rows must be [B,T,D]")
+    a, (B, T, D) = c.a, x.shape
+    a.B, a.T, a.D, a.eps, a.drop_p = B, T, D, eps, drop_p
+    a.w = c.plain(w, "w", (D,), _torch.float32)
+    a.seed = c.plain(seed, "seed", (2,), _torch.int64)
+    return B, T, D
+
+
+def pdn_add_norm_fwd(x, y, res=None, s=None, w=None, eps=1e-6, drop_p=0.0, seed=None, y_scale=None, stream=None) -> None:
+    """The seam between two sublayers: s = res + dropout(x), y = its RMS norm times
+    w (fp32 [D]), over x, res, s, y [B,T,D] (views are fine; s may be res).
+
+    s, in res's type, is what the norm and the backward read; without res and
+    dropout there is none: y is the norm of x.  y is fp32, bf16 or float8_e4m3fn,
+    which takes y_scale (fp32 [B,T], a scale a row, or [B,T,D / 32, 64 or 128], one
+    for each group of channels): y * y_scale is the value.  drop_p drops elements of x by
+    seed (int64 [2] in device memory: a key and a number of the call, such as the
+    layer's and step's), the same in pdn_add_norm_bwd; no mask is kept."""
+    c = _Call(AddNormArgs, x)
+    a = c.a
+    B, T, D = shape = _seam(c, x, w, eps, drop_p, seed)
+    s_dtype = x.dtype if res is None and s is None else (res if res is not None else s).dtype
+    a.dtype, a.s_dtype = _dtype_of(x, "x"), _CODES.get(s_dtype, -1)
+    _rows3(c, a, "x", x, "x", shape, x.dtype)
+    _rows3(c, a, "res", res, "res", shape, s_dtype)
+    _rows3(c, a, "s", s, "s", shape, s_dtype)
+    _rows3(c, a, "y", y, "y", shape, y.dtype)
+    if y.dtype == _torch.float8_e4m3fn:
+        a.y_dtype = PDN_E4M3
+        if y_scale is None:
+            raise ValueError("y_scale is required for y in 8 bits")
+        groups = y_scale.shape[2] if y_scale.dim() == 3 else 1
+        if groups < 1 or D % groups:
+            raise ValueError("y_scale must be [B,T] or [B,T,groups], groups a divisor of D")
+        a.group = D // groups if groups > 1 else 0
+        a.y_scale = c.plain(y_scale, "y_scale", (B, T) if y_scale.dim() == 2 else (B, T, groups), _torch.float32)
+    else:
+        a.y_dtype = _dtype_of(y, "y")
+        if y_scale is not None:
+            raise ValueError("y_scale goes with y in 8 bits")
+    c.launch("pdn_add_norm_fwd", stream)
+
+
+def _add_norm_bwd(s, dy, dres, ds, dx, w, dw, eps, drop_p, seed):
+    c = _Call(AddNormBwdArgs, s)
+    a, shape = c.a, _seam(c, s, w, eps, drop_p, seed)
+    a.dtype = a.s_dtype = _dtype_of(s, "s")
+    a.y_dtype = _dtype_of(dy, "dy")
+    if dx is not None:
+        a.dtype = _dtype_of(dx, "dx")
+        _rows3(c, a, "dx", dx, "dx", shape, dx.dtype)
+    _rows3(c, a, "s", s, "s", shape, s.dtype)
+    _rows3(c, a, "dy", dy, "dy", shape, dy.dtype)
+    _rows3(c, a, "ds", ds, "ds", shape, s.dtype)
+    _rows3(c, a, "dres", dres, "dres", shape, s.dtype)
+    a.dw = c.plain(dw, "dw", shape[-1:], _torch.float32)
+    return c
+
+
+def pdn_add_norm_bwd_workspace_size(s, dy, dres, ds=None, dx=None, w=None, dw=None, eps=1e-6, drop_p=0.0, seed=None) -> int:
+    return _add_norm_bwd(s, dy, dres, ds, dx, w, dw, eps, drop_p, seed).size("pdn_add_norm_bwd_workspace_size")
+
+
+def pdn_add_norm_bwd(s, dy, dres, ds=None, dx=None, w=None, dw=None, eps=1e-6, drop_p=0.0, seed=None, workspace=None,
+                     stream=None) -> None:
+    """Backward of pdn_add_norm_fwd: from dy and ds (what reaches s otherwise; None =
+    zeros), with s as the forward left it (x where it had none), to dres (s's type;
+    may be ds), dx (dropped as x was; None = not written) and dw (fp32 [D], given
+    exactly when w is)."""
+    _add_norm_bwd(s, dy, dres, ds, dx, w, dw, eps, drop_p, seed).launch("pdn_add_norm_bwd", stream, workspace)
+
+
+def _rows4(c, a, field, t, name, shape, dtype):
+    """A [B,heads,T,d] tensor and its strides."""
+    setattr(a, "d_o" if field == "do" else field, c.rows(t, name, shape, dtype))
+    sb, sh, st, _ = t.stride()
+    setattr(a, field + "_sb", sb)
+    setattr(a, field + "_sh", sh)
+    setattr(a, field + "_st", st)
+
+
+def _attn(c, a, q, k, v, o, lse, scale, window, first):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B,H,Tq,d], k and v [B,Hk,Tk,d]")
+    (B, H, Tq, d), (_, Hk, Tk, _) = q.shape, k.shape
+    a.B, a.H, a.Hk, a.Tq, a.Tk, a.d = B, H, Hk, Tq, Tk, d
+    a.dtype, a.o_dtype, a.window = _dtype_of(q, "q"), _dtype_of(o, "o"), window
+    a.scale = d ** -0.5 if scale is None else scale
+    for name, t, shape in (("q", q, (B, H, Tq, d)), ("k", k, (B, Hk, Tk, d)), ("v", v, (B, Hk, Tk, d))):
+        _rows4(c, a, name, t, name, shape, q.dtype)
+    _rows4(c, a, "o", o, "o", (B, H, Tq, d), o.dtype)
+    a.lse = c.plain(lse, "lse", (B, H, Tq), _torch.float32)
+    a.first = c.plain(first, "first", (B, Tq), _torch.int32)
+
+
+def _attn_fwd(q, k, v, o, lse, scale, window, first):
+    c = _Call(AttnArgs, q)
+    _attn(c, c.a, q, k, v, o, lse, scale, window, first)
+    return c
+
+
+def pdn_attn_fwd_workspace_size(q, k, v, o, lse=None, scale=None, window=0, first=None) -> int:
+    return _attn_fwd(q, k, v, o, lse, scale, window, first).size("pdn_attn_fwd_workspace_size")
+
+
+def pdn_attn_fwd(q, k, v, o, lse=None, scale=None, window=0, first=None, workspace=None, stream=None) -> None:
+    """Causal softmax attention: q, o [B,H,Tq,d], k, v [B,Hk,Tk,d] (views are fine:
+    a projection's rows transposed, every n-th of pdn_qk_norm_fwd's heads), the
+    queries being the last Tq of Tk tokens and head h reading key head h / (H / Hk).
+
+    scale: None = d^-0.5 (1.0 where q carries it already).  window: the keys that a
+    query sees at most, its own the last (0 = all).  first: int32 [B,Tq], the first
+    key that each query may see (its sequence's start in a packed row; Tk or more:
+    nothing).  lse: fp32 [B,H,Tq], which the backward needs."""
+    _attn_fwd(q, k, v, o, lse, scale, window, first).launch("pdn_attn_fwd", stream, workspace)
+
+
+def _attn_bwd(q, k, v, o, do, lse, dq, dk, dv, scale, window, first):
+    c = _Call(AttnBwdArgs, q)
+    a = c.a
+    if lse is None:
+        raise ValueError("lse is required")
+    _attn(c, a.fwd, q, k, v, o, lse, scale, window, first)
+    a.g_dtype = _dtype_of(dq, "dq")
+    _rows4(c, a, "do", do, "do", o.shape, o.dtype)
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        _rows4(c, a, name, t, name, like.shape, dq.dtype)
+    return c
+
+
+def pdn_attn_bwd_workspace_size(q, k, v, o, do, lse, dq, dk, dv, scale=None, window=0, first=None) -> int:
+    return _attn_bwd(q, k, v, o, do, lse, dq, dk, dv, scale, window, first).size("pdn_attn_bwd_workspace_size")
+
+
+def pdn_attn_bwd(q, k, v, o, do, lse, dq, dk, dv, scale=None, window=0, first=None, workspace=None, stream=None) -> None:
+    """Backward of pdn_attn_fwd: from do (o's type) to dq, dk, dv (shapes of q, k, v;
+    bf16 or fp32, views are fine), with o and lse as the forward wrote them."""
+    _attn_bwd(q, k, v, o, do, lse, dq, dk, dv, scale, window, first).launch("pdn_attn_bwd", stream, workspace)
+
+
+def _cache(c, m, N, k_pages, v_pages, table, lens, starts, max_new):
+    if k_pages.dim() != 4 or table.dim() != 2:
+        raise ValueError("k_pages and v_pages must be [pages,page_size,Hk,d], table [B,pages of a sequence]")
+    shape, B = k_pages.shape, table.shape[0]
+    m.pages, m.page_size, m.Hk, m.d = shape
+    m.B, m.N, m.table_width, m.dtype = B, N, table.shape[1], _dtype_of(k_pages, "k_pages")
+    m.k_pages, m.v_pages = c.rows(k_pages, "k_pages", shape, k_pages.dtype), c.rows(v_pages, "v_pages", shape, k_pages.dtype)
+    m.k_sp, m.k_st, m.k_sh, _ = k_pages.stride()
+    m.v_sp, m.v_st, m.v_sh, _ = v_pages.stride()
+    m.table = c.plain(table, "table", (B, m.table_width), _torch.int32)
+    m.lens = c.plain(lens, "lens", (B,), _torch.int32)
+    m.starts = c.plain(starts, "starts", (B + 1,), _torch.int32)
+    if starts is None and B > 0 and N % B:
+        raise ValueError("without starts every sequence has the same number of new tokens: %d rows, %d sequences" % (N, B))
+    m.max_new = max_new if max_new is not None else N if starts is not None or B == 0 else N // B
+
+
+def pdn_cache_append(k, v, k_pages, v_pages, table, lens, starts=None, max_new=None, stream=None) -> None:
+    """New tokens' keys and values into a paged cache: k, v [N,Hk,d] (views are fine)
+    to k_pages, v_pages [pages,page_size,Hk,d], sequence b's rows starts[b] ..
+    starts[b + 1] - 1 (int32 [B + 1]; None: N / B each) to its last tokens of lens[b]
+    (int32 [B], the new ones included) by table (int32 [B,width], its pages in
+    order).  max_new: at least the most new tokens of any sequence (None: N / B, or N
+    with starts)."""
+    c = _Call(CacheAppendArgs, k)
+    if k.dim() != 3:
+        raise ValueError("k and v must be [N,Hk,d]")
+    a, N = c.a, k.shape[0]
+    _cache(c, a.cache, N, k_pages, v_pages, table, lens, starts, max_new)
+    shape = (N, a.cache.Hk, a.cache.d)
+    a.k, a.v = c.rows(k, "k", shape, k_pages.dtype), c.rows(v, "v", shape, k_pages.dtype)
+    a.k_sn, a.k_sh, _ = k.stride()
+    a.v_sn, a.v_sh, _ = v.stride()
+    c.launch("pdn_cache_append", stream)
+
+
+def _attn_paged(q, o, k_pages, v_pages, table, lens, starts, max_new, scale, window, lse):
+    c = _Call(AttnPagedArgs, q)
+    if q.dim() != 3:
+        raise ValueError("q and o must be [N,H,d]")
+    a, (N, H, d) = c.a, q.shape
+    _cache(c, a.cache, N, k_pages, v_pages, table, lens, starts, max_new)
+    if d != a.cache.d:
+        raise ValueError("q's heads hold %d channels, the cache's %d" % (d, a.cache.d))
+    a.H, a.o_dtype, a.window = H, _dtype_of(o, "o"), window
+    a.scale = d ** -0.5 if scale is None else scale
+    a.q, a.o = c.rows(q, "q", (N, H, d), k_pages.dtype), c.rows(o, "o", (N, H, d), o.dtype)
+    a.q_sn, a.q_sh, _ = q.stride()
+    a.o_sn, a.o_sh, _ = o.stride()
+    a.lse = c.plain(lse, "lse", (N, H), _torch.float32)
+    return c
+
+
+def pdn_attn_paged_workspace_size(q, o, k_pages, v_pages, table, lens, starts=None, max_new=None, scale=None, window=0,
+                                  lse=None) -> int:
+    return _attn_paged(q, o, k_pages, v_pages, table, lens, starts, max_new, scale, window, lse).size("pdn_attn_paged_workspace_size")
+
+
+def pdn_attn_paged(q, o, k_pages, v_pages, table, lens, starts=None, max_new=None, scale=None, window=0, lse=None,
+                   workspace=None, stream=None) -> None:
+    """Attention of new tokens over their sequences' paged caches, which hold their
+    own keys and values already: q, o [N,H,d] (views are fine), the rest as in
+    pdn_cache_append, scale and window as in pdn_attn_fwd; lse fp32 [N,H] or None.
+    Rows that belong to no sequence are left as they were."""
+    _attn_paged(q, o, k_pages, v_pages, table, lens, starts, max_new, scale, window, lse).launch("pdn_attn_paged", stream, workspace)

@@ -1,0 +1,219 @@
+// What the attention kernels share: 32x32 matrix tiles of bf16 or fp32 operands,
+// tiles of rows in LDS, and which keys a query sees.  Not a public header.
+//
+// A matrix instruction's operands hold 8 consecutive k-slots to a lane, for both
+// types: lane l holds row (or column) l % 32 and slots 8 (l / 32) .. + 7.  Which k a
+// slot stands for is free as long as both operands agree.  A result's 16 registers
+// of lane l are column l % 32, rows 8 (i / 4) + 4 (l / 32) + i % 4; registers 8 s ..
+// 8 s + 7 of a result are therefore an operand of the next product, whose slots
+// stand for rows 16 s + 4 (l / 32) + {0 .. 3, 8 .. 11}.  So scores are formed
+// transposed (keys down, queries across): a query's sums run over a lane's own
+// registers and one other lane, and the probabilities never leave registers.
+#pragma once
+#include "common.h"
+#include "rows.h"
+
+#include <type_traits>
+
+namespace pdn {
+namespace attn {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) char lds_char;
+
+template <bool BF16>
+struct El;
+
+template <>
+struct El<true> {
+    static constexpr int BYTES = 2;
+    typedef bf16x8 Frag;
+    static __device__ __forceinline__ f32x16 mma(const Frag& a, const Frag& b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ Frag load(const void* p, long i) {
+        return *reinterpret_cast<const bf16x8*>(static_cast<const uint16_t*>(p) + i);
+    }
+    static __device__ __forceinline__ Frag zero() { return __builtin_bit_cast(Frag, u32x4{0u, 0u, 0u, 0u}); }
+    // registers 8 s .. 8 s + 7 of a result, to the nearest bf16
+    static __device__ __forceinline__ Frag of(const f32x16& r, int s) {
+        f32x8 w;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = r[8 * s + j];
+        return __builtin_convertvector(w, bf16x8);
+    }
+    // infinities and NaN to zero
+    static __device__ __forceinline__ Frag finite(const Frag& f) {
+        u32x4 w = __builtin_bit_cast(u32x4, f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if ((w[j] & 0x7f80u) == 0x7f80u) w[j] &= 0xffff0000u;
+            if ((w[j] & 0x7f800000u) == 0x7f800000u) w[j] &= 0xffffu;
+        }
+        return __builtin_bit_cast(Frag, w);
+    }
+};
+
+template <>
+struct El<false> {
+    static constexpr int BYTES = 4;
+    typedef f32x8 Frag;
+    static __device__ __forceinline__ f32x16 mma(const Frag& a, const Frag& b, f32x16 c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
+        return c;
+    }
+    static __device__ __forceinline__ Frag load(const void* p, long i) {
+        const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
+        const f32x4 lo = q[0], hi = q[1];
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    static __device__ __forceinline__ Frag zero() { return Frag{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}; }
+    static __device__ __forceinline__ Frag of(const f32x16& r, int s) {
+        Frag w;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = r[8 * s + j];
+        return w;
+    }
+    static __device__ __forceinline__ Frag finite(Frag f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = (__float_as_uint(f[j]) & 0x7f800000u) == 0x7f800000u ? 0.0f : f[j];
+        return f;
+    }
+};
+
+// A tile of rows in LDS, D channels each, as 16-byte chunks: chunk c of row r lies
+// at c ^ swizzle(r), so that neither the reads of one chunk of 16 rows nor those of
+// four neighbouring chunks of four rows meet in a bank.
+template <bool BF16, int D>
+struct Tile {
+    static constexpr int ROW = D * El<BF16>::BYTES, CHUNKS = ROW / 16;
+    static constexpr int ROWS_PER_DMA = 64 / CHUNKS;  // a wave's load of 16 bytes a lane
+    typedef typename El<BF16>::Frag Frag;
+
+    static __device__ __forceinline__ int swizzle(int r) {
+        if constexpr (CHUNKS >= 16) return ((r & 3) << 2) | ((r >> 2) & 3);
+        return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);  // two rows share the banks' width
+    }
+    // where chunk c of row r lies
+    static __device__ __forceinline__ int at(int r, int chunk) { return r * ROW + ((chunk ^ swizzle(r)) << 4); }
+
+    // Operands are read from LDS addresses tile + base(lane): tiles begin at multiples
+    // of 1024 bytes and operands at rows that are multiples of 16, so that the step to
+    // another chunk is an exclusive or of the address and to other rows a constant.
+
+    // rows l % 32, slots for channels 16 s + 8 (l / 32) .. + 7
+    static __device__ __forceinline__ uint32_t row_base(int lane) {
+        return at(lane & 31, (BF16 ? 1 : 2) * (lane >> 5));
+    }
+    static __device__ __forceinline__ Frag rows(uint32_t p, int r0, int s) {
+        if constexpr (BF16) {
+            return __builtin_bit_cast(Frag, read<u32x4>((p ^ (s << 5)) + r0 * ROW));
+        } else {
+            const f32x4 lo = read<f32x4>((p ^ (s << 6)) + r0 * ROW), hi = read<f32x4>((p ^ (s << 6) ^ 16) + r0 * ROW);
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    }
+    // channels 32 c + l % 32, slots for rows 4 (l / 32) + {0 .. 3, 8 .. 11}.  bf16 by
+    // transpose reads: of each 16 lanes lane 4 i + j points at row i, channels 4 j .. + 3
+    // of 16, and is given channel 4 i + j of the four rows.
+    static __device__ __forceinline__ uint32_t column_base(int lane) {
+        const int r = 4 * (lane >> 5);
+        if constexpr (BF16) return at(r + ((lane >> 2) & 3), ((lane >> 3) & 2) + ((lane >> 1) & 1)) + ((lane & 1) << 3);
+        return at(r, (lane & 31) >> 2) + ((lane & 3) << 2);
+    }
+    static __device__ __forceinline__ Frag columns(uint32_t p, int r0, int c) {
+        if constexpr (BF16) {
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)static_cast<uintptr_t>((p ^ (c << 6)) + r0 * ROW));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)static_cast<uintptr_t>((p ^ (c << 6) ^ 32) + (r0 + 8) * ROW));
+            return __builtin_bit_cast(Frag, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            Frag f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                f[j] = read<float>((p ^ (c << 7) ^ ((j & 3) << 6) ^ ((j >> 2) << 5)) + (r0 + (j & 3) + 8 * (j >> 2)) * ROW);
+            return f;
+        }
+    }
+
+private:
+    template <class T>
+    static __device__ __forceinline__ T read(uint32_t p) {
+        return *(const __attribute__((address_space(3))) T*)static_cast<uintptr_t>(p);
+    }
+};
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_char*)(const char*)p));
+}
+
+// 16 bytes a lane from memory to LDS, lane l's to dst + 16 l, past the registers.
+// Written out, because the compiler puts a wait for every such load of its own
+// before the next read of LDS, also of another buffer.  It has no result register,
+// and m0 no other use in these kernels; landed() waits for all of this wave's loads,
+// the compiler's own included.
+__device__ __forceinline__ void to_lds(const void* src, const char* dst) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane(lds_address(dst));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory");
+}
+// the same with 4 bytes a lane
+__device__ __forceinline__ void to_lds4(const void* src, const void* dst) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane(lds_address(dst));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(src) : "memory");
+}
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// The keys that a query sees: low .. low + count - 1.
+struct Seen {
+    int low, count;
+};
+
+// Query i of nq on nk keys, the queries being the last of them.
+__device__ __forceinline__ Seen seen_by(int i, int nq, int nk, int window, int first) {
+    const int p = i + nk - nq;
+    int low = first > 0 ? min(first, nk) : 0;
+    if (window > 0 && p - window + 1 > low) low = p - window + 1;
+    const int count = p - low + 1;  // p < nk
+    return Seen{low, count > 0 ? count : 0};
+}
+
+__device__ __forceinline__ bool sees(const Seen& s, int key) {
+    return static_cast<unsigned>(key - s.low) < static_cast<unsigned>(s.count);
+}
+
+__device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float lg2(float x) { return __builtin_amdgcn_logf(x); }
+
+// x, of which the compiler knows nothing: keeps what follows from it within a loop,
+// where taking it out would cost registers.
+__device__ __forceinline__ int opaque(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// The row of a 32x32 result's register i.
+__device__ __forceinline__ int result_row(int i, int lane) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
+
+__device__ __forceinline__ int wave_min_i(int x) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) x = min(x, __shfl_xor(x, off, 64));
+    return x;
+}
+__device__ __forceinline__ int wave_max_i(int x) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) x = max(x, __shfl_xor(x, off, 64));
+    return x;
+}
+
+// n / d for n below 2^16 and d up to 2^10, by a product with inverse_of(d).
+inline uint32_t inverse_of(uint32_t d) { return d == 1 ? 0u : static_cast<uint32_t>((uint64_t{1} << 32) / d + 1); }
+__device__ __forceinline__ int quotient(int n, uint32_t inverse) {
+    return inverse ? static_cast<int>(__umulhi(static_cast<uint32_t>(n), inverse)) : n;
+}
+
+}  // namespace attn
+}  // namespace pdn

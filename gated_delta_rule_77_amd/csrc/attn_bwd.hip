@@ -1,0 +1,567 @@
+// The gradient of causal softmax attention, from q, k, v, dO and what the forward
+// left (o and each row's lse):
+//
+//   P_ij = exp(scale s_ij - lse_i),  D_i = <dO_i, o_i>,  dS_ij = P_ij (<dO_i, v_j> - D_i)
+//   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dO_i
+//
+// in two passes that each own their sums, so that no atomics decide an order: dq by
+// rows of queries over tiles of keys (which also leaves D), then dk and dv by blocks of keys
+// over tiles of queries, head after head of those that share them.  P and <dO, v> are
+// formed in both: 14 products of d for each pair of a query and a key it sees, where
+// one pass would take 10.
+#include "attn.h"
+#include "block.h"
+#include "layer.h"
+
+namespace pdn {
+namespace {
+
+using namespace attn;
+
+constexpr int kThreads = 256;
+constexpr int kQueries = 64;  // of a tile in the pass over keys' gradients
+
+struct View4 {
+    const void* p;
+    long sb, sh, st;
+};
+struct Out4 {
+    void* p;
+    long sb, sh, st;
+};
+
+struct BwdParams {
+    View4 q, k, v, o, d_o;
+    Out4 dq, dk, dv;
+    const float* lse;
+    const int32_t* first;
+    float* delta;          // D: [B,H,Tq]
+    uint16_t* do16;        // bf16 copy of an fp32 dO, [B,H,Tq,D]; else null
+    int* first_range;      // [B][tiles of queries][2]: least and largest `first`; null without
+    int H, Hk, shared;
+    uint32_t inverse;
+    int Tq, Tk, window;
+    float scale, c;        // c: scale * log2(e)
+    int o_f32, g_f32;
+    int tiles;             // of the launch's own rows or keys
+    int query_tiles;
+};
+
+// The least and largest first key of each tile of queries.
+__global__ void __launch_bounds__(64) first_range_kernel(const int32_t* first, int Tq, int tiles, int* out) {
+    const int b = blockIdx.x / tiles, t = blockIdx.x - b * tiles;
+    const int i = min(t * kQueries + static_cast<int>(threadIdx.x), Tq - 1);
+    const int f = first[static_cast<long>(b) * Tq + i];
+    const int lo = wave_min_i(f), hi = wave_max_i(f);
+    if (threadIdx.x == 0) {
+        out[2 * blockIdx.x] = lo;
+        out[2 * blockIdx.x + 1] = hi;
+    }
+}
+
+// Four channels of an output's row.
+template <bool BF16>
+__device__ __forceinline__ void store4(void* p, long at, int f32, const f32x4& x) {
+    if (!BF16 || f32) *reinterpret_cast<f32x4*>(static_cast<float*>(p) + at) = x;
+    else *reinterpret_cast<bf16x4*>(static_cast<uint16_t*>(p) + at) = __builtin_convertvector(x, bf16x4);
+}
+
+template <bool BF16, int D, int QB>
+__global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_kernel(BwdParams p) {
+    using E = El<BF16>;
+    using TL = Tile<BF16, D>;
+    typedef typename E::Frag Frag;
+    constexpr int ROWS = 128 * QB, KT = !BF16 && D == 128 ? 32 : 64;
+    constexpr int S = D / 16, C = D / 32, KB = KT / 32;
+    constexpr int TILE = KT * TL::ROW, DMAS = KT / TL::ROWS_PER_DMA / 4;
+    __shared__ __align__(1024) char smem[4 * TILE];
+    __shared__ int bounds[2][4];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int h = lane >> 5;
+    const int nheads = static_cast<int>(gridDim.x) / p.tiles;
+    const int bh = blockIdx.x % nheads, tile = p.tiles - 1 - blockIdx.x / nheads;
+    const int b = bh / p.Hk, hk = bh - b * p.Hk;
+    const int nq = p.Tq, nk = p.Tk;
+    const char* kb = static_cast<const char*>(p.k.p) + (b * p.k.sb + hk * p.k.sh) * E::BYTES;
+    const char* vb = static_cast<const char*>(p.v.p) + (b * p.v.sb + hk * p.v.sh) * E::BYTES;
+    const int row0 = tile * ROWS, nrows = nq * p.shared;
+
+    const int t0 = row0 / p.shared, m0 = row0 - t0 * p.shared;
+    int token[QB], head[QB];
+    bool stored[QB];
+    Seen seen[QB];
+    Frag q[QB][S], dof[QB][S];
+    float lse2[QB], delta[QB];
+    int low = INT32_MAX, high = -1, full_low = 0, full_high = INT32_MAX;
+#pragma unroll
+    for (int a = 0; a < QB; ++a) {
+        const int dr = 32 * (wave * QB + a) + (lane & 31);
+        stored[a] = row0 + dr < nrows;
+        const int r = m0 + (stored[a] ? dr : nrows - 1 - row0), dt = quotient(r, p.inverse);
+        token[a] = t0 + dt;
+        head[a] = hk * p.shared + r - dt * p.shared;
+        const int f = p.first ? p.first[static_cast<long>(b) * nq + token[a]] : 0;
+        seen[a] = seen_by(token[a], nq, nk, p.window, f);
+        if (seen[a].count > 0) {
+            const int last = seen[a].low + seen[a].count - 1;
+            low = min(low, seen[a].low);
+            high = max(high, last);
+            full_low = max(full_low, seen[a].low);
+            full_high = min(full_high, last);
+        }
+        const long qa = b * p.q.sb + head[a] * p.q.sh + token[a] * p.q.st;
+        const long oa = b * p.o.sb + head[a] * p.o.sh + token[a] * p.o.st;
+        const long da = b * p.d_o.sb + head[a] * p.d_o.sh + token[a] * p.d_o.st;
+        const long row = (static_cast<long>(b) * p.H + head[a]) * nq + token[a];
+        float dot = 0.0f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int ch = 16 * s + 8 * h;
+            q[a][s] = E::load(p.q.p, qa + ch);
+            f32x8 x, y;
+            if (!BF16 || p.o_f32) {
+                x = El<false>::load(p.o.p, oa + ch);
+                y = El<false>::load(p.d_o.p, da + ch);
+                if constexpr (BF16) dof[a][s] = __builtin_convertvector(y, bf16x8);
+                else dof[a][s] = y;
+                if constexpr (BF16) {
+                    if (stored[a]) *reinterpret_cast<bf16x8*>(p.do16 + row * D + ch) = dof[a][s];
+                }
+            } else if constexpr (BF16) {
+                x = __builtin_convertvector(El<true>::load(p.o.p, oa + ch), f32x8);
+                dof[a][s] = E::load(p.d_o.p, da + ch);
+                y = __builtin_convertvector(dof[a][s], f32x8);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dot = fmaf(x[j], y[j], dot);
+        }
+        delta[a] = dot + __shfl_xor(dot, 32, 64);
+        lse2[a] = p.lse[row] * kLog2e;
+        if (stored[a] && h == 0) p.delta[row] = delta[a];
+    }
+    low = uniform(wave_min_i(low));
+    high = uniform(wave_max_i(high));
+    full_low = uniform(wave_max_i(full_low));
+    full_high = uniform(wave_min_i(full_high));
+    if (lane == 0) {
+        bounds[0][wave] = low;
+        bounds[1][wave] = high;
+    }
+    __syncthreads();
+    const int all_low = uniform(min(min(bounds[0][0], bounds[0][1]), min(bounds[0][2], bounds[0][3])));
+    const int all_high = uniform(max(max(bounds[1][0], bounds[1][1]), max(bounds[1][2], bounds[1][3])));
+    const int first_tile = all_low / KT, end_tile = all_high < 0 ? first_tile : all_high / KT + 1;
+
+    auto load_tile = [&](int t, int buffer) {
+        char* kd = smem + buffer * 2 * TILE;
+#pragma unroll
+        for (int i = 0; i < DMAS; ++i) {
+            const int n = wave * DMAS + i;
+            const int r = n * TL::ROWS_PER_DMA + lane / TL::CHUNKS;
+            const int chunk = (lane % TL::CHUNKS) ^ TL::swizzle(r);
+            const long key = min(t * KT + r, nk - 1);  // keys behind the last repeat it, unseen
+            to_lds(kb + key * p.k.st * E::BYTES + 16 * chunk, kd + n * 1024);
+            to_lds(vb + key * p.v.st * E::BYTES + 16 * chunk, kd + TILE + n * 1024);
+        }
+    };
+
+    f32x16 acc[QB][C];
+#pragma unroll
+    for (int a = 0; a < QB; ++a)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[a][c][i] = 0.0f;
+
+    const uint32_t at = lds_address(smem), row_base = TL::row_base(lane), column_base = TL::column_base(lane);
+    if (first_tile < end_tile) load_tile(first_tile, 0);
+    for (int t = first_tile; t < end_tile; ++t) {
+        const int buffer = (t - first_tile) & 1;
+        landed();
+        __syncthreads();
+        if (t + 1 < end_tile) load_tile(t + 1, buffer ^ 1);
+        const uint32_t kt = at + buffer * 2 * TILE, kr = kt + row_base, kc = kt + column_base, vr = kt + TILE + row_base;
+#pragma unroll
+        for (int kbk = 0; kbk < KB; ++kbk) {
+            const int r0 = 32 * kbk, k0 = t * KT + r0;
+            if (k0 > high || k0 + 31 < low) continue;
+            const bool partly = k0 < full_low || k0 + 31 > full_high;
+            f32x16 s[QB], dp[QB];
+#pragma unroll
+            for (int a = 0; a < QB; ++a)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[a][i] = dp[a][i] = 0.0f;
+#pragma unroll
+            for (int st = 0; st < S; ++st) {
+                const Frag kf = TL::rows(kr, r0, st);
+#pragma unroll
+                for (int a = 0; a < QB; ++a) s[a] = E::mma(kf, q[a][st], s[a]);
+            }
+#pragma unroll
+            for (int st = 0; st < S; ++st) {
+                const Frag vf = TL::rows(vr, r0, st);
+#pragma unroll
+                for (int a = 0; a < QB; ++a) dp[a] = E::mma(vf, dof[a][st], dp[a]);
+            }
+            bool dirty = false;
+            if (partly) {
+                // a key that is not finite gives scores that are not: it is taken out of the
+                // product for those that do not see it, and those that do have them from P
+                bool any = false;
+#pragma unroll
+                for (int a = 0; a < QB; ++a)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) any |= !(fabsf(s[a][i]) < INFINITY);
+                dirty = __ballot(any) != 0;
+            }
+            Frag df[QB][2];
+#pragma unroll
+            for (int a = 0; a < QB; ++a) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[a][i] = ex2(fmaf(s[a][i], p.c, -lse2[a])) * (dp[a][i] - delta[a]);
+                if (partly) {
+                    const Seen to = {opaque(seen[a].low - k0 - 4 * h), seen[a].count};
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (!sees(to, 8 * (i >> 2) + (i & 3))) s[a][i] = 0.0f;
+                }
+                df[a][0] = E::of(s[a], 0);
+                df[a][1] = E::of(s[a], 1);
+            }
+            if (!dirty) {
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const Frag kf = TL::columns(kc, r0 + 16 * u, c);
+#pragma unroll
+                        for (int a = 0; a < QB; ++a) acc[a][c] = E::mma(kf, df[a][u], acc[a][c]);
+                    }
+            } else {
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const Frag kf = E::finite(TL::columns(kc, r0 + 16 * u, c));
+#pragma unroll
+                        for (int a = 0; a < QB; ++a) acc[a][c] = E::mma(kf, df[a][u], acc[a][c]);
+                    }
+            }
+        }
+    }
+#pragma unroll
+    for (int a = 0; a < QB; ++a) {
+        if (!stored[a]) continue;
+        const long out = b * p.dq.sb + head[a] * p.dq.sh + token[a] * p.dq.st;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                f32x4 x;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = seen[a].count > 0 ? acc[a][c][4 * g + i] * p.scale : 0.0f;
+                store4<BF16>(p.dq.p, out + 32 * c + 8 * g + 4 * h, p.g_f32, x);
+            }
+    }
+}
+
+template <bool BF16, int D, int KB>
+__global__ void __launch_bounds__(kThreads, BF16 && KB * D == 64 ? 2 : 1) attn_dkv_kernel(BwdParams p) {
+    using E = El<BF16>;
+    using TL = Tile<BF16, D>;
+    typedef typename E::Frag Frag;
+    constexpr int KEYS = 128 * KB, QT = kQueries;
+    constexpr int S = D / 16, C = D / 32;
+    constexpr int TILE = QT * TL::ROW, DMAS = QT / TL::ROWS_PER_DMA / 4;
+    __shared__ __align__(1024) char smem[4 * TILE];
+    __shared__ __align__(16) float stats[2][3][QT];  // of a tile's queries: lse, D, first key
+    __shared__ int range[2][4];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int h = lane >> 5;
+    const int nheads = static_cast<int>(gridDim.x) / p.tiles;
+    const int bh = blockIdx.x % nheads, tile = blockIdx.x / nheads;  // the first keys have the most queries
+    const int b = bh / p.Hk, hk = bh - b * p.Hk;
+    const int nq = p.Tq, nk = p.Tk, off = nk - nq;
+    const int key0 = tile * KEYS, key1 = min(key0 + KEYS, nk) - 1;
+
+    // this lane's keys; those behind the last repeat it, unstored and unseen
+    int key[KB];
+    Frag k[KB][S], v[KB][S];
+#pragma unroll
+    for (int a = 0; a < KB; ++a) {
+        key[a] = key0 + 32 * (wave * KB + a) + (lane & 31);
+        const long j = min(key[a], nk - 1);
+        const long ka = b * p.k.sb + hk * p.k.sh + j * p.k.st, va = b * p.v.sb + hk * p.v.sh + j * p.v.st;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            k[a][s] = E::load(p.k.p, ka + 16 * s + 8 * h);
+            v[a][s] = E::load(p.v.p, va + 16 * s + 8 * h);
+        }
+    }
+
+    // the tiles of queries that see some of these keys
+    int begin = max(key0 - off, 0) / QT, end = nq;
+    if (p.window > 0 && key1 - off < nq - p.window) end = key1 - off + p.window;  // the last such query + 1
+    end = end <= 0 ? begin : (end + QT - 1) / QT;
+    if (p.first) {
+        int lo = INT32_MAX, hi = -1;
+        for (int t = begin + tid; t < end; t += kThreads)
+            if (p.first_range[2 * (b * p.query_tiles + t)] <= key1) {
+                lo = min(lo, t);
+                hi = t;
+            }
+        lo = wave_min_i(lo);
+        hi = wave_max_i(hi);
+        if (lane == 0) {
+            range[0][wave] = lo;
+            range[1][wave] = hi;
+        }
+        __syncthreads();
+        begin = max(begin, min(min(range[0][0], range[0][1]), min(range[0][2], range[0][3])));
+        end = max(max(range[1][0], range[1][1]), max(range[1][2], range[1][3])) + 1;
+    }
+    begin = uniform(begin);
+    end = uniform(end);
+
+    f32x16 dk[KB][C], dv[KB][C];
+#pragma unroll
+    for (int a = 0; a < KB; ++a)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dk[a][c][i] = dv[a][c][i] = 0.0f;
+
+    const bool copied = BF16 && p.o_f32;
+    auto load_tile = [&](int g, int t, int buffer) {
+        const int head = hk * p.shared + g;
+        const char* qb = static_cast<const char*>(p.q.p) + (b * p.q.sb + head * p.q.sh) * E::BYTES;
+        const char* db = copied ? reinterpret_cast<const char*>(p.do16 + (static_cast<long>(b) * p.H + head) * nq * D)
+                                : static_cast<const char*>(p.d_o.p) + (b * p.d_o.sb + head * p.d_o.sh) * E::BYTES;
+        const long ds = copied ? D : p.d_o.st;
+        char* qd = smem + buffer * 2 * TILE;
+#pragma unroll
+        for (int i = 0; i < DMAS; ++i) {
+            const int n = wave * DMAS + i;
+            const int r = n * TL::ROWS_PER_DMA + lane / TL::CHUNKS;
+            const int chunk = (lane % TL::CHUNKS) ^ TL::swizzle(r);
+            const long row = min(t * QT + r, nq - 1);  // queries behind the last repeat it, unseen
+            to_lds(qb + row * p.q.st * E::BYTES + 16 * chunk, qd + n * 1024);
+            to_lds(db + row * ds * E::BYTES + 16 * chunk, qd + TILE + n * 1024);
+        }
+        const int i = min(t * QT + lane, nq - 1);
+        const long row = (static_cast<long>(b) * p.H + head) * nq + i;
+        if (wave == 0) to_lds4(p.lse + row, &stats[buffer][0][0]);
+        if (wave == 1) to_lds4(p.delta + row, &stats[buffer][1][0]);
+        if (wave == 2 && p.first) to_lds4(p.first + static_cast<long>(b) * nq + i, &stats[buffer][2][0]);
+    };
+
+    const uint32_t at = lds_address(smem), row_base = TL::row_base(lane), column_base = TL::column_base(lane);
+    const int count = end > begin ? (end - begin) * p.shared : 0;
+    int g = 0, t = begin;
+    if (count > 0) load_tile(0, begin, 0);
+    for (int n = 0; n < count; ++n) {
+        const int buffer = n & 1;
+        landed();
+        __syncthreads();
+        const int now = t;
+        if (++t == end) {
+            t = begin;
+            ++g;
+        }
+        if (n + 1 < count) load_tile(g, t, buffer ^ 1);
+        const uint32_t qt = at + buffer * 2 * TILE, qr = qt + row_base, qc = qt + column_base, dr = qr + TILE, dc = qc + TILE;
+        const int w0 = key0 + 32 * KB * wave, w1 = w0 + 32 * KB - 1;  // this wave's keys
+        // whether queries and keys all see each other; some do
+        const bool packed = p.first && p.first_range[2 * (b * p.query_tiles + now) + 1] > w0;
+#pragma unroll
+        for (int rb = 0; rb < QT / 32; ++rb) {
+            const int r0 = 32 * rb, i0 = now * QT + r0, p0 = i0 + off;
+            if (i0 >= nq || p0 + 31 < w0 || (p.window > 0 && p0 - p.window >= w1)) continue;
+            const bool partly = packed || i0 + 31 >= nq || p0 < w1 || (p.window > 0 && p0 + 31 - p.window >= w0);
+            f32x16 s[KB], dp[KB];
+#pragma unroll
+            for (int a = 0; a < KB; ++a)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[a][i] = dp[a][i] = 0.0f;
+#pragma unroll
+            for (int st = 0; st < S; ++st) {
+                const Frag f = TL::rows(qr, r0, st);
+#pragma unroll
+                for (int a = 0; a < KB; ++a) s[a] = E::mma(f, k[a][st], s[a]);
+            }
+#pragma unroll
+            for (int st = 0; st < S; ++st) {
+                const Frag f = TL::rows(dr, r0, st);
+#pragma unroll
+                for (int a = 0; a < KB; ++a) dp[a] = E::mma(f, v[a][st], dp[a]);
+            }
+            bool dirty = false;
+            if (partly) {
+                // as for dq: queries and their dO that are not finite are taken out of the
+                // products for keys they do not see, and reach the others through P and D
+                bool any = false;
+#pragma unroll
+                for (int a = 0; a < KB; ++a)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) any |= !(fabsf(s[a][i]) < INFINITY) || !(fabsf(dp[a][i]) < INFINITY);
+                dirty = __ballot(any) != 0;
+            }
+            Frag pf[KB][2], df[KB][2];
+#pragma unroll
+            for (int a = 0; a < KB; ++a) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const f32x4 lse = *reinterpret_cast<const f32x4*>(&stats[buffer][0][r0 + 8 * e + 4 * h]);
+                    const f32x4 dl = *reinterpret_cast<const f32x4*>(&stats[buffer][1][r0 + 8 * e + 4 * h]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int x = 4 * e + i;
+                        s[a][x] = ex2(fmaf(s[a][x], p.c, -lse[i] * kLog2e));
+                        dp[a][x] = s[a][x] * (dp[a][x] - dl[i]);
+                        if (dirty) s[a][x] += 0.0f * dl[i];
+                    }
+                }
+                if (partly) {
+                    // query r of the block sees the key from r = from on, to the window's end
+                    const int from = opaque(key[a] - p0 - 4 * h);
+                    int to = nq - i0 - 4 * h;
+                    if (p.window > 0) to = min(to, from + p.window);
+                    if (key[a] >= nk) to = INT32_MIN;
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        const int r = 8 * (x >> 2) + (x & 3);
+                        bool seen = r >= from && r < to;
+                        if (packed) seen = seen && __float_as_int(stats[buffer][2][r0 + r + 4 * h]) <= key[a];
+                        if (!seen) s[a][x] = dp[a][x] = 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    pf[a][u] = E::of(s[a], u);
+                    df[a][u] = E::of(dp[a], u);
+                }
+            }
+            auto products = [&](auto clean) {
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        Frag x = TL::columns(dc, r0 + 16 * u, c), y = TL::columns(qc, r0 + 16 * u, c);
+                        if constexpr (decltype(clean)::value) {
+                            x = E::finite(x);
+                            y = E::finite(y);
+                        }
+#pragma unroll
+                        for (int a = 0; a < KB; ++a) {
+                            dv[a][c] = E::mma(x, pf[a][u], dv[a][c]);
+                            dk[a][c] = E::mma(y, df[a][u], dk[a][c]);
+                        }
+                    }
+            };
+            if (!dirty) products(std::false_type());
+            else products(std::true_type());
+        }
+    }
+#pragma unroll
+    for (int a = 0; a < KB; ++a) {
+        if (key[a] >= nk) continue;
+        const long ko = b * p.dk.sb + hk * p.dk.sh + key[a] * p.dk.st, vo = b * p.dv.sb + hk * p.dv.sh + key[a] * p.dv.st;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f32x4 x, y;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = dk[a][c][4 * e + i] * p.scale;
+                    y[i] = dv[a][c][4 * e + i];
+                }
+                store4<BF16>(p.dk.p, ko + 32 * c + 8 * e + 4 * h, p.g_f32, x);
+                store4<BF16>(p.dv.p, vo + 32 * c + 8 * e + 4 * h, p.g_f32, y);
+            }
+    }
+}
+
+struct Layout {
+    size_t delta, do16, first_range, bytes;  // offsets in the workspace
+};
+
+size_t up256(size_t n) { return (n + 255) & ~size_t{255}; }
+
+int query_tiles(int Tq) { return (Tq + kQueries - 1) / kQueries; }
+
+Layout layout(const pdn_attn_bwd_args& a) {
+    const pdn_attn_args& f = a.fwd;
+    const size_t rows = static_cast<size_t>(f.B) * f.H * f.Tq;
+    Layout l{};
+    l.do16 = up256(rows * sizeof(float));
+    l.first_range = l.do16 + (f.dtype == PDN_BF16 && f.o_dtype == PDN_F32 ? up256(rows * f.d * 2) : 0);
+    l.bytes = l.first_range + (f.first ? up256(static_cast<size_t>(f.B) * query_tiles(f.Tq) * 2 * sizeof(int)) : 0);
+    return l;
+}
+
+template <bool BF16, int D>
+hipError_t launch(BwdParams p, long heads, hipStream_t stream) {
+    constexpr int QB = 1, KB = 1;
+    if (p.Tq > 0) {
+        const long rows = static_cast<long>(p.Tq) * p.shared;
+        p.tiles = static_cast<int>((rows + 128 * QB - 1) / (128 * QB));
+        attn_dq_kernel<BF16, D, QB><<<dim3(static_cast<unsigned>(heads * p.tiles)), dim3(kThreads), 0, stream>>>(p);
+        const hipError_t rc = hipGetLastError();
+        if (rc != hipSuccess) return rc;
+    }
+    if (p.Tk > 0) {
+        p.tiles = (p.Tk + 128 * KB - 1) / (128 * KB);
+        attn_dkv_kernel<BF16, D, KB><<<dim3(static_cast<unsigned>(heads * p.tiles)), dim3(kThreads), 0, stream>>>(p);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t attn_bwd_workspace_bytes(const pdn_attn_bwd_args& a) { return layout(a).bytes; }
+
+hipError_t launch_attn_bwd(const pdn_attn_bwd_args& a, hipStream_t stream) {
+    const pdn_attn_args& f = a.fwd;
+    const Layout l = layout(a);
+    char* ws = static_cast<char*>(a.workspace);
+    BwdParams p{};
+    p.q = {f.q, f.q_sb, f.q_sh, f.q_st};
+    p.k = {f.k, f.k_sb, f.k_sh, f.k_st};
+    p.v = {f.v, f.v_sb, f.v_sh, f.v_st};
+    p.o = {f.o, f.o_sb, f.o_sh, f.o_st};
+    p.d_o = {a.d_o, a.do_sb, a.do_sh, a.do_st};
+    p.dq = {a.dq, a.dq_sb, a.dq_sh, a.dq_st};
+    p.dk = {a.dk, a.dk_sb, a.dk_sh, a.dk_st};
+    p.dv = {a.dv, a.dv_sb, a.dv_sh, a.dv_st};
+    p.lse = f.lse;
+    p.first = f.first;
+    p.delta = reinterpret_cast<float*>(ws + l.delta);
+    p.do16 = reinterpret_cast<uint16_t*>(ws + l.do16);
+    p.first_range = reinterpret_cast<int*>(ws + l.first_range);
+    p.H = f.H;
+    p.Hk = f.Hk;
+    p.shared = f.H / f.Hk;
+    p.inverse = inverse_of(p.shared);
+    p.Tq = f.Tq;
+    p.Tk = f.Tk;
+    p.window = f.window < f.Tk ? f.window : 0;  // as far as there are keys: all of them
+    p.scale = f.scale;
+    p.c = f.scale * kLog2e;
+    p.o_f32 = f.o_dtype == PDN_F32;
+    p.g_f32 = a.g_dtype == PDN_F32;
+    p.query_tiles = query_tiles(f.Tq);
+    if (f.first && f.Tq > 0) {
+        first_range_kernel<<<dim3(static_cast<unsigned>(f.B * p.query_tiles)), dim3(64), 0, stream>>>(f.first, f.Tq, p.query_tiles,
+                                                                                                     p.first_range);
+        const hipError_t rc = hipGetLastError();
+        if (rc != hipSuccess) return rc;
+    }
+    const long heads = static_cast<long>(f.B) * f.Hk;
+    if (f.dtype == PDN_BF16) return f.d == 64 ? launch<true, 64>(p, heads, stream) : launch<true, 128>(p, heads, stream);
+    return f.d == 64 ? launch<false, 64>(p, heads, stream) : launch<false, 128>(p, heads, stream);
+}
+
+}  // namespace pdn

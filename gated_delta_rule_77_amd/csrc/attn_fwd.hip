@@ -1,0 +1,629 @@
+// Causal softmax attention, over contiguous keys and over a paged cache:
+//
+//   o_i = sum_j exp(c (s_ij - m_i)) v_j / sum_j exp(c (s_ij - m_i)),  s = <q, k>,
+//
+// one pass over the keys with a running maximum m and sum.  The heads that share a
+// key head are rows of one tile beside the tokens (row = token * shared + head), so
+// that a tile of keys is read once for all of them and a tile's diagonal is short.
+//
+// A workgroup is four waves.  WK = 1: each wave holds 32 QB rows of its own and the
+// waves share tiles of KT keys in LDS, loaded one tile ahead past the registers.
+// WK > 1 (few rows, a decode step above all): WK waves share the rows, each takes
+// its part of every tile's keys, and their sums are joined at the end.  Where the
+// grid would not fill the device, the keys are dealt to `splits` workgroups, whose
+// sums a second kernel joins.
+#include "attn.h"
+#include "block.h"
+#include "layer.h"
+#include "pages.h"
+
+namespace pdn {
+namespace {
+
+using namespace attn;
+
+struct FwdParams {
+    const void *q, *k, *v;
+    void* o;
+    float* lse;
+    const int32_t* first;
+    long q_sb, q_sh, q_st, k_sb, k_sh, k_st, v_sb, v_sh, v_st, o_sb, o_sh, o_st;
+    int H, Hk, shared;   // query heads, key heads, H / Hk
+    uint32_t inverse;    // of `shared`
+    int Tq, Tk;
+    int window;
+    float c;             // scale * log2(e)
+    int o_f32;
+    int tiles, splits;   // of rows; of the keys
+    float* part;         // splits > 1: [splits][rows][D] sums, then [splits][rows][2] (maximum, sum)
+    long rows;           // B H Tq
+    // paged: q_st, o_st step rows of N; k_sb, v_sb step pages
+    PageMap map;
+};
+
+constexpr int kThreads = 256;
+// A row's maximum is moved (and its sums scaled) when a score passes it by this
+// much, in powers of two: until then the exponentials stay below 2^8, well inside
+// fp32 and, as bf16 factors, as exact as any.
+constexpr float kSlack = 8.0f;
+
+// Tiles of keys in flight: one being read, one being loaded.
+constexpr int kBuffers = 2;
+
+template <bool BF16, int D, int QB, int WK, int KT, bool PAGED>
+__global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128 * 128 ? 2 : 1) attn_fwd_kernel(FwdParams p) {
+    using E = El<BF16>;
+    using TL = Tile<BF16, D>;
+    typedef typename E::Frag Frag;
+    constexpr int WR = 4 / WK;                 // waves with rows of their own
+    constexpr int ROWS = 32 * QB * WR;         // of the workgroup
+    constexpr int KB = KT / 32 / WK;           // a wave's blocks of 32 keys in a tile
+    constexpr int S = D / 16, C = D / 32;
+    constexpr int TILE = KT * TL::ROW, DMAS = KT / TL::ROWS_PER_DMA / 4;
+    static_assert(KB >= 1 && DMAS >= 1, "every wave has keys to read and rows to load");
+    __shared__ __align__(1024) char smem[kBuffers * 2 * TILE];
+    __shared__ int bounds[2][4];
+    __shared__ float joined[WK > 1 ? 2 : 1][WK > 1 ? 4 : 1][32 * QB];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+    const int h = lane >> 5;
+    // heads before tiles: the workgroups of one key head follow each other on one XCD
+    // (for 8 heads, or multiples), the tiles with the most keys first
+    const int nheads = static_cast<int>(gridDim.x) / (p.tiles * p.splits);
+    const int bh = blockIdx.x % nheads, rest = blockIdx.x / nheads;
+    const int split = rest % p.splits, tile = p.tiles - 1 - rest / p.splits;
+    const int b = bh / p.Hk, hk = bh - b * p.Hk;
+
+    int nq = p.Tq, nk = p.Tk;
+    const char *qb = static_cast<const char*>(p.q), *kb = static_cast<const char*>(p.k), *vb = static_cast<const char*>(p.v);
+    long orow = 0;   // of the sequence's token 0
+    if constexpr (PAGED) {
+        const Sequence sq = sequence_of(p.map, b);
+        nq = min(sq.n, p.Tq);
+        nk = sq.len;
+        const int behind = sq.n - nq;  // tokens past what the launch was sized for stay out
+        nk = max(nk - behind, 0);
+        qb += sq.start * p.q_st * E::BYTES;
+        orow = sq.start;
+    } else {
+        qb += b * p.q_sb * E::BYTES;
+        kb += b * p.k_sb * E::BYTES;
+        vb += b * p.v_sb * E::BYTES;
+    }
+    kb += hk * p.k_sh * E::BYTES;
+    vb += hk * p.v_sh * E::BYTES;
+    const int row0 = tile * ROWS, nrows = nq * p.shared;
+    if (row0 >= nrows) return;
+
+    // this lane's rows: their tokens, heads and keys; rows behind the last repeat it, unstored
+    const int t0 = row0 / p.shared, m0 = row0 - t0 * p.shared;
+    int token[QB], head[QB];
+    bool stored[QB];
+    Seen seen[QB];
+    Frag q[QB][S];
+    int low = INT32_MAX, high = -1, full_low = 0, full_high = INT32_MAX;
+#pragma unroll
+    for (int a = 0; a < QB; ++a) {
+        const int dr = 32 * ((wave / WK) * QB + a) + (lane & 31);
+        stored[a] = row0 + dr < nrows;
+        const int r = m0 + (stored[a] ? dr : nrows - 1 - row0), dt = quotient(r, p.inverse);
+        token[a] = t0 + dt;
+        head[a] = hk * p.shared + r - dt * p.shared;
+        const int f = !PAGED && p.first ? p.first[static_cast<long>(b) * p.Tq + token[a]] : 0;
+        seen[a] = seen_by(token[a], nq, nk, p.window, f);
+        if (seen[a].count > 0) {
+            const int last = seen[a].low + seen[a].count - 1;
+            low = min(low, seen[a].low);
+            high = max(high, last);
+            full_low = max(full_low, seen[a].low);
+            full_high = min(full_high, last);
+        }
+        const char* at = qb + (token[a] * p.q_st + head[a] * p.q_sh) * E::BYTES;
+#pragma unroll
+        for (int s = 0; s < S; ++s) q[a][s] = E::load(at, 16 * s + 8 * h);
+    }
+    low = uniform(wave_min_i(low));
+    high = uniform(wave_max_i(high));
+    full_low = uniform(wave_max_i(full_low));
+    full_high = uniform(wave_min_i(full_high));
+    if (lane == 0) {
+        bounds[0][wave] = low;
+        bounds[1][wave] = high;
+    }
+    __syncthreads();
+    const int all_low = uniform(min(min(bounds[0][0], bounds[0][1]), min(bounds[0][2], bounds[0][3])));
+    const int all_high = uniform(max(max(bounds[1][0], bounds[1][1]), max(bounds[1][2], bounds[1][3])));
+    int first_tile = all_low / KT, end_tile = all_high < 0 ? first_tile : all_high / KT + 1;
+    if (p.splits > 1) {
+        const int n = end_tile > first_tile ? (end_tile - first_tile + p.splits - 1) / p.splits : 0;
+        first_tile += split * n;
+        end_tile = min(end_tile, first_tile + n);
+    }
+
+    // this lane's part of each tile: 16 bytes of rows r, the source chunk swizzled
+    auto load_tile = [&](int t, int buffer) {
+        char* kd = smem + buffer * 2 * TILE;
+        char* vd = kd + TILE;
+#pragma unroll
+        for (int i = 0; i < DMAS; ++i) {
+            const int n = wave * DMAS + i;
+            const int r = n * TL::ROWS_PER_DMA + lane / TL::CHUNKS;
+            const int chunk = (lane % TL::CHUNKS) ^ TL::swizzle(r);
+            const int key = min(t * KT + r, nk - 1);  // keys behind the last repeat it, unseen
+            long ko, vo;
+            if constexpr (PAGED) {
+                const long page = page_of(p.map, b, key);
+                const int in = key & ((1 << p.map.shift) - 1);
+                ko = page * p.k_sb + in * p.k_st;
+                vo = page * p.v_sb + in * p.v_st;
+            } else {
+                ko = key * p.k_st;
+                vo = key * p.v_st;
+            }
+            to_lds(kb + ko * E::BYTES + 16 * chunk, kd + n * 1024);
+            to_lds(vb + vo * E::BYTES + 16 * chunk, vd + n * 1024);
+        }
+    };
+
+    // 0 v, summed over the channels, of a block's keys: a result's rows
+    auto times_zero = [&](uint32_t vr, int r0) {
+        f32x16 x;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+#pragma unroll
+        for (int st = 0; st < S; ++st) x = E::mma(TL::rows(vr, r0, st), E::zero(), x);
+        return x;
+    };
+    auto not_finite = [&](uint32_t vr, int r0) {
+        const f32x16 x = times_zero(vr, r0);
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) any |= x[i] != x[i];
+        return __ballot(any);
+    };
+
+    f32x16 acc[QB][C];
+    float mc[QB], sum[QB];   // maximum times c; this half wave's part of the sum
+#pragma unroll
+    for (int a = 0; a < QB; ++a) {
+        mc[a] = -INFINITY;
+        sum[a] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[a][c][i] = 0.0f;
+    }
+
+    const uint32_t at = lds_address(smem), row_base = TL::row_base(lane), column_base = TL::column_base(lane);
+    if (first_tile < end_tile) load_tile(first_tile, 0);
+    for (int t = first_tile; t < end_tile; ++t) {
+        const int buffer = (t - first_tile) & 1;
+        landed();
+        __syncthreads();  // every wave's part of the tile; and the other buffer has been read
+        if (t + 1 < end_tile) load_tile(t + 1, buffer ^ 1);
+        const uint32_t kt = at + buffer * 2 * TILE + row_base, vt = at + (buffer * 2 + 1) * TILE;
+        const uint32_t vr = vt + row_base, vc = vt + column_base;
+#pragma unroll
+        for (int kbk = 0; kbk < KB; ++kbk) {
+            const int r0 = 32 * ((wave % WK) * KB + kbk), k0 = t * KT + r0;
+            if (k0 > high || k0 + 31 < low) continue;
+            const bool partly = k0 < full_low || k0 + 31 > full_high;
+            f32x16 s[QB];
+#pragma unroll
+            for (int a = 0; a < QB; ++a)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[a][i] = 0.0f;
+#pragma unroll
+            for (int st = 0; st < S; ++st) {
+                const Frag kf = TL::rows(kt, r0, st);
+#pragma unroll
+                for (int a = 0; a < QB; ++a) s[a] = E::mma(kf, q[a][st], s[a]);
+            }
+            bool dirty = false;
+            if (partly) {
+                // Unseen keys: no part in the maximum, a probability of zero.  Zero times a
+                // value that is not finite would still be NaN: such values (which 0 v shows)
+                // are taken out of the product, and make the probabilities of those that see
+                // them NaN instead.
+                dirty = not_finite(vr, r0) != 0;
+#pragma unroll
+                for (int a = 0; a < QB; ++a) {
+                    const Seen to = {opaque(seen[a].low - k0 - 4 * h), seen[a].count};
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (!sees(to, 8 * (i >> 2) + (i & 3))) s[a][i] = -INFINITY;
+                }
+            }
+            float top[QB];
+            bool moves = false;
+#pragma unroll
+            for (int a = 0; a < QB; ++a) {
+                float x = s[a][0];
+#pragma unroll
+                for (int i = 1; i < 16; ++i) x = fmaxf(x, s[a][i]);
+                top[a] = fmaxf(x, __shfl_xor(x, 32, 64)) * p.c;
+                moves |= top[a] > mc[a] + kSlack;
+            }
+            if (__ballot(moves) != 0) {
+#pragma unroll
+                for (int a = 0; a < QB; ++a) {
+                    // each row by itself: what another holds has no part in its rounding either
+                    const float to = top[a] > mc[a] + kSlack ? top[a] : mc[a];
+                    const float by = to == mc[a] ? 1.0f : ex2(mc[a] - to);
+                    mc[a] = to;
+                    sum[a] *= by;
+#pragma unroll
+                    for (int c = 0; c < C; ++c)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) acc[a][c][i] *= by;
+                }
+            }
+            Frag pf[QB][2];
+#pragma unroll
+            for (int a = 0; a < QB; ++a) {
+                const float m = mc[a] == -INFINITY ? 0.0f : mc[a];
+                float add = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    s[a][i] = ex2(fmaf(s[a][i], p.c, -m));
+                    add += s[a][i];
+                }
+                sum[a] += add;
+                if (dirty) {
+                    const f32x16 poison = times_zero(vr, r0);
+                    const Seen to = {opaque(seen[a].low - k0 - 4 * h), seen[a].count};
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (sees(to, 8 * (i >> 2) + (i & 3))) s[a][i] += poison[i];
+                }
+                pf[a][0] = E::of(s[a], 0);
+                pf[a][1] = E::of(s[a], 1);
+            }
+            if (!dirty) {
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const Frag vf = TL::columns(vc, r0 + 16 * u, c);
+#pragma unroll
+                        for (int a = 0; a < QB; ++a) acc[a][c] = E::mma(vf, pf[a][u], acc[a][c]);
+                    }
+            } else {
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const Frag vf = E::finite(TL::columns(vc, r0 + 16 * u, c));
+#pragma unroll
+                        for (int a = 0; a < QB; ++a) acc[a][c] = E::mma(vf, pf[a][u], acc[a][c]);
+                    }
+            }
+        }
+    }
+#pragma unroll
+    for (int a = 0; a < QB; ++a) sum[a] += __shfl_xor(sum[a], 32, 64);
+
+    // a row of the sums
+    auto index = [&](int a) { return (static_cast<long>(b) * p.H + head[a]) * p.Tq + token[a]; };
+    auto store4 = [&](int a, int ch, f32x4 x) {  // four channels of one row
+        if (p.splits > 1) {
+            *reinterpret_cast<f32x4*>(p.part + (split * p.rows + index(a)) * D + ch) = x;
+            return;
+        }
+        const long at = (PAGED ? (orow + token[a]) * p.o_st : b * p.o_sb + token[a] * p.o_st) + head[a] * p.o_sh + ch;
+        if (!BF16 || p.o_f32) {
+            *reinterpret_cast<f32x4*>(static_cast<float*>(p.o) + at) = x;
+        } else {
+            *reinterpret_cast<bf16x4*>(static_cast<uint16_t*>(p.o) + at) = __builtin_convertvector(x, bf16x4);
+        }
+    };
+    auto store_sums = [&](int a, float m, float l) {
+        if (p.splits > 1) {
+            float* ml = p.part + p.splits * p.rows * D + (split * p.rows + index(a)) * 2;
+            ml[0] = seen[a].count > 0 ? m : -INFINITY;
+            ml[1] = seen[a].count > 0 ? l : 0.0f;
+        } else if (p.lse) {
+            p.lse[PAGED ? (orow + token[a]) * p.H + head[a] : index(a)] = seen[a].count > 0 ? (m + lg2(l)) * kLn2 : -INFINITY;
+        }
+    };
+    // what turns a row's sums into its output (or leaves them, for the join)
+    auto norm = [&](float l) { return p.splits > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l; };
+
+    if constexpr (WK == 1) {
+#pragma unroll
+        for (int a = 0; a < QB; ++a) {
+            if (!stored[a]) continue;
+            const bool none = seen[a].count == 0;
+            const float n = norm(sum[a]);
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    f32x4 x;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = none ? 0.0f : acc[a][c][4 * g + i] * n;
+                    store4(a, 32 * c + 8 * g + 4 * h, x);
+                }
+            if (h == 0) store_sums(a, mc[a], sum[a]);
+        }
+    } else {
+        // The WK waves of a row: their maxima and sums, then their scaled sums by channel
+        // through the tiles' memory.  A wave adds up D / WK of the channels.
+        static_assert(kBuffers * 2 * TILE >= 4 * QB * 32 * (D + 4) * 4, "the waves' sums fit the tiles' memory");
+        static_assert(QB == 1, "one block of rows a wave");
+        if (h == 0) {
+            joined[0][wave][lane & 31] = mc[0];
+            joined[1][wave][lane & 31] = sum[0];
+        }
+        __syncthreads();
+        const int w0 = wave / WK * WK;
+        float m = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WK; ++w) m = fmaxf(m, joined[0][w0 + w][lane & 31]);
+#pragma unroll
+        for (int w = 0; w < WK; ++w) {
+            const float mw = joined[0][w0 + w][lane & 31];
+            l += mw == -INFINITY ? joined[1][w0 + w][lane & 31] : joined[1][w0 + w][lane & 31] * ex2(mw - m);
+        }
+        const float by = mc[0] == -INFINITY ? 1.0f : ex2(mc[0] - m);
+        float* mine = reinterpret_cast<float*>(smem) + (wave * 32 + (lane & 31)) * (D + 4);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                f32x4 x;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = acc[0][c][4 * g + i] * by;
+                *reinterpret_cast<f32x4*>(mine + 32 * c + 8 * g + 4 * h) = x;
+            }
+        __syncthreads();
+        if (!stored[0]) return;
+        const bool none = seen[0].count == 0;
+        const float n = norm(l);
+        constexpr int PART = D / WK;
+#pragma unroll
+        for (int j = 0; j < PART / 8; ++j) {
+            const int ch = (wave % WK) * PART + 8 * j + 4 * h;
+            f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < WK; ++w)
+                x += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(smem) + ((w0 + w) * 32 + (lane & 31)) * (D + 4) + ch);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = none ? 0.0f : x[i] * n;
+            store4(0, ch, x);
+        }
+        if (h == 0 && wave % WK == 0) store_sums(0, m, l);
+    }
+}
+
+// The splits' sums of each row joined: D / 4 lanes to a row.
+struct JoinParams {
+    const float* part;
+    void* o;
+    float* lse;
+    long rows, o_sb, o_sh, o_st;
+    int splits, H, Tq;
+    int o_f32;
+    PageMap map;
+};
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(kThreads) attn_join_kernel(JoinParams p) {
+    constexpr int LPR = D / 4;
+    const long row = (static_cast<long>(blockIdx.x) * kThreads + threadIdx.x) / LPR;
+    if (row >= p.rows) return;
+    const int ch = 4 * (threadIdx.x % LPR);
+    const long bh = row / p.Tq, b = bh / p.H, head = bh - b * p.H;
+    long t = row - bh * p.Tq, out = row;  // out: of lse
+    if constexpr (PAGED) {
+        const Sequence s = sequence_of(p.map, static_cast<int>(b));
+        if (t >= s.n) return;
+        t += s.start;
+        out = t * p.H + head;
+    }
+    const long at = b * p.o_sb + head * p.o_sh + t * p.o_st + ch;
+    const float* ml = p.part + p.splits * p.rows * D + row * 2;
+    float m = -INFINITY;
+    for (int s = 0; s < p.splits; ++s) m = fmaxf(m, ml[s * p.rows * 2]);
+    float l = 0.0f;
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < p.splits; ++s) {
+        const float ms = ml[s * p.rows * 2], ls = ml[s * p.rows * 2 + 1];
+        if (ls == 0.0f) continue;  // no keys there
+        const float by = ms == -INFINITY ? 1.0f : ex2(ms - m);
+        l = fmaf(ls, by, l);
+        x += *reinterpret_cast<const f32x4*>(p.part + (s * p.rows + row) * D + ch) * by;
+    }
+    const bool none = l == 0.0f;
+    const float n = none ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] *= n;
+    if (p.o_f32) *reinterpret_cast<f32x4*>(static_cast<float*>(p.o) + at) = x;
+    else *reinterpret_cast<bf16x4*>(static_cast<uint16_t*>(p.o) + at) = __builtin_convertvector(x, bf16x4);
+    if (p.lse && ch == 0) p.lse[out] = none ? -INFINITY : (m + lg2(l)) * kLn2;
+}
+
+// How a call is laid over the device, by its sizes alone.
+struct Plan {
+    int qb, wk, rows;   // blocks of rows a wave, waves that share rows, rows of a workgroup
+    int tiles, splits;
+};
+
+constexpr long kFill = 512;       // workgroups that fill the device: two to a compute unit
+constexpr int kLeastKeys = 256;   // of a split
+
+Plan plan(bool bf16, int d, long heads, long rows, long keys) {
+    Plan p{};
+    const bool wide = !bf16 && d == 128;  // 512-byte rows: half the keys to a tile
+    if (rows <= (wide ? 64 : 32)) {
+        p.qb = 1;
+        p.wk = wide ? 2 : 4;
+    } else {
+        p.qb = bf16 && rows > 128 ? 2 : 1;
+        p.wk = 1;
+    }
+    p.rows = 32 * p.qb * (4 / p.wk);
+    p.tiles = static_cast<int>((rows + p.rows - 1) / p.rows);
+    const long groups = heads * p.tiles;
+    p.splits = 1;
+    if (groups < kFill / 2) {
+        long want = kFill / groups, most = keys / kLeastKeys;
+        if (want > most) want = most;
+        if (want > 128) want = 128;
+        p.splits = want > 1 ? static_cast<int>(want) : 1;
+    }
+    return p;
+}
+
+size_t part_bytes(const Plan& p, long rows, int d) {
+    return p.splits > 1 ? static_cast<size_t>(p.splits) * rows * (d + 2) * sizeof(float) : 0;
+}
+
+template <bool BF16, int D, bool PAGED>
+hipError_t launch_kind(const FwdParams& p, const Plan& pl, long groups, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(groups)), block(kThreads);
+    constexpr bool wide = !BF16 && D == 128;
+    constexpr int WK = wide ? 2 : 4, KT_FEW = wide ? 64 : 128, KT = wide ? 32 : 64;
+    if (pl.wk > 1) attn_fwd_kernel<BF16, D, 1, WK, KT_FEW, PAGED><<<grid, block, 0, stream>>>(p);
+    else if (pl.qb == 1) attn_fwd_kernel<BF16, D, 1, 1, KT, PAGED><<<grid, block, 0, stream>>>(p);
+    else if constexpr (BF16) attn_fwd_kernel<BF16, D, 2, 1, KT, PAGED><<<grid, block, 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+template <bool PAGED>
+hipError_t launch(const FwdParams& p, const Plan& pl, int32_t dtype, int d, long heads, hipStream_t stream) {
+    const long groups = heads * pl.tiles * pl.splits;
+    if (dtype == PDN_BF16) return d == 64 ? launch_kind<true, 64, PAGED>(p, pl, groups, stream) : launch_kind<true, 128, PAGED>(p, pl, groups, stream);
+    return d == 64 ? launch_kind<false, 64, PAGED>(p, pl, groups, stream) : launch_kind<false, 128, PAGED>(p, pl, groups, stream);
+}
+
+template <bool PAGED>
+hipError_t launch_join(const JoinParams& p, int d, hipStream_t stream) {
+    const long threads = p.rows * (d / 4);
+    const dim3 grid(static_cast<unsigned>((threads + kThreads - 1) / kThreads)), block(kThreads);
+    if (d == 64) attn_join_kernel<64, PAGED><<<grid, block, 0, stream>>>(p);
+    else attn_join_kernel<128, PAGED><<<grid, block, 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+Plan plan_of(const pdn_attn_args& a) {
+    return plan(a.dtype == PDN_BF16, a.d, static_cast<long>(a.B) * a.Hk, static_cast<long>(a.Tq) * (a.H / a.Hk),
+                a.window > 0 && a.window < a.Tk - a.Tq ? a.window + a.Tq : a.Tk);
+}
+
+Plan plan_of(const pdn_attn_paged_args& a) {
+    const long keys = static_cast<long>(a.cache.table_width) * a.cache.page_size;
+    return plan(a.cache.dtype == PDN_BF16, a.cache.d, static_cast<long>(a.cache.B) * a.cache.Hk,
+                static_cast<long>(a.cache.max_new) * (a.H / a.cache.Hk),
+                a.window > 0 && static_cast<long>(a.window) + a.cache.max_new < keys ? static_cast<long>(a.window) + a.cache.max_new : keys);
+}
+
+}  // namespace
+
+// 128 rows to a workgroup (or one workgroup for fewer), 128 keys in the backward, and 64
+// queries to a wave of its range kernel; a call with splits is a small one.
+bool attn_fits(const pdn_attn_args& a) {
+    const long heads = static_cast<long>(a.B) * a.Hk, rows = static_cast<long>(a.Tq) * (a.H / a.Hk);
+    return heads * ((rows + 127) / 128 + 1) * kThreads < kMaxGridThreads && heads * ((a.Tk + 127L) / 128) * kThreads < kMaxGridThreads &&
+           static_cast<long>(a.B) * (a.Tq + 64L) < kMaxGridThreads;
+}
+
+bool attn_paged_fits(const pdn_attn_paged_args& a) {
+    const long heads = static_cast<long>(a.cache.B) * a.cache.Hk, rows = static_cast<long>(a.cache.max_new) * (a.H / a.cache.Hk);
+    return heads * ((rows + 127) / 128 + 1) * kThreads < kMaxGridThreads;
+}
+
+size_t attn_fwd_workspace_bytes(const pdn_attn_args& a) {
+    return a.Tq == 0 ? 0 : part_bytes(plan_of(a), static_cast<long>(a.B) * a.H * a.Tq, a.d);
+}
+
+hipError_t launch_attn_fwd(const pdn_attn_args& a, hipStream_t stream) {
+    if (a.Tq == 0) return hipSuccess;
+    const Plan pl = plan_of(a);
+    FwdParams p{};
+    p.q = a.q;
+    p.k = a.k;
+    p.v = a.v;
+    p.o = a.o;
+    p.lse = a.lse;
+    p.first = a.first;
+    p.q_sb = a.q_sb, p.q_sh = a.q_sh, p.q_st = a.q_st;
+    p.k_sb = a.k_sb, p.k_sh = a.k_sh, p.k_st = a.k_st;
+    p.v_sb = a.v_sb, p.v_sh = a.v_sh, p.v_st = a.v_st;
+    p.o_sb = a.o_sb, p.o_sh = a.o_sh, p.o_st = a.o_st;
+    p.H = a.H;
+    p.Hk = a.Hk;
+    p.shared = a.H / a.Hk;
+    p.inverse = inverse_of(p.shared);
+    p.Tq = a.Tq;
+    p.Tk = a.Tk;
+    p.window = a.window < a.Tk ? a.window : 0;  // as far as there are keys: all of them
+    p.c = a.scale * kLog2e;
+    p.o_f32 = a.o_dtype == PDN_F32;
+    p.tiles = pl.tiles;
+    p.splits = pl.splits;
+    p.part = static_cast<float*>(a.workspace);
+    p.rows = static_cast<long>(a.B) * a.H * a.Tq;
+    const hipError_t rc = launch<false>(p, pl, a.dtype, a.d, static_cast<long>(a.B) * a.Hk, stream);
+    if (rc != hipSuccess || pl.splits == 1) return rc;
+    JoinParams j{};
+    j.part = p.part;
+    j.o = a.o;
+    j.lse = a.lse;
+    j.rows = p.rows;
+    j.o_sb = a.o_sb, j.o_sh = a.o_sh, j.o_st = a.o_st;
+    j.splits = pl.splits;
+    j.H = a.H;
+    j.Tq = a.Tq;
+    j.o_f32 = p.o_f32;
+    return launch_join<false>(j, a.d, stream);
+}
+
+size_t attn_paged_workspace_bytes(const pdn_attn_paged_args& a) {
+    return a.cache.N == 0 || a.cache.max_new == 0 ? 0 : part_bytes(plan_of(a), static_cast<long>(a.cache.B) * a.H * a.cache.max_new, a.cache.d);
+}
+
+hipError_t launch_attn_paged(const pdn_attn_paged_args& a, hipStream_t stream) {
+    const pdn_cache& c = a.cache;
+    if (c.N == 0 || c.max_new == 0) return hipSuccess;
+    const Plan pl = plan_of(a);
+    FwdParams p{};
+    p.q = a.q;
+    p.k = c.k_pages;
+    p.v = c.v_pages;
+    p.o = a.o;
+    p.lse = a.lse;
+    p.q_sh = a.q_sh, p.q_st = a.q_sn;
+    p.k_sb = c.k_sp, p.k_sh = c.k_sh, p.k_st = c.k_st;
+    p.v_sb = c.v_sp, p.v_sh = c.v_sh, p.v_st = c.v_st;
+    p.o_sh = a.o_sh, p.o_st = a.o_sn;
+    p.H = a.H;
+    p.Hk = c.Hk;
+    p.shared = a.H / c.Hk;
+    p.inverse = inverse_of(p.shared);
+    p.Tq = c.max_new;
+    p.window = a.window < c.table_width * c.page_size ? a.window : 0;
+    p.c = a.scale * kLog2e;
+    p.o_f32 = a.o_dtype == PDN_F32;
+    p.tiles = pl.tiles;
+    p.splits = pl.splits;
+    p.part = static_cast<float*>(a.workspace);
+    p.rows = static_cast<long>(c.B) * a.H * c.max_new;
+    p.map = page_map(c);
+    const hipError_t rc = launch<true>(p, pl, c.dtype, c.d, static_cast<long>(c.B) * c.Hk, stream);
+    if (rc != hipSuccess || pl.splits == 1) return rc;
+    JoinParams j{};
+    j.part = p.part;
+    j.o = a.o;
+    j.lse = a.lse;
+    j.rows = p.rows;
+    j.o_sh = a.o_sh, j.o_st = a.o_sn;
+    j.splits = pl.splits;
+    j.H = a.H;
+    j.Tq = c.max_new;
+    j.o_f32 = p.o_f32;
+    j.map = p.map;
+    return launch_join<true>(j, c.d, stream);
+}
+
+}  // namespace pdn

@@ -9,13 +9,15 @@
 #include <atomic>
 #include <mutex>
 
+#include "checks.h"
 #include "kernels.h"
 #include "layer.h"
 #include "pdn.h"
 
 namespace {
 
-bool valid_dtype(int32_t d) { return d == PDN_F32 || d == PDN_BF16; }
+using namespace pdn::checks;
+
 bool valid_alpha(int32_t m) {
     return m == PDN_ALPHA_NONE || m == PDN_ALPHA_SCALAR || m == PDN_ALPHA_VEC;
 }
@@ -33,13 +35,9 @@ bool valid_precond(float eps, int32_t mode, float x) {
     return true;
 }
 
-// Largest B*H (and B*H*T) the launch grids and 32/64-bit index math accept.
-constexpr long kMaxBH = 1L << 24;
 // B * H * T: keeps every launch grid (at most one wave per 32-token chunk and
 // (b, h), four per workgroup) below 2^31 workgroups
 constexpr long kMaxTokens = 1L << 36;
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Gate enums and pointers.  With no tokens to process (need_data false) the
 // gate pointers may be NULL.
@@ -155,63 +153,6 @@ int check_decode(const pdn_decode_args* a) {
 
 // ---- the operators around the recurrence ----
 
-// B * T of the strided operators: their kernels index tokens in 32 bits.
-constexpr long kMaxRows = 1L << 30;
-
-int elt_bytes(int32_t dtype) { return dtype == PDN_BF16 ? 2 : 4; }
-
-// A strided tensor: a pointer, the sizes of its dimensions but the last (which
-// is contiguous, `width` elements) and their strides.
-struct View {
-    const void* p;
-    int64_t size[3], stride[3];
-    int64_t width;
-    int bytes;
-};
-
-View view3(const void* p, int64_t s0, int64_t s1, int64_t s2, int64_t t0, int64_t t1, int64_t t2, int64_t width, int32_t dtype) {
-    return View{p, {s0, s1, s2}, {t0, t1, t2}, width, elt_bytes(dtype)};
-}
-
-// Strides of a strided tensor (only dimensions longer than 1 are stepped
-// over): not negative, every row 16-byte aligned, the whole within 63 bits;
-// and, for an output, no row over another.
-int check_view(const View& v, bool output) {
-    if (!aligned16(v.p)) return PDN_EINVAL;
-    constexpr int64_t kMost = int64_t{1} << 56;
-    int64_t size[3], stride[3];
-    int n = 0;
-    __int128 reach = v.width;
-    for (int i = 0; i < 3; ++i) {
-        if (v.size[i] <= 1) continue;
-        if (v.stride[i] < 0 || v.stride[i] > kMost) return PDN_EINVAL;
-        if (v.stride[i] * v.bytes % 16 != 0) return PDN_EINVAL;
-        reach += static_cast<__int128>(v.stride[i]) * (v.size[i] - 1);
-        size[n] = v.size[i];
-        stride[n++] = v.stride[i];
-    }
-    if (reach > kMost) return PDN_EINVAL;
-    if (!output) return PDN_OK;
-    // from the smallest stride up, each step passes all that lies below it
-    for (int i = 0; i < n; ++i)
-        for (int j = i + 1; j < n; ++j)
-            if (stride[j] < stride[i]) {
-                const int64_t a = stride[i], b = size[i];
-                stride[i] = stride[j];
-                size[i] = size[j];
-                stride[j] = a;
-                size[j] = b;
-            }
-    int64_t span = v.width;
-    for (int i = 0; i < n; ++i) {
-        if (stride[i] < span) return PDN_EINVAL;
-        span = stride[i] * (size[i] - 1) + span;
-    }
-    return PDN_OK;
-}
-
-bool valid_eps(float eps) { return std::isnormal(eps) && eps > 0.0f; }
-
 int check_rows(int32_t B, int32_t H, int32_t T) {
     if (B < 1 || H < 1 || T < 0) return PDN_EINVAL;
     if (static_cast<long>(B) * H > kMaxBH) return PDN_EUNSUPPORTED;
@@ -244,12 +185,6 @@ int check_qk_norm(const pdn_qk_norm_args* a, bool backward = false) {
     rc = check_view(view3(a->xq, a->B, a->T, a->Hq, a->xq_sb, a->xq_st, a->xq_sh, a->d, a->dtype), false);
     if (rc != PDN_OK) return rc;
     return check_view(view3(a->xk, a->B, a->T, a->Hk, a->xk_sb, a->xk_st, a->xk_sh, a->d, a->dtype), false);
-}
-
-int check_workspace(const void* workspace, size_t bytes, size_t need) {
-    if (need == 0) return PDN_OK;
-    if (workspace && !aligned16(workspace)) return PDN_EINVAL;
-    return !workspace || bytes < need ? PDN_EWORKSPACE : PDN_OK;
 }
 
 int check_qk_norm_bwd(const pdn_qk_norm_bwd_args* a, bool check_ws = true) {
@@ -370,37 +305,6 @@ int check_scan_step(const pdn_scan_step_args* a) {
     rc = check_view(view3(a->log_a, a->B, 1, 1, a->log_a_sb, 0, 0, a->D, a->log_dtype), false);
     if (rc != PDN_OK) return rc;
     return check_view(view3(a->h, a->B, 1, 1, a->h_sb, 0, 0, a->D, a->dtype), true);
-}
-
-// The extern "C" bodies: an answer, a size or a launch, and no exception out.
-template <class F>
-int answer(F f) {
-    try {
-        return f();
-    } catch (...) {
-        return PDN_EINVAL;
-    }
-}
-
-template <class A, class Check, class Launch>
-int call(const A* args, void* stream, Check check, Launch launch) {
-    try {
-        const int rc = check(args);
-        if (rc != PDN_OK) return rc;
-        return launch(*args, static_cast<hipStream_t>(stream)) == hipSuccess ? PDN_OK : PDN_EHIP;
-    } catch (...) {
-        return PDN_EHIP;
-    }
-}
-
-template <class A, class Check, class Size>
-int size_of(const A* args, size_t* bytes, Check check, Size size) {
-    if (!args || !bytes) return PDN_EINVAL;
-    return answer([&] {
-        const int rc = check(args);
-        if (rc == PDN_OK) *bytes = size(*args);
-        return rc;
-    });
 }
 
 // Scratch of pdn_chunk_fwd_noalloc: one copy per GPU, loaded with the code
