@@ -149,23 +149,33 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_char*)(const char*)p));
 }
 
-// 16 bytes a lane from memory to LDS, lane l's to dst + 16 l, past the registers.
-// Written out, because the compiler puts a wait for every such load of its own
-// before the next read of LDS, also of another buffer.  It has no result register,
-// and m0 no other use in these kernels; landed() waits for all of this wave's loads,
-// the compiler's own included.
-__device__ __forceinline__ void to_lds(const void* src, const char* dst) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane(lds_address(dst));
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory");
-}
-// the same with 4 bytes a lane
-__device__ __forceinline__ void to_lds4(const void* src, const void* dst) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane(lds_address(dst));
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(src) : "memory");
-}
-__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// From memory to LDS past the registers: 16 (or 4) bytes a lane, lane l's to LDS address
+// dst + 16 l (4 l).  Written out, because the compiler puts a wait for every such load of
+// its own before the next read of LDS, also of another buffer.  They have no result
+// register, and m0 no other use in these kernels.  landed() waits for all of this
+// wave's loads; the compiler takes note of its wait (and drops its own for what it
+// loaded before).
+__device__ __forceinline__ void to_lds(const void* src, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(uniform(dst)), "v"(src) : "memory");
+}
+__device__ __forceinline__ const char* uniform(const char* p) {
+    const uint64_t x = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = uniform(static_cast<int>(x)), hi = uniform(static_cast<int>(x >> 32));
+    return reinterpret_cast<const char*>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+// the same from a uniform address and 32-bit offsets of the lanes
+__device__ __forceinline__ void to_lds(const char* base, uint32_t offset, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform(dst)), "v"(offset), "s"(uniform(base)) : "memory");
+}
+__device__ __forceinline__ void to_lds4(const void* src, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(uniform(dst)), "v"(src) : "memory");
+}
+__device__ __forceinline__ void landed() {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0), the other counters free
+}
 
 // The keys that a query sees: low .. low + count - 1.
 struct Seen {
@@ -195,8 +205,13 @@ __device__ __forceinline__ int opaque(int x) {
     return x;
 }
 
-// The row of a 32x32 result's register i.
-__device__ __forceinline__ int result_row(int i, int lane) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
+// x of the two half waves joined, the same in both: lanes l and l ^ 32 swap theirs.
+template <bool MAX>
+__device__ __forceinline__ float halves(float x) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    const float a = __uint_as_float(p[0]), b = __uint_as_float(p[1]);
+    return MAX ? fmaxf(a, b) : a + b;
+}
 
 __device__ __forceinline__ int wave_min_i(int x) {
 #pragma unroll

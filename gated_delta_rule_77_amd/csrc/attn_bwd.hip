@@ -153,8 +153,8 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
     const int all_high = uniform(max(max(bounds[1][0], bounds[1][1]), max(bounds[1][2], bounds[1][3])));
     const int first_tile = all_low / KT, end_tile = all_high < 0 ? first_tile : all_high / KT + 1;
 
-    auto load_tile = [&](int t, int buffer) {
-        char* kd = smem + buffer * 2 * TILE;
+    auto load_tile = [&](int t, int buffer) __attribute__((always_inline)) {
+        const uint32_t kd = lds_address(smem) + buffer * 2 * TILE;
 #pragma unroll
         for (int i = 0; i < DMAS; ++i) {
             const int n = wave * DMAS + i;
@@ -334,13 +334,13 @@ __global__ void __launch_bounds__(kThreads, BF16 && KB * D == 64 ? 2 : 1) attn_d
             for (int i = 0; i < 16; ++i) dk[a][c][i] = dv[a][c][i] = 0.0f;
 
     const bool copied = BF16 && p.o_f32;
-    auto load_tile = [&](int g, int t, int buffer) {
+    auto load_tile = [&](int g, int t, int buffer) __attribute__((always_inline)) {
         const int head = hk * p.shared + g;
         const char* qb = static_cast<const char*>(p.q.p) + (b * p.q.sb + head * p.q.sh) * E::BYTES;
         const char* db = copied ? reinterpret_cast<const char*>(p.do16 + (static_cast<long>(b) * p.H + head) * nq * D)
                                 : static_cast<const char*>(p.d_o.p) + (b * p.d_o.sb + head * p.d_o.sh) * E::BYTES;
         const long ds = copied ? D : p.d_o.st;
-        char* qd = smem + buffer * 2 * TILE;
+        const uint32_t qd = lds_address(smem) + buffer * 2 * TILE;
 #pragma unroll
         for (int i = 0; i < DMAS; ++i) {
             const int n = wave * DMAS + i;
@@ -352,9 +352,9 @@ __global__ void __launch_bounds__(kThreads, BF16 && KB * D == 64 ? 2 : 1) attn_d
         }
         const int i = min(t * QT + lane, nq - 1);
         const long row = (static_cast<long>(b) * p.H + head) * nq + i;
-        if (wave == 0) to_lds4(p.lse + row, &stats[buffer][0][0]);
-        if (wave == 1) to_lds4(p.delta + row, &stats[buffer][1][0]);
-        if (wave == 2 && p.first) to_lds4(p.first + static_cast<long>(b) * nq + i, &stats[buffer][2][0]);
+        if (wave == 0) to_lds4(p.lse + row, lds_address(&stats[buffer][0][0]));
+        if (wave == 1) to_lds4(p.delta + row, lds_address(&stats[buffer][1][0]));
+        if (wave == 2 && p.first) to_lds4(p.first + static_cast<long>(b) * nq + i, lds_address(&stats[buffer][2][0]));
     };
 
     const uint32_t at = lds_address(smem), row_base = TL::row_base(lane), column_base = TL::column_base(lane);
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, BF16 && KB * D == 64 ? 2 : 1) attn_d
                     df[a][u] = E::of(dp[a], u);
                 }
             }
-            auto products = [&](auto clean) {
+            auto products = [&](auto clean) __attribute__((always_inline)) {
 #pragma unroll
                 for (int c = 0; c < C; ++c)
 #pragma unroll

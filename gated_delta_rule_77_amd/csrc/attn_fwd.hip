@@ -140,33 +140,54 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
         end_tile = min(end_tile, first_tile + n);
     }
 
-    // this lane's part of each tile: 16 bytes of rows r, the source chunk swizzled
-    auto load_tile = [&](int t, int buffer) {
-        char* kd = smem + buffer * 2 * TILE;
-        char* vd = kd + TILE;
+    const uint32_t at = lds_address(smem), row_base = TL::row_base(lane), column_base = TL::column_base(lane);
+
+    // A tile's rows to LDS: a wave's loads of RPD rows each, 16 bytes a lane, the source
+    // chunk swizzled.  Such rows lie at one stride from a uniform address, on one page of a
+    // cache too; those of a tile that passes the last key repeat it, unseen.
+    constexpr int RPD = TL::ROWS_PER_DMA;
+    uint32_t k_off[DMAS], v_off[DMAS];
+#pragma unroll
+    for (int i = 0; i < DMAS; ++i) {
+        const int r = lane / TL::CHUNKS, chunk = (lane % TL::CHUNKS) ^ TL::swizzle((wave * DMAS + i) * RPD + r);
+        k_off[i] = static_cast<uint32_t>(r * p.k_st * E::BYTES) + 16 * chunk;
+        v_off[i] = static_cast<uint32_t>(r * p.v_st * E::BYTES) + 16 * chunk;
+    }
+    auto place = [&](int key, long& ko, long& vo) __attribute__((always_inline)) {
+        if constexpr (PAGED) {
+            const long page = page_of(p.map, b, key);
+            const int in = key & ((1 << p.map.shift) - 1);
+            ko = page * p.k_sb + in * p.k_st;
+            vo = page * p.v_sb + in * p.v_st;
+        } else {
+            ko = key * p.k_st;
+            vo = key * p.v_st;
+        }
+    };
+    auto load_tile = [&](int t, int buffer) __attribute__((always_inline)) {
+        const uint32_t dst = at + buffer * 2 * TILE + wave * DMAS * 1024;
+        if (t * KT + KT <= nk) {
+#pragma unroll
+            for (int i = 0; i < DMAS; ++i) {
+                long ko, vo;
+                place(uniform(t * KT + (wave * DMAS + i) * RPD), ko, vo);
+                to_lds(kb + ko * E::BYTES, k_off[i], dst + i * 1024);
+                to_lds(vb + vo * E::BYTES, v_off[i], dst + TILE + i * 1024);
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < DMAS; ++i) {
-            const int n = wave * DMAS + i;
-            const int r = n * TL::ROWS_PER_DMA + lane / TL::CHUNKS;
-            const int chunk = (lane % TL::CHUNKS) ^ TL::swizzle(r);
-            const int key = min(t * KT + r, nk - 1);  // keys behind the last repeat it, unseen
+            const int r = (wave * DMAS + i) * RPD + lane / TL::CHUNKS, chunk = (lane % TL::CHUNKS) ^ TL::swizzle(r);
             long ko, vo;
-            if constexpr (PAGED) {
-                const long page = page_of(p.map, b, key);
-                const int in = key & ((1 << p.map.shift) - 1);
-                ko = page * p.k_sb + in * p.k_st;
-                vo = page * p.v_sb + in * p.v_st;
-            } else {
-                ko = key * p.k_st;
-                vo = key * p.v_st;
-            }
-            to_lds(kb + ko * E::BYTES + 16 * chunk, kd + n * 1024);
-            to_lds(vb + vo * E::BYTES + 16 * chunk, vd + n * 1024);
+            place(min(t * KT + r, nk - 1), ko, vo);
+            to_lds(kb + ko * E::BYTES + 16 * chunk, dst + i * 1024);
+            to_lds(vb + vo * E::BYTES + 16 * chunk, dst + TILE + i * 1024);
         }
     };
 
     // 0 v, summed over the channels, of a block's keys: a result's rows
-    auto times_zero = [&](uint32_t vr, int r0) {
+    auto times_zero = [&](uint32_t vr, int r0) __attribute__((always_inline)) {
         f32x16 x;
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = 0.0f;
@@ -174,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
         for (int st = 0; st < S; ++st) x = E::mma(TL::rows(vr, r0, st), E::zero(), x);
         return x;
     };
-    auto not_finite = [&](uint32_t vr, int r0) {
+    auto not_finite = [&](uint32_t vr, int r0) __attribute__((always_inline)) {
         const f32x16 x = times_zero(vr, r0);
         bool any = false;
 #pragma unroll
@@ -194,114 +215,179 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
             for (int i = 0; i < 16; ++i) acc[a][c][i] = 0.0f;
     }
 
-    const uint32_t at = lds_address(smem), row_base = TL::row_base(lane), column_base = TL::column_base(lane);
-    if (first_tile < end_tile) load_tile(first_tile, 0);
-    for (int t = first_tile; t < end_tile; ++t) {
+    // The maximum moved where a row's scores pass it (each row by itself: what another
+    // holds has no part in its rounding either).
+    auto move = [&](const float (&top)[QB]) __attribute__((always_inline)) {
+        bool moves = false;
+#pragma unroll
+        for (int a = 0; a < QB; ++a) moves |= top[a] > mc[a] + kSlack;
+        if (__ballot(moves) == 0) return;
+#pragma unroll
+        for (int a = 0; a < QB; ++a) {
+            const float to = top[a] > mc[a] + kSlack ? top[a] : mc[a];
+            const float by = to == mc[a] ? 1.0f : ex2(mc[a] - to);
+            mc[a] = to;
+            sum[a] *= by;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[a][c][i] *= by;
+        }
+    };
+
+    // a block of 32 keys of which some rows may not see all
+    auto some_seen = [&](int r0, int k0, uint32_t kt, uint32_t vt) __attribute__((always_inline)) {
+        if (k0 > high || k0 + 31 < low) return;
+        const uint32_t kr = kt + row_base, vr = vt + row_base, vc = vt + column_base;
+        f32x16 s[QB];
+#pragma unroll
+        for (int a = 0; a < QB; ++a)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[a][i] = 0.0f;
+#pragma unroll
+        for (int st = 0; st < S; ++st) {
+            const Frag kf = TL::rows(kr, r0, st);
+#pragma unroll
+            for (int a = 0; a < QB; ++a) s[a] = E::mma(kf, q[a][st], s[a]);
+        }
+        // Unseen keys: no part in the maximum, a probability of zero.  Zero times a value
+        // that is not finite would still be NaN: such values (which 0 v shows) are taken out
+        // of the product, and make the probabilities of those that see them NaN instead.
+        const bool dirty = not_finite(vr, r0) != 0;
+        float top[QB];
+#pragma unroll
+        for (int a = 0; a < QB; ++a) {
+            const Seen to = {opaque(seen[a].low - k0 - 4 * h), seen[a].count};
+            float x = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (!sees(to, 8 * (i >> 2) + (i & 3))) s[a][i] = -INFINITY;
+                x = fmaxf(x, s[a][i]);
+            }
+            top[a] = halves<true>(x) * p.c;
+        }
+        move(top);
+        Frag pf[QB][2];
+#pragma unroll
+        for (int a = 0; a < QB; ++a) {
+            const float m = mc[a] == -INFINITY ? 0.0f : mc[a];
+            float add = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[a][i] = ex2(fmaf(s[a][i], p.c, -m));
+                add += s[a][i];
+            }
+            sum[a] += add;
+            if (dirty) {
+                const f32x16 poison = times_zero(vr, r0);
+                const Seen to = {opaque(seen[a].low - k0 - 4 * h), seen[a].count};
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (sees(to, 8 * (i >> 2) + (i & 3))) s[a][i] += poison[i];
+            }
+            pf[a][0] = E::of(s[a], 0);
+            pf[a][1] = E::of(s[a], 1);
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                Frag vf = TL::columns(vc, r0 + 16 * u, c);
+                if (dirty) vf = E::finite(vf);
+#pragma unroll
+                for (int a = 0; a < QB; ++a) acc[a][c] = E::mma(vf, pf[a][u], acc[a][c]);
+            }
+    };
+
+    // a wave's keys of a tile that all its rows see
+    auto all_seen = [&](int r0, uint32_t kt, uint32_t vt) __attribute__((always_inline)) {
+        const uint32_t kr = kt + row_base, vc = vt + column_base;
+        f32x16 s[KB][QB];
+#pragma unroll
+        for (int e = 0; e < KB; ++e) {
+#pragma unroll
+            for (int a = 0; a < QB; ++a)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[e][a][i] = 0.0f;
+#pragma unroll
+            for (int st = 0; st < S; ++st) {
+                const Frag kf = TL::rows(kr, r0 + 32 * e, st);
+#pragma unroll
+                for (int a = 0; a < QB; ++a) s[e][a] = E::mma(kf, q[a][st], s[e][a]);
+            }
+        }
+        float top[QB];
+#pragma unroll
+        for (int a = 0; a < QB; ++a) {
+            float x = s[0][a][0];
+#pragma unroll
+            for (int e = 0; e < KB; ++e)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x = fmaxf(x, s[e][a][i]);
+            top[a] = halves<true>(x) * p.c;
+        }
+        move(top);
+        Frag pf[KB][QB][2];
+#pragma unroll
+        for (int a = 0; a < QB; ++a) {
+            const float m = mc[a] == -INFINITY ? 0.0f : mc[a];
+#pragma unroll
+            for (int e = 0; e < KB; ++e) {
+                float add = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    s[e][a][i] = ex2(fmaf(s[e][a][i], p.c, -m));
+                    add += s[e][a][i];
+                }
+                sum[a] += add;
+                pf[e][a][0] = E::of(s[e][a], 0);
+                pf[e][a][1] = E::of(s[e][a], 1);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int e = 0; e < KB; ++e)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const Frag vf = TL::columns(vc, r0 + 32 * e + 16 * u, c);
+#pragma unroll
+                    for (int a = 0; a < QB; ++a) acc[a][c] = E::mma(vf, pf[e][a][u], acc[a][c]);
+                }
+    };
+
+    // The tiles in order; those that all of the wave's rows see whole in a loop of their own.
+    const int rw = 32 * KB * (wave % WK);  // the wave's first row of a tile
+    int t = first_tile;
+    auto next = [&](uint32_t& kt) __attribute__((always_inline)) {
         const int buffer = (t - first_tile) & 1;
         landed();
         __syncthreads();  // every wave's part of the tile; and the other buffer has been read
         if (t + 1 < end_tile) load_tile(t + 1, buffer ^ 1);
-        const uint32_t kt = at + buffer * 2 * TILE + row_base, vt = at + (buffer * 2 + 1) * TILE;
-        const uint32_t vr = vt + row_base, vc = vt + column_base;
-#pragma unroll
-        for (int kbk = 0; kbk < KB; ++kbk) {
-            const int r0 = 32 * ((wave % WK) * KB + kbk), k0 = t * KT + r0;
-            if (k0 > high || k0 + 31 < low) continue;
-            const bool partly = k0 < full_low || k0 + 31 > full_high;
-            f32x16 s[QB];
-#pragma unroll
-            for (int a = 0; a < QB; ++a)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s[a][i] = 0.0f;
-#pragma unroll
-            for (int st = 0; st < S; ++st) {
-                const Frag kf = TL::rows(kt, r0, st);
-#pragma unroll
-                for (int a = 0; a < QB; ++a) s[a] = E::mma(kf, q[a][st], s[a]);
-            }
-            bool dirty = false;
-            if (partly) {
-                // Unseen keys: no part in the maximum, a probability of zero.  Zero times a
-                // value that is not finite would still be NaN: such values (which 0 v shows)
-                // are taken out of the product, and make the probabilities of those that see
-                // them NaN instead.
-                dirty = not_finite(vr, r0) != 0;
-#pragma unroll
-                for (int a = 0; a < QB; ++a) {
-                    const Seen to = {opaque(seen[a].low - k0 - 4 * h), seen[a].count};
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (!sees(to, 8 * (i >> 2) + (i & 3))) s[a][i] = -INFINITY;
-                }
-            }
-            float top[QB];
-            bool moves = false;
-#pragma unroll
-            for (int a = 0; a < QB; ++a) {
-                float x = s[a][0];
-#pragma unroll
-                for (int i = 1; i < 16; ++i) x = fmaxf(x, s[a][i]);
-                top[a] = fmaxf(x, __shfl_xor(x, 32, 64)) * p.c;
-                moves |= top[a] > mc[a] + kSlack;
-            }
-            if (__ballot(moves) != 0) {
-#pragma unroll
-                for (int a = 0; a < QB; ++a) {
-                    // each row by itself: what another holds has no part in its rounding either
-                    const float to = top[a] > mc[a] + kSlack ? top[a] : mc[a];
-                    const float by = to == mc[a] ? 1.0f : ex2(mc[a] - to);
-                    mc[a] = to;
-                    sum[a] *= by;
-#pragma unroll
-                    for (int c = 0; c < C; ++c)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[a][c][i] *= by;
-                }
-            }
-            Frag pf[QB][2];
-#pragma unroll
-            for (int a = 0; a < QB; ++a) {
-                const float m = mc[a] == -INFINITY ? 0.0f : mc[a];
-                float add = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    s[a][i] = ex2(fmaf(s[a][i], p.c, -m));
-                    add += s[a][i];
-                }
-                sum[a] += add;
-                if (dirty) {
-                    const f32x16 poison = times_zero(vr, r0);
-                    const Seen to = {opaque(seen[a].low - k0 - 4 * h), seen[a].count};
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (sees(to, 8 * (i >> 2) + (i & 3))) s[a][i] += poison[i];
-                }
-                pf[a][0] = E::of(s[a], 0);
-                pf[a][1] = E::of(s[a], 1);
-            }
-            if (!dirty) {
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const Frag vf = TL::columns(vc, r0 + 16 * u, c);
-#pragma unroll
-                        for (int a = 0; a < QB; ++a) acc[a][c] = E::mma(vf, pf[a][u], acc[a][c]);
-                    }
-            } else {
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const Frag vf = E::finite(TL::columns(vc, r0 + 16 * u, c));
-#pragma unroll
-                        for (int a = 0; a < QB; ++a) acc[a][c] = E::mma(vf, pf[a][u], acc[a][c]);
-                    }
-            }
+        kt = at + buffer * 2 * TILE;
+    };
+    auto some = [&](int end) __attribute__((always_inline)) {
+        for (; t < end; ++t) {
+            uint32_t kt;
+            next(kt);
+#pragma unroll 1
+            for (int e = 0; e < KB; ++e) some_seen(0, t * KT + rw + 32 * e, kt + (rw + 32 * e) * TL::ROW, kt + TILE + (rw + 32 * e) * TL::ROW);
         }
+    };
+    int from = (full_low - rw + KT - 1) / KT, to = (full_high + 1 - rw - 32 * KB) / KT + 1;  // whole tiles from .. to - 1
+    from = max(from, first_tile);
+    to = min(full_high + 1 < rw + 32 * KB ? first_tile : to, end_tile);
+    if (low == INT32_MAX || from >= to) from = to = end_tile;
+    if (first_tile < end_tile) load_tile(first_tile, 0);
+    some(min(from, end_tile));
+    for (; t < to; ++t) {
+        uint32_t kt;
+        next(kt);
+        all_seen(0, kt + rw * TL::ROW, kt + TILE + rw * TL::ROW);
     }
+    some(end_tile);
 #pragma unroll
-    for (int a = 0; a < QB; ++a) sum[a] += __shfl_xor(sum[a], 32, 64);
+    for (int a = 0; a < QB; ++a) sum[a] = halves<false>(sum[a]);
 
     // a row of the sums
     auto index = [&](int a) { return (static_cast<long>(b) * p.H + head[a]) * p.Tq + token[a]; };
@@ -459,7 +545,7 @@ Plan plan(bool bf16, int d, long heads, long rows, long keys) {
         p.qb = 1;
         p.wk = wide ? 2 : 4;
     } else {
-        p.qb = bf16 && rows > 128 ? 2 : 1;
+        p.qb = 1;
         p.wk = 1;
     }
     p.rows = 32 * p.qb * (4 / p.wk);
@@ -485,8 +571,7 @@ hipError_t launch_kind(const FwdParams& p, const Plan& pl, long groups, hipStrea
     constexpr bool wide = !BF16 && D == 128;
     constexpr int WK = wide ? 2 : 4, KT_FEW = wide ? 64 : 128, KT = wide ? 32 : 64;
     if (pl.wk > 1) attn_fwd_kernel<BF16, D, 1, WK, KT_FEW, PAGED><<<grid, block, 0, stream>>>(p);
-    else if (pl.qb == 1) attn_fwd_kernel<BF16, D, 1, 1, KT, PAGED><<<grid, block, 0, stream>>>(p);
-    else if constexpr (BF16) attn_fwd_kernel<BF16, D, 2, 1, KT, PAGED><<<grid, block, 0, stream>>>(p);
+    else attn_fwd_kernel<BF16, D, 1, 1, KT, PAGED><<<grid, block, 0, stream>>>(p);
     return hipGetLastError();
 }
 
