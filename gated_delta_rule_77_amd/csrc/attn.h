@@ -97,6 +97,14 @@ struct Tile {
         if constexpr (CHUNKS >= 16) return ((r & 3) << 2) | ((r >> 2) & 3);
         return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);  // two rows share the banks' width
     }
+    // A wave's load of 16 bytes a lane fills rows n ROWS_PER_DMA .. of a tile: what lane l
+    // takes, row l / CHUNKS of them, chunk lane_chunk(l) ^ swizzle(n ROWS_PER_DMA) (the
+    // swizzle moves bits, so that of a sum of rows without carries is its parts').
+    static __device__ __forceinline__ uint32_t lane_chunk(int lane) { return (lane % CHUNKS) ^ swizzle(lane / CHUNKS); }
+    // its offset from the row n ROWS_PER_DMA, for rows `stride` bytes apart: part = lane / CHUNKS * stride
+    static __device__ __forceinline__ uint32_t lane_offset(uint32_t part, uint32_t chunk, int n) {
+        return part + ((chunk ^ swizzle(n * ROWS_PER_DMA)) << 4);
+    }
     // where chunk c of row r lies
     static __device__ __forceinline__ int at(int r, int chunk) { return r * ROW + ((chunk ^ swizzle(r)) << 4); }
 
@@ -169,8 +177,16 @@ __device__ __forceinline__ const char* uniform(const char* p) {
 __device__ __forceinline__ void to_lds(const char* base, uint32_t offset, uint32_t dst) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform(dst)), "v"(offset), "s"(uniform(base)) : "memory");
 }
-__device__ __forceinline__ void to_lds4(const void* src, uint32_t dst) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(uniform(dst)), "v"(src) : "memory");
+__device__ __forceinline__ void to_lds4(const void* base, uint32_t offset, uint32_t dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(uniform(dst)), "v"(offset),
+                 "s"(uniform(static_cast<const char*>(base)))
+                 : "memory");
+}
+// The same but for the last N loads.  The compiler does not see this wait: its own loads
+// have to have landed before.
+template <int N>
+__device__ __forceinline__ void landed_but() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void landed() {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");

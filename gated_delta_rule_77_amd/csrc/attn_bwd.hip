@@ -19,7 +19,7 @@ namespace {
 using namespace attn;
 
 constexpr int kThreads = 256;
-constexpr int kQueries = 64;  // of a tile in the pass over keys' gradients
+constexpr int kQueries = 32;  // of a tile in the pass over keys' gradients
 
 struct View4 {
     const void* p;
@@ -35,7 +35,7 @@ struct BwdParams {
     Out4 dq, dk, dv;
     const float* lse;
     const int32_t* first;
-    float* delta;          // D: [B,H,Tq]
+    float *delta, *lse2;   // D, and lse in powers of two: [B,H,Tq]
     uint16_t* do16;        // bf16 copy of an fp32 dO, [B,H,Tq,D]; else null
     int* first_range;      // [B][tiles of queries][2]: least and largest `first`; null without
     int H, Hk, shared;
@@ -50,7 +50,7 @@ struct BwdParams {
 // The least and largest first key of each tile of queries.
 __global__ void __launch_bounds__(64) first_range_kernel(const int32_t* first, int Tq, int tiles, int* out) {
     const int b = blockIdx.x / tiles, t = blockIdx.x - b * tiles;
-    const int i = min(t * kQueries + static_cast<int>(threadIdx.x), Tq - 1);
+    const int i = min(t * kQueries + static_cast<int>(threadIdx.x % kQueries), Tq - 1);
     const int f = first[static_cast<long>(b) * Tq + i];
     const int lo = wave_min_i(f), hi = wave_max_i(f);
     if (threadIdx.x == 0) {
@@ -138,7 +138,10 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
         }
         delta[a] = dot + __shfl_xor(dot, 32, 64);
         lse2[a] = p.lse[row] * kLog2e;
-        if (stored[a] && h == 0) p.delta[row] = delta[a];
+        if (stored[a] && h == 0) {
+            p.delta[row] = delta[a];
+            p.lse2[row] = lse2[a];
+        }
     }
     low = uniform(wave_min_i(low));
     high = uniform(wave_max_i(high));
@@ -153,16 +156,30 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
     const int all_high = uniform(max(max(bounds[1][0], bounds[1][1]), max(bounds[1][2], bounds[1][3])));
     const int first_tile = all_low / KT, end_tile = all_high < 0 ? first_tile : all_high / KT + 1;
 
+    const uint32_t at = lds_address(smem), row_base = TL::row_base(lane), column_base = TL::column_base(lane);
+
+    // as in the forward
+    constexpr int RPD = TL::ROWS_PER_DMA;
+    const uint32_t chunk = TL::lane_chunk(lane);
+    const uint32_t k_part = static_cast<uint32_t>(lane / TL::CHUNKS * p.k.st * E::BYTES), v_part = static_cast<uint32_t>(lane / TL::CHUNKS * p.v.st * E::BYTES);
     auto load_tile = [&](int t, int buffer) __attribute__((always_inline)) {
-        const uint32_t kd = lds_address(smem) + buffer * 2 * TILE;
+        const uint32_t dst = at + buffer * 2 * TILE + wave * DMAS * 1024;
+        if (t * KT + KT <= nk) {
 #pragma unroll
-        for (int i = 0; i < DMAS; ++i) {
-            const int n = wave * DMAS + i;
-            const int r = n * TL::ROWS_PER_DMA + lane / TL::CHUNKS;
-            const int chunk = (lane % TL::CHUNKS) ^ TL::swizzle(r);
-            const long key = min(t * KT + r, nk - 1);  // keys behind the last repeat it, unseen
-            to_lds(kb + key * p.k.st * E::BYTES + 16 * chunk, kd + n * 1024);
-            to_lds(vb + key * p.v.st * E::BYTES + 16 * chunk, kd + TILE + n * 1024);
+            for (int i = 0; i < DMAS; ++i) {
+                const int n = wave * DMAS + i;
+                const long key = t * KT + n * RPD;
+                to_lds(kb + key * p.k.st * E::BYTES, TL::lane_offset(k_part, chunk, n), dst + i * 1024);
+                to_lds(vb + key * p.v.st * E::BYTES, TL::lane_offset(v_part, chunk, n), dst + TILE + i * 1024);
+            }
+        } else {  // keys behind the last repeat it, unseen
+#pragma unroll
+            for (int i = 0; i < DMAS; ++i) {
+                const int n = wave * DMAS + i;
+                const long key = min(t * KT + n * RPD + lane / TL::CHUNKS, nk - 1);
+                to_lds(kb + key * p.k.st * E::BYTES + TL::lane_offset(0, chunk, n), dst + i * 1024);
+                to_lds(vb + key * p.v.st * E::BYTES + TL::lane_offset(0, chunk, n), dst + TILE + i * 1024);
+            }
         }
     };
 
@@ -174,82 +191,94 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[a][c][i] = 0.0f;
 
-    const uint32_t at = lds_address(smem), row_base = TL::row_base(lane), column_base = TL::column_base(lane);
-    if (first_tile < end_tile) load_tile(first_tile, 0);
-    for (int t = first_tile; t < end_tile; ++t) {
+    // A block of 32 keys.  `partly`: some rows may not see all of them.  A key that is not
+    // finite gives scores that are not: it is taken out of the product for those that do not
+    // see it, and those that do have them from P.
+    auto block = [&](int k0, uint32_t kt, auto partly) __attribute__((always_inline)) {
+        constexpr bool PARTLY = decltype(partly)::value;
+        const uint32_t kr = kt + row_base, kc = kt + column_base, vr = kr + TILE;
+        f32x16 s[QB], dp[QB];
+#pragma unroll
+        for (int a = 0; a < QB; ++a)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[a][i] = dp[a][i] = 0.0f;
+#pragma unroll
+        for (int st = 0; st < S; ++st) {
+            const Frag kf = TL::rows(kr, 0, st);
+#pragma unroll
+            for (int a = 0; a < QB; ++a) s[a] = E::mma(kf, q[a][st], s[a]);
+        }
+#pragma unroll
+        for (int st = 0; st < S; ++st) {
+            const Frag vf = TL::rows(vr, 0, st);
+#pragma unroll
+            for (int a = 0; a < QB; ++a) dp[a] = E::mma(vf, dof[a][st], dp[a]);
+        }
+        bool dirty = false;
+        if constexpr (PARTLY) {
+            bool any = false;
+#pragma unroll
+            for (int a = 0; a < QB; ++a)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) any |= !(fabsf(s[a][i]) < INFINITY);
+            dirty = __ballot(any) != 0;
+        }
+        Frag df[QB][2];
+#pragma unroll
+        for (int a = 0; a < QB; ++a) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[a][i] = ex2(fmaf(s[a][i], p.c, -lse2[a])) * (dp[a][i] - delta[a]);
+            if constexpr (PARTLY) {
+                const Seen to = {opaque(seen[a].low - k0 - 4 * h), seen[a].count};
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (!sees(to, 8 * (i >> 2) + (i & 3))) s[a][i] = 0.0f;
+            }
+            df[a][0] = E::of(s[a], 0);
+            df[a][1] = E::of(s[a], 1);
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                Frag kf = TL::columns(kc, 16 * u, c);
+                if constexpr (PARTLY)
+                    if (dirty) kf = E::finite(kf);
+#pragma unroll
+                for (int a = 0; a < QB; ++a) acc[a][c] = E::mma(kf, df[a][u], acc[a][c]);
+            }
+    };
+
+    int t = first_tile;
+    auto next = [&](uint32_t& kt) __attribute__((always_inline)) {
         const int buffer = (t - first_tile) & 1;
         landed();
         __syncthreads();
         if (t + 1 < end_tile) load_tile(t + 1, buffer ^ 1);
-        const uint32_t kt = at + buffer * 2 * TILE, kr = kt + row_base, kc = kt + column_base, vr = kt + TILE + row_base;
-#pragma unroll
-        for (int kbk = 0; kbk < KB; ++kbk) {
-            const int r0 = 32 * kbk, k0 = t * KT + r0;
-            if (k0 > high || k0 + 31 < low) continue;
-            const bool partly = k0 < full_low || k0 + 31 > full_high;
-            f32x16 s[QB], dp[QB];
-#pragma unroll
-            for (int a = 0; a < QB; ++a)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s[a][i] = dp[a][i] = 0.0f;
-#pragma unroll
-            for (int st = 0; st < S; ++st) {
-                const Frag kf = TL::rows(kr, r0, st);
-#pragma unroll
-                for (int a = 0; a < QB; ++a) s[a] = E::mma(kf, q[a][st], s[a]);
-            }
-#pragma unroll
-            for (int st = 0; st < S; ++st) {
-                const Frag vf = TL::rows(vr, r0, st);
-#pragma unroll
-                for (int a = 0; a < QB; ++a) dp[a] = E::mma(vf, dof[a][st], dp[a]);
-            }
-            bool dirty = false;
-            if (partly) {
-                // a key that is not finite gives scores that are not: it is taken out of the
-                // product for those that do not see it, and those that do have them from P
-                bool any = false;
-#pragma unroll
-                for (int a = 0; a < QB; ++a)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) any |= !(fabsf(s[a][i]) < INFINITY);
-                dirty = __ballot(any) != 0;
-            }
-            Frag df[QB][2];
-#pragma unroll
-            for (int a = 0; a < QB; ++a) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s[a][i] = ex2(fmaf(s[a][i], p.c, -lse2[a])) * (dp[a][i] - delta[a]);
-                if (partly) {
-                    const Seen to = {opaque(seen[a].low - k0 - 4 * h), seen[a].count};
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (!sees(to, 8 * (i >> 2) + (i & 3))) s[a][i] = 0.0f;
-                }
-                df[a][0] = E::of(s[a], 0);
-                df[a][1] = E::of(s[a], 1);
-            }
-            if (!dirty) {
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const Frag kf = TL::columns(kc, r0 + 16 * u, c);
-#pragma unroll
-                        for (int a = 0; a < QB; ++a) acc[a][c] = E::mma(kf, df[a][u], acc[a][c]);
-                    }
-            } else {
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const Frag kf = E::finite(TL::columns(kc, r0 + 16 * u, c));
-#pragma unroll
-                        for (int a = 0; a < QB; ++a) acc[a][c] = E::mma(kf, df[a][u], acc[a][c]);
-                    }
+        kt = at + buffer * 2 * TILE;
+    };
+    auto some = [&](int end) __attribute__((always_inline)) {
+        for (; t < end; ++t) {
+            uint32_t kt;
+            next(kt);
+#pragma unroll 1
+            for (int e = 0; e < KB; ++e) {
+                const int k0 = t * KT + 32 * e;
+                if (k0 <= high && k0 + 31 >= low) block(k0, kt + 32 * e * TL::ROW, std::true_type());
             }
         }
+    };
+    int from = max((full_low + KT - 1) / KT, first_tile), to = min((full_high + 1) / KT, end_tile);  // whole tiles
+    if (low == INT32_MAX || from >= to) from = to = end_tile;
+    if (first_tile < end_tile) load_tile(first_tile, 0);
+    some(min(from, end_tile));
+    for (; t < to; ++t) {
+        uint32_t kt;
+        next(kt);
+#pragma unroll
+        for (int e = 0; e < KB; ++e) block(0, kt + 32 * e * TL::ROW, std::false_type());
     }
+    some(end_tile);
 #pragma unroll
     for (int a = 0; a < QB; ++a) {
         if (!stored[a]) continue;
@@ -267,15 +296,16 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
 }
 
 template <bool BF16, int D, int KB>
-__global__ void __launch_bounds__(kThreads, BF16 && KB * D == 64 ? 2 : 1) attn_dkv_kernel(BwdParams p) {
+__global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dkv_kernel(BwdParams p) {
     using E = El<BF16>;
     using TL = Tile<BF16, D>;
     typedef typename E::Frag Frag;
     constexpr int KEYS = 128 * KB, QT = kQueries;
     constexpr int S = D / 16, C = D / 32;
     constexpr int TILE = QT * TL::ROW, DMAS = QT / TL::ROWS_PER_DMA / 4;
-    __shared__ __align__(1024) char smem[4 * TILE];
-    __shared__ __align__(16) float stats[2][3][QT];  // of a tile's queries: lse, D, first key
+    constexpr int VALUES = KEYS * TL::ROW, V_DMAS = KEYS / TL::ROWS_PER_DMA / 4;
+    __shared__ __align__(1024) char smem[4 * TILE + VALUES];  // two tiles of queries and dO, the keys' values
+    __shared__ __align__(16) float stats[2][3][64];  // of a tile's queries (QT of them): lse, D, first key
     __shared__ int range[2][4];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -288,17 +318,14 @@ __global__ void __launch_bounds__(kThreads, BF16 && KB * D == 64 ? 2 : 1) attn_d
 
     // this lane's keys; those behind the last repeat it, unstored and unseen
     int key[KB];
-    Frag k[KB][S], v[KB][S];
+    Frag k[KB][S];
 #pragma unroll
     for (int a = 0; a < KB; ++a) {
         key[a] = key0 + 32 * (wave * KB + a) + (lane & 31);
         const long j = min(key[a], nk - 1);
-        const long ka = b * p.k.sb + hk * p.k.sh + j * p.k.st, va = b * p.v.sb + hk * p.v.sh + j * p.v.st;
+        const long ka = b * p.k.sb + hk * p.k.sh + j * p.k.st;
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            k[a][s] = E::load(p.k.p, ka + 16 * s + 8 * h);
-            v[a][s] = E::load(p.v.p, va + 16 * s + 8 * h);
-        }
+        for (int s = 0; s < S; ++s) k[a][s] = E::load(p.k.p, ka + 16 * s + 8 * h);
     }
 
     // the tiles of queries that see some of these keys
@@ -325,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, BF16 && KB * D == 64 ? 2 : 1) attn_d
     begin = uniform(begin);
     end = uniform(end);
 
+    if (!p.first && tid < 64) stats[0][2][tid] = stats[1][2][tid] = __int_as_float(INT32_MIN);  // before the first barrier
     f32x16 dk[KB][C], dv[KB][C];
 #pragma unroll
     for (int a = 0; a < KB; ++a)
@@ -333,135 +361,192 @@ __global__ void __launch_bounds__(kThreads, BF16 && KB * D == 64 ? 2 : 1) attn_d
 #pragma unroll
             for (int i = 0; i < 16; ++i) dk[a][c][i] = dv[a][c][i] = 0.0f;
 
+    const uint32_t at = lds_address(smem), row_base = TL::row_base(lane), column_base = TL::column_base(lane);
     const bool copied = BF16 && p.o_f32;
-    auto load_tile = [&](int g, int t, int buffer) __attribute__((always_inline)) {
-        const int head = hk * p.shared + g;
-        const char* qb = static_cast<const char*>(p.q.p) + (b * p.q.sb + head * p.q.sh) * E::BYTES;
-        const char* db = copied ? reinterpret_cast<const char*>(p.do16 + (static_cast<long>(b) * p.H + head) * nq * D)
-                                : static_cast<const char*>(p.d_o.p) + (b * p.d_o.sb + head * p.d_o.sh) * E::BYTES;
-        const long ds = copied ? D : p.d_o.st;
-        const uint32_t qd = lds_address(smem) + buffer * 2 * TILE;
+    constexpr int RPD = TL::ROWS_PER_DMA;
+    const long d_st = copied ? D : p.d_o.st;
+    auto load_values = [&]() __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < DMAS; ++i) {
-            const int n = wave * DMAS + i;
-            const int r = n * TL::ROWS_PER_DMA + lane / TL::CHUNKS;
-            const int chunk = (lane % TL::CHUNKS) ^ TL::swizzle(r);
-            const long row = min(t * QT + r, nq - 1);  // queries behind the last repeat it, unseen
-            to_lds(qb + row * p.q.st * E::BYTES + 16 * chunk, qd + n * 1024);
-            to_lds(db + row * ds * E::BYTES + 16 * chunk, qd + TILE + n * 1024);
+        for (int i = 0; i < V_DMAS; ++i) {
+            const int n = wave * V_DMAS + i;
+            const long j = min(key0 + n * RPD + lane / TL::CHUNKS, nk - 1);
+            const char* vb = static_cast<const char*>(p.v.p) + (b * p.v.sb + hk * p.v.sh + j * p.v.st) * E::BYTES;
+            to_lds(vb + TL::lane_offset(0, TL::lane_chunk(lane), n), at + 4 * TILE + n * 1024);
         }
-        const int i = min(t * QT + lane, nq - 1);
-        const long row = (static_cast<long>(b) * p.H + head) * nq + i;
-        if (wave == 0) to_lds4(p.lse + row, lds_address(&stats[buffer][0][0]));
-        if (wave == 1) to_lds4(p.delta + row, lds_address(&stats[buffer][1][0]));
-        if (wave == 2 && p.first) to_lds4(p.first + static_cast<long>(b) * nq + i, lds_address(&stats[buffer][2][0]));
+    };
+    // of the next tile's head: its queries, dO and their sums
+    const char* q_head = static_cast<const char*>(p.q.p) + (b * p.q.sb + hk * p.shared * p.q.sh) * E::BYTES;
+    const char* d_head = copied ? reinterpret_cast<const char*>(p.do16) + (static_cast<long>(b) * p.H + hk * p.shared) * nq * D * 2
+                                : static_cast<const char*>(p.d_o.p) + (b * p.d_o.sb + hk * p.shared * p.d_o.sh) * E::BYTES;
+    const long q_step = p.q.sh * E::BYTES, d_step = copied ? static_cast<long>(nq) * D * 2 : p.d_o.sh * E::BYTES;
+    const long q_row = p.q.st * E::BYTES, d_row = d_st * E::BYTES;
+    // of its sums: this wave's are lse (wave 0), D (1) or first keys (2)
+    const long sums = (static_cast<long>(b) * p.H + hk * p.shared) * nq;
+    const char* s_head = reinterpret_cast<const char*>(wave == 0 ? p.lse2 + sums : wave == 1 ? p.delta + sums : nullptr);
+    const long s_step = wave < 2 ? 4L * nq : 0;
+    if (wave == 2 && p.first) s_head = reinterpret_cast<const char*>(p.first + static_cast<long>(b) * nq);
+    auto load_tile = [&](int t, int buffer) __attribute__((always_inline)) {
+        const uint32_t dst = at + buffer * 2 * TILE + wave * DMAS * 1024;
+        const int ln = opaque(lane), r = ln / TL::CHUNKS;
+        const uint32_t chunk = TL::lane_chunk(ln), q_part = r * static_cast<uint32_t>(q_row), d_part = r * static_cast<uint32_t>(d_row);
+        if (t * QT + QT <= nq) {
+#pragma unroll
+            for (int i = 0; i < DMAS; ++i) {
+                const int n = wave * DMAS + i;
+                const long row = t * QT + n * RPD;
+                to_lds(q_head + row * q_row, TL::lane_offset(q_part, chunk, n), dst + i * 1024);
+                to_lds(d_head + row * d_row, TL::lane_offset(d_part, chunk, n), dst + TILE + i * 1024);
+            }
+        } else {  // queries behind the last repeat it, unseen
+#pragma unroll
+            for (int i = 0; i < DMAS; ++i) {
+                const int n = wave * DMAS + i;
+                const long row = min(t * QT + n * RPD + r, nq - 1);
+                to_lds(q_head + row * q_row + TL::lane_offset(0, chunk, n), dst + i * 1024);
+                to_lds(d_head + row * d_row + TL::lane_offset(0, chunk, n), dst + TILE + i * 1024);
+            }
+        }
+        if (s_head) to_lds4(s_head + 4L * QT * t, 4 * min(ln, nq - 1 - t * QT), lds_address(&stats[buffer][wave][0]));
     };
 
-    const uint32_t at = lds_address(smem), row_base = TL::row_base(lane), column_base = TL::column_base(lane);
-    const int count = end > begin ? (end - begin) * p.shared : 0;
-    int g = 0, t = begin;
-    if (count > 0) load_tile(0, begin, 0);
-    for (int n = 0; n < count; ++n) {
-        const int buffer = n & 1;
-        landed();
-        __syncthreads();
-        const int now = t;
-        if (++t == end) {
-            t = begin;
-            ++g;
-        }
-        if (n + 1 < count) load_tile(g, t, buffer ^ 1);
-        const uint32_t qt = at + buffer * 2 * TILE, qr = qt + row_base, qc = qt + column_base, dr = qr + TILE, dc = qc + TILE;
-        const int w0 = key0 + 32 * KB * wave, w1 = w0 + 32 * KB - 1;  // this wave's keys
-        // whether queries and keys all see each other; some do
-        const bool packed = p.first && p.first_range[2 * (b * p.query_tiles + now) + 1] > w0;
+    // A block of 32 queries from i0.  `partly`: some may not see all of the wave's keys; queries
+    // and their dO that are not finite are then taken out of the products for keys that they
+    // do not see, and reach the others through P and D.
+    auto block = [&](int i0, uint32_t qt, const float* lses, auto partly) __attribute__((always_inline)) {
+        constexpr bool PARTLY = decltype(partly)::value;
+        // (nothing that follows from the lane stays from block to block: there is no register for it)
+        const uint32_t row = opaque(row_base), column = opaque(column_base);
+        const uint32_t qr = qt + row, qc = qt + column, dr = qr + TILE, dc = qc + TILE;
+        const uint32_t vr = at + 4 * TILE + 32 * KB * wave * TL::ROW + row;
+        const float* deltas = lses + 64;
+        f32x16 s[KB], dp[KB];
 #pragma unroll
-        for (int rb = 0; rb < QT / 32; ++rb) {
-            const int r0 = 32 * rb, i0 = now * QT + r0, p0 = i0 + off;
-            if (i0 >= nq || p0 + 31 < w0 || (p.window > 0 && p0 - p.window >= w1)) continue;
-            const bool partly = packed || i0 + 31 >= nq || p0 < w1 || (p.window > 0 && p0 + 31 - p.window >= w0);
-            f32x16 s[KB], dp[KB];
+        for (int a = 0; a < KB; ++a)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[a][i] = dp[a][i] = 0.0f;
+#pragma unroll
+        for (int st = 0; st < S; ++st) {
+            const Frag f = TL::rows(qr, 0, st);
+#pragma unroll
+            for (int a = 0; a < KB; ++a) s[a] = E::mma(f, k[a][st], s[a]);
+        }
+#pragma unroll
+        for (int st = 0; st < S; ++st) {
+            const Frag f = TL::rows(dr, 0, st);
+#pragma unroll
+            for (int a = 0; a < KB; ++a) dp[a] = E::mma(f, TL::rows(vr, 32 * a, st), dp[a]);
+        }
+        bool dirty = false;
+        if constexpr (PARTLY) {
+            bool any = false;
 #pragma unroll
             for (int a = 0; a < KB; ++a)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s[a][i] = dp[a][i] = 0.0f;
+                for (int i = 0; i < 16; ++i) any |= !(fabsf(s[a][i]) < INFINITY) || !(fabsf(dp[a][i]) < INFINITY);
+            dirty = __ballot(any) != 0;
+        }
+        Frag pf[KB][2], df[KB][2];
 #pragma unroll
-            for (int st = 0; st < S; ++st) {
-                const Frag f = TL::rows(qr, r0, st);
+        for (int a = 0; a < KB; ++a) {
 #pragma unroll
-                for (int a = 0; a < KB; ++a) s[a] = E::mma(f, k[a][st], s[a]);
+            for (int e = 0; e < 4; ++e) {
+                const f32x4 lse = *reinterpret_cast<const f32x4*>(lses + 8 * e + 4 * h);
+                const f32x4 dl = *reinterpret_cast<const f32x4*>(deltas + 8 * e + 4 * h);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int x = 4 * e + i;
+                    s[a][x] = ex2(fmaf(s[a][x], p.c, -lse[i]));
+                    dp[a][x] = s[a][x] * (dp[a][x] - dl[i]);
+                    if constexpr (PARTLY)
+                        if (dirty) s[a][x] += 0.0f * dl[i];
+                }
             }
-#pragma unroll
-            for (int st = 0; st < S; ++st) {
-                const Frag f = TL::rows(dr, r0, st);
-#pragma unroll
-                for (int a = 0; a < KB; ++a) dp[a] = E::mma(f, v[a][st], dp[a]);
-            }
-            bool dirty = false;
-            if (partly) {
-                // as for dq: queries and their dO that are not finite are taken out of the
-                // products for keys they do not see, and reach the others through P and D
-                bool any = false;
-#pragma unroll
-                for (int a = 0; a < KB; ++a)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) any |= !(fabsf(s[a][i]) < INFINITY) || !(fabsf(dp[a][i]) < INFINITY);
-                dirty = __ballot(any) != 0;
-            }
-            Frag pf[KB][2], df[KB][2];
-#pragma unroll
-            for (int a = 0; a < KB; ++a) {
+            if constexpr (PARTLY) {
+                // query r of the block sees the key from r = from on, to the window's end, and
+                // where its first key is not behind it
+                const int from = opaque(key[a] - off - i0 - 4 * h);
+                int to = nq - i0 - 4 * h;
+                if (p.window > 0) to = min(to, from + p.window);
+                if (key[a] >= nk) to = INT32_MIN;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const f32x4 lse = *reinterpret_cast<const f32x4*>(&stats[buffer][0][r0 + 8 * e + 4 * h]);
-                    const f32x4 dl = *reinterpret_cast<const f32x4*>(&stats[buffer][1][r0 + 8 * e + 4 * h]);
+                    const f32x4 first = *reinterpret_cast<const f32x4*>(deltas + 64 + 8 * e + 4 * h);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int x = 4 * e + i;
-                        s[a][x] = ex2(fmaf(s[a][x], p.c, -lse[i] * kLog2e));
-                        dp[a][x] = s[a][x] * (dp[a][x] - dl[i]);
-                        if (dirty) s[a][x] += 0.0f * dl[i];
-                    }
-                }
-                if (partly) {
-                    // query r of the block sees the key from r = from on, to the window's end
-                    const int from = opaque(key[a] - p0 - 4 * h);
-                    int to = nq - i0 - 4 * h;
-                    if (p.window > 0) to = min(to, from + p.window);
-                    if (key[a] >= nk) to = INT32_MIN;
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                        const int r = 8 * (x >> 2) + (x & 3);
-                        bool seen = r >= from && r < to;
-                        if (packed) seen = seen && __float_as_int(stats[buffer][2][r0 + r + 4 * h]) <= key[a];
+                        const int x = 4 * e + i, r = 8 * e + i;
+                        const bool seen = (r >= from) & (r < to) & (__float_as_int(first[i]) <= key[a]);
                         if (!seen) s[a][x] = dp[a][x] = 0.0f;
                     }
                 }
+            }
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    pf[a][u] = E::of(s[a], u);
-                    df[a][u] = E::of(dp[a], u);
+            for (int u = 0; u < 2; ++u) {
+                pf[a][u] = E::of(s[a], u);
+                df[a][u] = E::of(dp[a], u);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                Frag x = TL::columns(dc, 16 * u, c), y = TL::columns(qc, 16 * u, c);
+                if constexpr (PARTLY)
+                    if (dirty) {
+                        x = E::finite(x);
+                        y = E::finite(y);
+                    }
+#pragma unroll
+                for (int a = 0; a < KB; ++a) {
+                    dv[a][c] = E::mma(x, pf[a][u], dv[a][c]);
+                    dk[a][c] = E::mma(y, df[a][u], dk[a][c]);
                 }
             }
-            auto products = [&](auto clean) __attribute__((always_inline)) {
+    };
+
+    // The tiles of each head in turn; runs of those whose queries all see all of the wave's
+    // keys in a loop of their own.
+    const int w0 = key0 + 32 * KB * wave, w1 = w0 + 32 * KB - 1;  // this wave's keys
+    const int count = end > begin ? (end - begin) * p.shared : 0;
+    int n = 0, t = begin, i0 = 0, buffer = 1;  // the next tile; the present one's first query and place
+    bool partly = false;
+    auto next = [&]() __attribute__((always_inline)) {
+        landed();
+        if (n == count) {
+            n = count + 1;  // none is left
+            return;
+        }
+        i0 = t * QT;
+        buffer ^= 1;
+        __syncthreads();
+        if (++t == end) {
+            t = begin;
+            q_head += q_step;
+            d_head += d_step;
+            s_head += s_step;
+        }
+        if (++n < count) load_tile(t, buffer ^ 1);
+        const int p0 = i0 + off;
+        partly = i0 + QT > nq || p0 < w1 || (p.window > 0 && p0 + QT - 1 - p.window >= w0) ||
+                 (p.first && __ballot(__float_as_int(stats[buffer][2][lane % QT]) > w0) != 0);
+    };
+    if (count > 0) {
+        load_values();
+        load_tile(begin, 0);
+    }
+    next();
+    while (n <= count && count > 0) {
+        for (; n <= count && partly; next()) {
+#pragma unroll 1
+            for (int e = 0; e < QT / 32; ++e) {
+                const int i = i0 + 32 * e, p0 = i + off;
+                if (i < nq && p0 + 31 >= w0 && !(p.window > 0 && p0 - p.window >= w1))
+                    block(i, at + buffer * 2 * TILE + 32 * e * TL::ROW, &stats[buffer][0][32 * e], std::true_type());
+            }
+        }
+        for (; n <= count && !partly; next()) {
 #pragma unroll
-                for (int c = 0; c < C; ++c)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        Frag x = TL::columns(dc, r0 + 16 * u, c), y = TL::columns(qc, r0 + 16 * u, c);
-                        if constexpr (decltype(clean)::value) {
-                            x = E::finite(x);
-                            y = E::finite(y);
-                        }
-#pragma unroll
-                        for (int a = 0; a < KB; ++a) {
-                            dv[a][c] = E::mma(x, pf[a][u], dv[a][c]);
-                            dk[a][c] = E::mma(y, df[a][u], dk[a][c]);
-                        }
-                    }
-            };
-            if (!dirty) products(std::false_type());
-            else products(std::true_type());
+            for (int e = 0; e < QT / 32; ++e)
+                block(0, at + buffer * 2 * TILE + 32 * e * TL::ROW, &stats[buffer][0][32 * e], std::false_type());
         }
     }
 #pragma unroll
@@ -485,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, BF16 && KB * D == 64 ? 2 : 1) attn_d
 }
 
 struct Layout {
-    size_t delta, do16, first_range, bytes;  // offsets in the workspace
+    size_t delta, lse2, do16, first_range, bytes;  // offsets in the workspace
 };
 
 size_t up256(size_t n) { return (n + 255) & ~size_t{255}; }
@@ -496,7 +581,8 @@ Layout layout(const pdn_attn_bwd_args& a) {
     const pdn_attn_args& f = a.fwd;
     const size_t rows = static_cast<size_t>(f.B) * f.H * f.Tq;
     Layout l{};
-    l.do16 = up256(rows * sizeof(float));
+    l.lse2 = up256(rows * sizeof(float));
+    l.do16 = 2 * l.lse2;
     l.first_range = l.do16 + (f.dtype == PDN_BF16 && f.o_dtype == PDN_F32 ? up256(rows * f.d * 2) : 0);
     l.bytes = l.first_range + (f.first ? up256(static_cast<size_t>(f.B) * query_tiles(f.Tq) * 2 * sizeof(int)) : 0);
     return l;
@@ -539,6 +625,7 @@ hipError_t launch_attn_bwd(const pdn_attn_bwd_args& a, hipStream_t stream) {
     p.lse = f.lse;
     p.first = f.first;
     p.delta = reinterpret_cast<float*>(ws + l.delta);
+    p.lse2 = reinterpret_cast<float*>(ws + l.lse2);
     p.do16 = reinterpret_cast<uint16_t*>(ws + l.do16);
     p.first_range = reinterpret_cast<int*>(ws + l.first_range);
     p.H = f.H;

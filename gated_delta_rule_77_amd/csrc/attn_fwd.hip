@@ -146,13 +146,8 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
     // chunk swizzled.  Such rows lie at one stride from a uniform address, on one page of a
     // cache too; those of a tile that passes the last key repeat it, unseen.
     constexpr int RPD = TL::ROWS_PER_DMA;
-    uint32_t k_off[DMAS], v_off[DMAS];
-#pragma unroll
-    for (int i = 0; i < DMAS; ++i) {
-        const int r = lane / TL::CHUNKS, chunk = (lane % TL::CHUNKS) ^ TL::swizzle((wave * DMAS + i) * RPD + r);
-        k_off[i] = static_cast<uint32_t>(r * p.k_st * E::BYTES) + 16 * chunk;
-        v_off[i] = static_cast<uint32_t>(r * p.v_st * E::BYTES) + 16 * chunk;
-    }
+    const uint32_t chunk = TL::lane_chunk(lane);
+    const uint32_t k_part = static_cast<uint32_t>(lane / TL::CHUNKS * p.k_st * E::BYTES), v_part = static_cast<uint32_t>(lane / TL::CHUNKS * p.v_st * E::BYTES);
     auto place = [&](int key, long& ko, long& vo) __attribute__((always_inline)) {
         if constexpr (PAGED) {
             const long page = page_of(p.map, b, key);
@@ -171,18 +166,19 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
             for (int i = 0; i < DMAS; ++i) {
                 long ko, vo;
                 place(uniform(t * KT + (wave * DMAS + i) * RPD), ko, vo);
-                to_lds(kb + ko * E::BYTES, k_off[i], dst + i * 1024);
-                to_lds(vb + vo * E::BYTES, v_off[i], dst + TILE + i * 1024);
+                to_lds(kb + ko * E::BYTES, TL::lane_offset(k_part, chunk, wave * DMAS + i), dst + i * 1024);
+                to_lds(vb + vo * E::BYTES, TL::lane_offset(v_part, chunk, wave * DMAS + i), dst + TILE + i * 1024);
             }
             return;
         }
 #pragma unroll
         for (int i = 0; i < DMAS; ++i) {
-            const int r = (wave * DMAS + i) * RPD + lane / TL::CHUNKS, chunk = (lane % TL::CHUNKS) ^ TL::swizzle(r);
+            const int n = wave * DMAS + i;
+            const uint32_t in_row = TL::lane_offset(0, chunk, n);
             long ko, vo;
-            place(min(t * KT + r, nk - 1), ko, vo);
-            to_lds(kb + ko * E::BYTES + 16 * chunk, dst + i * 1024);
-            to_lds(vb + vo * E::BYTES + 16 * chunk, dst + TILE + i * 1024);
+            place(min(t * KT + n * RPD + lane / TL::CHUNKS, nk - 1), ko, vo);
+            to_lds(kb + ko * E::BYTES + in_row, dst + i * 1024);
+            to_lds(vb + vo * E::BYTES + in_row, dst + TILE + i * 1024);
         }
     };
 
