@@ -43,7 +43,9 @@ struct BwdParams {
     int Tq, Tk, window;
     float scale, c;        // c: scale * log2(e)
     int o_f32, g_f32;
-    int tiles;             // of the launch's own rows or keys
+    int tiles, splits;     // of the launch's own rows or keys; of what each goes over
+    float* part;           // splits > 1: sums [splits][rows][D], those of dv behind those of dk
+    long rows;             // B H Tq, or B Hk Tk
     int query_tiles;
 };
 
@@ -79,9 +81,8 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int h = lane >> 5;
-    const int nheads = static_cast<int>(gridDim.x) / p.tiles;
-    const int bh = blockIdx.x % nheads, tile = p.tiles - 1 - blockIdx.x / nheads;
-    const int b = bh / p.Hk, hk = bh - b * p.Hk;
+    const int hk = blockIdx.x % p.Hk, rest = blockIdx.x / p.Hk;  // as in the forward
+    const int split = rest % p.splits, tile = p.tiles - 1 - rest / p.splits % p.tiles, b = rest / p.splits / p.tiles;
     const int nq = p.Tq, nk = p.Tk;
     const char* kb = static_cast<const char*>(p.k.p) + (b * p.k.sb + hk * p.k.sh) * E::BYTES;
     const char* vb = static_cast<const char*>(p.v.p) + (b * p.v.sb + hk * p.v.sh) * E::BYTES;
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
                 if constexpr (BF16) dof[a][s] = __builtin_convertvector(y, bf16x8);
                 else dof[a][s] = y;
                 if constexpr (BF16) {
-                    if (stored[a]) *reinterpret_cast<bf16x8*>(p.do16 + row * D + ch) = dof[a][s];
+                    if (stored[a] && split == 0) *reinterpret_cast<bf16x8*>(p.do16 + row * D + ch) = dof[a][s];
                 }
             } else if constexpr (BF16) {
                 x = __builtin_convertvector(El<true>::load(p.o.p, oa + ch), f32x8);
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
         }
         delta[a] = dot + __shfl_xor(dot, 32, 64);
         lse2[a] = p.lse[row] * kLog2e;
-        if (stored[a] && h == 0) {
+        if (stored[a] && h == 0 && split == 0) {
             p.delta[row] = delta[a];
             p.lse2[row] = lse2[a];
         }
@@ -154,7 +155,12 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
     __syncthreads();
     const int all_low = uniform(min(min(bounds[0][0], bounds[0][1]), min(bounds[0][2], bounds[0][3])));
     const int all_high = uniform(max(max(bounds[1][0], bounds[1][1]), max(bounds[1][2], bounds[1][3])));
-    const int first_tile = all_low / KT, end_tile = all_high < 0 ? first_tile : all_high / KT + 1;
+    int first_tile = all_low / KT, end_tile = all_high < 0 ? first_tile : all_high / KT + 1;
+    if (p.splits > 1) {
+        const int n = (end_tile - first_tile + p.splits - 1) / p.splits;
+        first_tile += split * n;
+        end_tile = min(end_tile, first_tile + n);
+    }
 
     const uint32_t at = lds_address(smem), row_base = TL::row_base(lane), column_base = TL::column_base(lane);
 
@@ -282,20 +288,24 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
 #pragma unroll
     for (int a = 0; a < QB; ++a) {
         if (!stored[a]) continue;
-        const long out = b * p.dq.sb + head[a] * p.dq.sh + token[a] * p.dq.st;
+        const long row = (static_cast<long>(b) * p.H + head[a]) * nq + token[a];
+        const long out = p.splits > 1 ? (split * p.rows + row) * D : b * p.dq.sb + head[a] * p.dq.sh + token[a] * p.dq.st;
+        const float scale = p.splits > 1 ? 1.0f : p.scale;
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 f32x4 x;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = seen[a].count > 0 ? acc[a][c][4 * g + i] * p.scale : 0.0f;
-                store4<BF16>(p.dq.p, out + 32 * c + 8 * g + 4 * h, p.g_f32, x);
+                for (int i = 0; i < 4; ++i) x[i] = seen[a].count > 0 ? acc[a][c][4 * g + i] * scale : 0.0f;
+                if (p.splits > 1) store4<false>(p.part, out + 32 * c + 8 * g + 4 * h, 1, x);
+                else store4<BF16>(p.dq.p, out + 32 * c + 8 * g + 4 * h, p.g_f32, x);
             }
     }
 }
 
-template <bool BF16, int D, int KB>
+// PARTS: the workgroups of a block of keys are p.splits.
+template <bool BF16, int D, int KB, bool PARTS>
 __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dkv_kernel(BwdParams p) {
     using E = El<BF16>;
     using TL = Tile<BF16, D>;
@@ -310,9 +320,10 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dkv_kernel(BwdPar
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int h = lane >> 5;
-    const int nheads = static_cast<int>(gridDim.x) / p.tiles;
-    const int bh = blockIdx.x % nheads, tile = blockIdx.x / nheads;  // the first keys have the most queries
-    const int b = bh / p.Hk, hk = bh - b * p.Hk;
+    const int hk = blockIdx.x % p.Hk, rest = blockIdx.x / p.Hk;
+    // the first keys have the most queries
+    const int splits = PARTS ? p.splits : 1;
+    const int split = rest % splits, tile = rest / splits % p.tiles, b = rest / splits / p.tiles;
     const int nq = p.Tq, nk = p.Tk, off = nk - nq;
     const int key0 = tile * KEYS, key1 = min(key0 + KEYS, nk) - 1;
 
@@ -506,8 +517,16 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dkv_kernel(BwdPar
     // The tiles of each head in turn; runs of those whose queries all see all of the wave's
     // keys in a loop of their own.
     const int w0 = key0 + 32 * KB * wave, w1 = w0 + 32 * KB - 1;  // this wave's keys
-    const int count = end > begin ? (end - begin) * p.shared : 0;
-    int n = 0, t = begin, i0 = 0, buffer = 1;  // the next tile; the present one's first query and place
+    int count = end > begin ? (end - begin) * p.shared : 0, t = begin;
+    if (PARTS && count > 0) {  // this part of them
+        const int each = (count + splits - 1) / splits, from = min(split * each, count), g = from / (end - begin);
+        count = min(each, count - from);
+        t = begin + from - g * (end - begin);
+        q_head += g * q_step;
+        d_head += g * d_step;
+        s_head += g * s_step;
+    }
+    int n = 0, i0 = 0, buffer = 1;  // tiles begun; the present one's first query and place
     bool partly = false;
     auto next = [&]() __attribute__((always_inline)) {
         landed();
@@ -531,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dkv_kernel(BwdPar
     };
     if (count > 0) {
         load_values();
-        load_tile(begin, 0);
+        load_tile(t, 0);
     }
     next();
     while (n <= count && count > 0) {
@@ -552,7 +571,10 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dkv_kernel(BwdPar
 #pragma unroll
     for (int a = 0; a < KB; ++a) {
         if (key[a] >= nk) continue;
-        const long ko = b * p.dk.sb + hk * p.dk.sh + key[a] * p.dk.st, vo = b * p.dv.sb + hk * p.dv.sh + key[a] * p.dv.st;
+        const long row = (static_cast<long>(b) * p.Hk + hk) * nk + key[a];
+        const long ko = !PARTS ? b * p.dk.sb + hk * p.dk.sh + key[a] * p.dk.st : (split * p.rows + row) * D;
+        const long vo = !PARTS ? b * p.dv.sb + hk * p.dv.sh + key[a] * p.dv.st : ((splits + split) * p.rows + row) * D;
+        const float scale = !PARTS ? p.scale : 1.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -560,49 +582,111 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dkv_kernel(BwdPar
                 f32x4 x, y;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[i] = dk[a][c][4 * e + i] * p.scale;
+                    x[i] = dk[a][c][4 * e + i] * scale;
                     y[i] = dv[a][c][4 * e + i];
                 }
-                store4<BF16>(p.dk.p, ko + 32 * c + 8 * e + 4 * h, p.g_f32, x);
-                store4<BF16>(p.dv.p, vo + 32 * c + 8 * e + 4 * h, p.g_f32, y);
+                if constexpr (!PARTS) {
+                    store4<BF16>(p.dk.p, ko + 32 * c + 8 * e + 4 * h, p.g_f32, x);
+                    store4<BF16>(p.dv.p, vo + 32 * c + 8 * e + 4 * h, p.g_f32, y);
+                } else {
+                    store4<false>(p.part, ko + 32 * c + 8 * e + 4 * h, 1, x);
+                    store4<false>(p.part, vo + 32 * c + 8 * e + 4 * h, 1, y);
+                }
             }
     }
 }
 
-struct Layout {
-    size_t delta, lse2, do16, first_range, bytes;  // offsets in the workspace
-};
+// The parts' sums of each row added up, in their order: D / 4 lanes to a row.
+template <bool BF16, int D>
+__global__ void __launch_bounds__(kThreads) attn_add_parts_kernel(const float* part, int splits, long rows, Out4 out, int heads, int T, float scale,
+                                                                  int f32) {
+    constexpr int LPR = D / 4;
+    const long row = (static_cast<long>(blockIdx.x) * kThreads + threadIdx.x) / LPR;
+    if (row >= rows) return;
+    const int ch = 4 * (threadIdx.x % LPR);
+    const long bh = row / T, b = bh / heads;
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) x += *reinterpret_cast<const f32x4*>(part + (s * rows + row) * D + ch);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] *= scale;
+    store4<BF16>(out.p, b * out.sb + (bh - b * heads) * out.sh + (row - bh * T) * out.st + ch, f32, x);
+}
 
 size_t up256(size_t n) { return (n + 255) & ~size_t{255}; }
 
 int query_tiles(int Tq) { return (Tq + kQueries - 1) / kQueries; }
 
+// Where the grid of a pass would not fill the device, what each of its workgroups goes
+// over (keys for dq, queries of the heads for dk and dv) is dealt to `splits` of them.
+constexpr long kFill = 512;       // two workgroups to a compute unit
+constexpr int kMaxSplits = 32;
+constexpr int kLeastKeys = 256;   // of a part, for dq
+constexpr int kLeastTiles = 8;    // of 32 queries, for dk and dv
+
+int splits_of(long groups, long most) {
+    long n = groups < kFill ? (kFill + groups - 1) / groups : 1;
+    if (n > most) n = most;
+    if (n > kMaxSplits) n = kMaxSplits;
+    return n > 1 ? static_cast<int>(n) : 1;
+}
+
+struct Layout {
+    int q_splits, k_splits;
+    size_t delta, lse2, do16, first_range, part, bytes;  // offsets in the workspace
+};
+
 Layout layout(const pdn_attn_bwd_args& a) {
     const pdn_attn_args& f = a.fwd;
-    const size_t rows = static_cast<size_t>(f.B) * f.H * f.Tq;
+    const size_t rows = static_cast<size_t>(f.B) * f.H * f.Tq, keys = static_cast<size_t>(f.B) * f.Hk * f.Tk;
+    const long heads = static_cast<long>(f.B) * f.Hk, shared = f.H / f.Hk, window = f.window > 0 && f.window < f.Tk ? f.window : f.Tk;
     Layout l{};
+    l.q_splits = f.Tq > 0 ? splits_of(heads * ((f.Tq * shared + 127) / 128), window / kLeastKeys) : 1;
+    l.k_splits = f.Tk > 0 ? splits_of(heads * ((f.Tk + 127) / 128), shared * query_tiles(window < f.Tq ? static_cast<int>(window) : f.Tq) / kLeastTiles) : 1;
     l.lse2 = up256(rows * sizeof(float));
     l.do16 = 2 * l.lse2;
     l.first_range = l.do16 + (f.dtype == PDN_BF16 && f.o_dtype == PDN_F32 ? up256(rows * f.d * 2) : 0);
-    l.bytes = l.first_range + (f.first ? up256(static_cast<size_t>(f.B) * query_tiles(f.Tq) * 2 * sizeof(int)) : 0);
+    l.part = l.first_range + (f.first ? up256(static_cast<size_t>(f.B) * query_tiles(f.Tq) * 2 * sizeof(int)) : 0);
+    // dq's parts have been added up before dk's and dv's are formed
+    const size_t q = l.q_splits > 1 ? l.q_splits * rows * f.d * sizeof(float) : 0;
+    const size_t k = l.k_splits > 1 ? 2 * l.k_splits * keys * f.d * sizeof(float) : 0;
+    l.bytes = l.part + up256(q > k ? q : k);
     return l;
 }
 
 template <bool BF16, int D>
-hipError_t launch(BwdParams p, long heads, hipStream_t stream) {
-    constexpr int QB = 1, KB = 1;
+hipError_t add_parts(const BwdParams& p, const float* part, const Out4& out, int heads, int T, float scale, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>((p.rows * (D / 4) + kThreads - 1) / kThreads)), block(kThreads);
+    attn_add_parts_kernel<BF16, D><<<grid, block, 0, stream>>>(part, p.splits, p.rows, out, heads, T, scale, p.g_f32);
+    return hipGetLastError();
+}
+
+template <bool BF16, int D>
+hipError_t launch(BwdParams p, int B, const Layout& l, hipStream_t stream) {
+    const long heads = static_cast<long>(B) * p.Hk;
+    const dim3 block(kThreads);
+    hipError_t rc = hipSuccess;
     if (p.Tq > 0) {
         const long rows = static_cast<long>(p.Tq) * p.shared;
-        p.tiles = static_cast<int>((rows + 128 * QB - 1) / (128 * QB));
-        attn_dq_kernel<BF16, D, QB><<<dim3(static_cast<unsigned>(heads * p.tiles)), dim3(kThreads), 0, stream>>>(p);
-        const hipError_t rc = hipGetLastError();
-        if (rc != hipSuccess) return rc;
+        p.tiles = static_cast<int>((rows + 127) / 128);
+        p.splits = l.q_splits;
+        p.rows = rows * heads;
+        attn_dq_kernel<BF16, D, 1><<<dim3(static_cast<unsigned>(heads * p.tiles * p.splits)), block, 0, stream>>>(p);
+        rc = hipGetLastError();
+        if (rc == hipSuccess && p.splits > 1) rc = add_parts<BF16, D>(p, p.part, p.dq, p.H, p.Tq, p.scale, stream);
     }
-    if (p.Tk > 0) {
-        p.tiles = (p.Tk + 128 * KB - 1) / (128 * KB);
-        attn_dkv_kernel<BF16, D, KB><<<dim3(static_cast<unsigned>(heads * p.tiles)), dim3(kThreads), 0, stream>>>(p);
+    if (p.Tk > 0 && rc == hipSuccess) {
+        p.tiles = (p.Tk + 127) / 128;
+        p.splits = l.k_splits;
+        p.rows = heads * p.Tk;
+        const dim3 grid(static_cast<unsigned>(heads * p.tiles * p.splits));
+        if (p.splits > 1) attn_dkv_kernel<BF16, D, 1, true><<<grid, block, 0, stream>>>(p);
+        else attn_dkv_kernel<BF16, D, 1, false><<<grid, block, 0, stream>>>(p);
+        rc = hipGetLastError();
+        if (rc == hipSuccess && p.splits > 1) rc = add_parts<BF16, D>(p, p.part, p.dk, p.Hk, p.Tk, p.scale, stream);
+        if (rc == hipSuccess && p.splits > 1) rc = add_parts<BF16, D>(p, p.part + p.splits * p.rows * D, p.dv, p.Hk, p.Tk, 1.0f, stream);
     }
-    return hipGetLastError();
+    return rc;
 }
 
 }  // namespace
@@ -646,9 +730,9 @@ hipError_t launch_attn_bwd(const pdn_attn_bwd_args& a, hipStream_t stream) {
         const hipError_t rc = hipGetLastError();
         if (rc != hipSuccess) return rc;
     }
-    const long heads = static_cast<long>(f.B) * f.Hk;
-    if (f.dtype == PDN_BF16) return f.d == 64 ? launch<true, 64>(p, heads, stream) : launch<true, 128>(p, heads, stream);
-    return f.d == 64 ? launch<false, 64>(p, heads, stream) : launch<false, 128>(p, heads, stream);
+    p.part = reinterpret_cast<float*>(ws + l.part);
+    if (f.dtype == PDN_BF16) return f.d == 64 ? launch<true, 64>(p, f.B, l, stream) : launch<true, 128>(p, f.B, l, stream);
+    return f.d == 64 ? launch<false, 64>(p, f.B, l, stream) : launch<false, 128>(p, f.B, l, stream);
 }
 
 }  // namespace pdn

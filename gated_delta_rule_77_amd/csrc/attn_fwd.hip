@@ -42,6 +42,9 @@ struct FwdParams {
 };
 
 constexpr int kThreads = 256;
+constexpr int kLeastKeys = 256;  // of a part of the keys
+constexpr int kMaxSplits = 128;
+constexpr int kFewParts = 8;     // that a row's lanes join one after another
 // A row's maximum is moved (and its sums scaled) when a score passes it by this
 // much, in powers of two: until then the exponentials stay below 2^8, well inside
 // fp32 and, as bf16 factors, as exact as any.
@@ -60,6 +63,7 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
     constexpr int KB = KT / 32 / WK;           // a wave's blocks of 32 keys in a tile
     constexpr int S = D / 16, C = D / 32;
     constexpr int TILE = KT * TL::ROW, DMAS = KT / TL::ROWS_PER_DMA / 4;
+    constexpr bool ALONE = WK == 4 && KB == 1;  // a wave reads the 32 rows of each tile that it loads
     static_assert(KB >= 1 && DMAS >= 1, "every wave has keys to read and rows to load");
     __shared__ __align__(1024) char smem[kBuffers * 2 * TILE];
     __shared__ int bounds[2][4];
@@ -67,12 +71,12 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int h = lane >> 5;
-    // heads before tiles: the workgroups of one key head follow each other on one XCD
-    // (for 8 heads, or multiples), the tiles with the most keys first
-    const int nheads = static_cast<int>(gridDim.x) / (p.tiles * p.splits);
-    const int bh = blockIdx.x % nheads, rest = blockIdx.x / nheads;
-    const int split = rest % p.splits, tile = p.tiles - 1 - rest / p.splits;
-    const int b = bh / p.Hk, hk = bh - b * p.Hk;
+    // Key heads first: their workgroups are dealt over the XCDs, so that every XCD (and every
+    // part of it) has its share of each sequence, whatever their lengths, and a head's keys
+    // are in as few L2s as that allows.  Then the parts of the keys, the tiles of rows (those
+    // with the most keys first), and the sequences.
+    const int hk = blockIdx.x % p.Hk, rest = blockIdx.x / p.Hk;
+    const int split = rest % p.splits, tile = p.tiles - 1 - rest / p.splits % p.tiles, b = rest / p.splits / p.tiles;
 
     int nq = p.Tq, nk = p.Tk;
     const char *qb = static_cast<const char*>(p.q), *kb = static_cast<const char*>(p.k), *vb = static_cast<const char*>(p.v);
@@ -135,7 +139,8 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
     const int all_high = uniform(max(max(bounds[1][0], bounds[1][1]), max(bounds[1][2], bounds[1][3])));
     int first_tile = all_low / KT, end_tile = all_high < 0 ? first_tile : all_high / KT + 1;
     if (p.splits > 1) {
-        const int n = end_tile > first_tile ? (end_tile - first_tile + p.splits - 1) / p.splits : 0;
+        // even parts, but not shorter than what is worth a workgroup (short sequences of a batch)
+        const int n = max((end_tile - first_tile + p.splits - 1) / p.splits, kLeastKeys / KT);
         first_tile += split * n;
         end_tile = min(end_tile, first_tile + n);
     }
@@ -148,9 +153,21 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
     constexpr int RPD = TL::ROWS_PER_DMA;
     const uint32_t chunk = TL::lane_chunk(lane);
     const uint32_t k_part = static_cast<uint32_t>(lane / TL::CHUNKS * p.k_st * E::BYTES), v_part = static_cast<uint32_t>(lane / TL::CHUNKS * p.v_st * E::BYTES);
-    auto place = [&](int key, long& ko, long& vo) __attribute__((always_inline)) {
+    // The sequence's pages, 64 a lane at a time and the next 64 behind them, so that no tile
+    // waits for the table.  A load's rows lie on one page (16 tokens at the least).
+    int pages = 0, ahead = 0, pages_at = 0;
+    auto fetch_pages = [&](int at) __attribute__((always_inline)) {
+        return page_of(p.map, b, min((at + lane) << p.map.shift, nk - 1));
+    };
+    auto place = [&](int first, int key, long& ko, long& vo) __attribute__((always_inline)) {  // of a token in the load that begins at `first`
         if constexpr (PAGED) {
-            const long page = page_of(p.map, b, key);
+            const int n = uniform(min(first, nk - 1) >> p.map.shift);
+            if (n >= pages_at + 64) {
+                pages_at += 64;
+                pages = ahead;
+                ahead = fetch_pages(pages_at + 64);
+            }
+            const long page = __builtin_amdgcn_readlane(pages, n - pages_at);
             const int in = key & ((1 << p.map.shift) - 1);
             ko = page * p.k_sb + in * p.k_st;
             vo = page * p.v_sb + in * p.v_st;
@@ -165,20 +182,20 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
 #pragma unroll
             for (int i = 0; i < DMAS; ++i) {
                 long ko, vo;
-                place(uniform(t * KT + (wave * DMAS + i) * RPD), ko, vo);
+                place(t * KT + (wave * DMAS + i) * RPD, t * KT + (wave * DMAS + i) * RPD, ko, vo);
                 to_lds(kb + ko * E::BYTES, TL::lane_offset(k_part, chunk, wave * DMAS + i), dst + i * 1024);
                 to_lds(vb + vo * E::BYTES, TL::lane_offset(v_part, chunk, wave * DMAS + i), dst + TILE + i * 1024);
             }
-            return;
-        }
+        } else {
 #pragma unroll
-        for (int i = 0; i < DMAS; ++i) {
-            const int n = wave * DMAS + i;
-            const uint32_t in_row = TL::lane_offset(0, chunk, n);
-            long ko, vo;
-            place(min(t * KT + n * RPD + lane / TL::CHUNKS, nk - 1), ko, vo);
-            to_lds(kb + ko * E::BYTES + in_row, dst + i * 1024);
-            to_lds(vb + vo * E::BYTES + in_row, dst + TILE + i * 1024);
+            for (int i = 0; i < DMAS; ++i) {
+                const int n = wave * DMAS + i;
+                const uint32_t in_row = TL::lane_offset(0, chunk, n);
+                long ko, vo;
+                place(t * KT + n * RPD, min(t * KT + n * RPD + lane / TL::CHUNKS, nk - 1), ko, vo);
+                to_lds(kb + ko * E::BYTES + in_row, dst + i * 1024);
+                to_lds(vb + vo * E::BYTES + in_row, dst + TILE + i * 1024);
+            }
         }
     };
 
@@ -357,10 +374,23 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
     int t = first_tile;
     auto next = [&](uint32_t& kt) __attribute__((always_inline)) {
         const int buffer = (t - first_tile) & 1;
-        landed();
-        __syncthreads();  // every wave's part of the tile; and the other buffer has been read
-        if (t + 1 < end_tile) load_tile(t + 1, buffer ^ 1);
+        if constexpr (ALONE) {
+            if (t + 1 < end_tile) landed_but<2 * DMAS>();
+            else landed_but<0>();
+        } else {
+            landed();
+            __syncthreads();  // every wave's part of the tile; and the other buffer has been read
+            if (t + 1 < end_tile) load_tile(t + 1, buffer ^ 1);
+        }
         kt = at + buffer * 2 * TILE;
+    };
+    // A wave that reads the rows that it loads itself goes at its own pace, without barriers,
+    // and loads two tiles ahead, into the place that it has just read.
+    auto done = [&]() __attribute__((always_inline)) {
+        if constexpr (ALONE) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            if (t + 2 < end_tile) load_tile(t + 2, (t - first_tile) & 1);
+        }
     };
     auto some = [&](int end) __attribute__((always_inline)) {
         for (; t < end; ++t) {
@@ -368,18 +398,29 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
             next(kt);
 #pragma unroll 1
             for (int e = 0; e < KB; ++e) some_seen(0, t * KT + rw + 32 * e, kt + (rw + 32 * e) * TL::ROW, kt + TILE + (rw + 32 * e) * TL::ROW);
+            done();
         }
     };
     int from = (full_low - rw + KT - 1) / KT, to = (full_high + 1 - rw - 32 * KB) / KT + 1;  // whole tiles from .. to - 1
     from = max(from, first_tile);
     to = min(full_high + 1 < rw + 32 * KB ? first_tile : to, end_tile);
     if (low == INT32_MAX || from >= to) from = to = end_tile;
-    if (first_tile < end_tile) load_tile(first_tile, 0);
+    if (first_tile < end_tile) {
+        if constexpr (PAGED) {
+            pages_at = uniform((min(first_tile * KT, nk - 1) >> p.map.shift) & ~63);
+            pages = fetch_pages(pages_at);
+            ahead = fetch_pages(pages_at + 64);
+        }
+        landed();
+        load_tile(first_tile, 0);
+        if (ALONE && first_tile + 1 < end_tile) load_tile(first_tile + 1, 1);
+    }
     some(min(from, end_tile));
     for (; t < to; ++t) {
         uint32_t kt;
         next(kt);
         all_seen(0, kt + rw * TL::ROW, kt + TILE + rw * TL::ROW);
+        done();
     }
     some(end_tile);
 #pragma unroll
@@ -389,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
     auto index = [&](int a) { return (static_cast<long>(b) * p.H + head[a]) * p.Tq + token[a]; };
     auto store4 = [&](int a, int ch, f32x4 x) {  // four channels of one row
         if (p.splits > 1) {
-            *reinterpret_cast<f32x4*>(p.part + (split * p.rows + index(a)) * D + ch) = x;
+            if (first_tile < end_tile) *reinterpret_cast<f32x4*>(p.part + (split * p.rows + index(a)) * D + ch) = x;
             return;
         }
         const long at = (PAGED ? (orow + token[a]) * p.o_st : b * p.o_sb + token[a] * p.o_st) + head[a] * p.o_sh + ch;
@@ -489,12 +530,15 @@ struct JoinParams {
     PageMap map;
 };
 
-template <int D, bool PAGED>
+// G = 1: D / 4 lanes to a row, which take its parts one after another.  G > 1: a workgroup
+// to a row, G groups of such lanes with every G-th part each.
+template <int D, int G, bool PAGED>
 __global__ void __launch_bounds__(kThreads) attn_join_kernel(JoinParams p) {
     constexpr int LPR = D / 4;
-    const long row = (static_cast<long>(blockIdx.x) * kThreads + threadIdx.x) / LPR;
+    static_assert(G == 1 || G * LPR == kThreads, "a row is a workgroup's");
+    const long row = G > 1 ? blockIdx.x : (static_cast<long>(blockIdx.x) * kThreads + threadIdx.x) / LPR;
     if (row >= p.rows) return;
-    const int ch = 4 * (threadIdx.x % LPR);
+    const int ch = 4 * (threadIdx.x % LPR), group = threadIdx.x / LPR;
     const long bh = row / p.Tq, b = bh / p.H, head = bh - b * p.H;
     long t = row - bh * p.Tq, out = row;  // out: of lse
     if constexpr (PAGED) {
@@ -505,16 +549,53 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(JoinParams p) {
     }
     const long at = b * p.o_sb + head * p.o_sh + t * p.o_st + ch;
     const float* ml = p.part + p.splits * p.rows * D + row * 2;
-    float m = -INFINITY;
-    for (int s = 0; s < p.splits; ++s) m = fmaxf(m, ml[s * p.rows * 2]);
-    float l = 0.0f;
+    float m = -INFINITY, l = 0.0f;
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < p.splits; ++s) {
-        const float ms = ml[s * p.rows * 2], ls = ml[s * p.rows * 2 + 1];
-        if (ls == 0.0f) continue;  // no keys there
-        const float by = ms == -INFINITY ? 1.0f : ex2(ms - m);
-        l = fmaf(ls, by, l);
-        x += *reinterpret_cast<const f32x4*>(p.part + (s * p.rows + row) * D + ch) * by;
+    if constexpr (G > 1) {
+        __shared__ float weight[kMaxSplits];
+        __shared__ float red[2][4];
+        __shared__ f32x4 sums[G][LPR];
+        const int tid = threadIdx.x, wave = tid >> 6;
+        float ms = -INFINITY, ls = 0.0f;
+        if (tid < p.splits) {
+            ms = ml[tid * p.rows * 2];
+            ls = ml[tid * p.rows * 2 + 1];
+        }
+        float top = ms;
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+        if ((tid & 63) == 0) red[0][wave] = top;
+        __syncthreads();
+        m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+        const float w = ls == 0.0f ? 0.0f : ms == -INFINITY ? 1.0f : ex2(ms - m);
+        if (tid < p.splits) weight[tid] = w;
+        const float part = wave_sum(ls * w);
+        if ((tid & 63) == 0) red[1][wave] = part;
+        __syncthreads();
+        l = red[1][0] + red[1][1] + red[1][2] + red[1][3];
+#pragma unroll 4
+        for (int s = group; s < p.splits; s += G) {
+            const float by = weight[s];
+            // a part without keys has left nothing there
+            if (by != 0.0f) x += *reinterpret_cast<const f32x4*>(p.part + (s * p.rows + row) * D + ch) * by;
+        }
+        sums[group][threadIdx.x % LPR] = x;
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int g = 1; g < G; ++g) x += sums[g][threadIdx.x];
+    } else {
+#pragma unroll 4
+        for (int s = 0; s < p.splits; ++s) m = fmaxf(m, ml[s * p.rows * 2]);
+#pragma unroll 4
+        for (int s = 0; s < p.splits; ++s) {
+            const float ms = ml[s * p.rows * 2], ls = ml[s * p.rows * 2 + 1];
+            const f32x4 y = *reinterpret_cast<const f32x4*>(p.part + (s * p.rows + row) * D + ch);
+            const float by = ls == 0.0f ? 0.0f : ms == -INFINITY ? 1.0f : ex2(ms - m);
+            l = fmaf(ls, by, l);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] += by == 0.0f ? 0.0f : y[i] * by;  // a part without keys has left nothing there
+        }
     }
     const bool none = l == 0.0f;
     const float n = none ? 0.0f : 1.0f / l;
@@ -531,10 +612,10 @@ struct Plan {
     int tiles, splits;
 };
 
-constexpr long kFill = 512;       // workgroups that fill the device: two to a compute unit
-constexpr int kLeastKeys = 256;   // of a split
 
-Plan plan(bool bf16, int d, long heads, long rows, long keys) {
+constexpr long kUnits = 256;  // compute units
+
+Plan plan(bool bf16, int d, long heads, long rows, long keys, bool ragged) {
     Plan p{};
     const bool wide = !bf16 && d == 128;  // 512-byte rows: half the keys to a tile
     if (rows <= (wide ? 64 : 32)) {
@@ -547,13 +628,18 @@ Plan plan(bool bf16, int d, long heads, long rows, long keys) {
     p.rows = 32 * p.qb * (4 / p.wk);
     p.tiles = static_cast<int>((rows + p.rows - 1) / p.rows);
     const long groups = heads * p.tiles;
-    p.splits = 1;
-    if (groups < kFill / 2) {
-        long want = kFill / groups, most = keys / kLeastKeys;
-        if (want > most) want = most;
-        if (want > 128) want = 128;
-        p.splits = want > 1 ? static_cast<int>(want) : 1;
+    long splits = 1, least = bf16 ? 512 : 256;
+    if (p.wk > 1 && groups < kUnits) {
+        splits = kUnits / groups;
+    } else if (p.wk > 1) {
+        splits = (8 * kUnits + groups - 1) / groups;
+        least = 1024;
+    } else if (groups < (ragged ? 4 : 2) * kUnits) {
+        splits = ((ragged ? 4 : 2) * kUnits + groups - 1) / groups;
     }
+    if (splits > keys / least) splits = keys / least;
+    if (splits > kMaxSplits) splits = kMaxSplits;
+    p.splits = splits > 1 ? static_cast<int>(splits) : 1;
     return p;
 }
 
@@ -580,23 +666,29 @@ hipError_t launch(const FwdParams& p, const Plan& pl, int32_t dtype, int d, long
 
 template <bool PAGED>
 hipError_t launch_join(const JoinParams& p, int d, hipStream_t stream) {
-    const long threads = p.rows * (d / 4);
-    const dim3 grid(static_cast<unsigned>((threads + kThreads - 1) / kThreads)), block(kThreads);
-    if (d == 64) attn_join_kernel<64, PAGED><<<grid, block, 0, stream>>>(p);
-    else attn_join_kernel<128, PAGED><<<grid, block, 0, stream>>>(p);
+    const dim3 block(kThreads);
+    if (p.splits > kFewParts) {
+        const dim3 grid(static_cast<unsigned>(p.rows));
+        if (d == 64) attn_join_kernel<64, 16, PAGED><<<grid, block, 0, stream>>>(p);
+        else attn_join_kernel<128, 8, PAGED><<<grid, block, 0, stream>>>(p);
+    } else {
+        const dim3 grid(static_cast<unsigned>((p.rows * (d / 4) + kThreads - 1) / kThreads));
+        if (d == 64) attn_join_kernel<64, 1, PAGED><<<grid, block, 0, stream>>>(p);
+        else attn_join_kernel<128, 1, PAGED><<<grid, block, 0, stream>>>(p);
+    }
     return hipGetLastError();
 }
 
 Plan plan_of(const pdn_attn_args& a) {
     return plan(a.dtype == PDN_BF16, a.d, static_cast<long>(a.B) * a.Hk, static_cast<long>(a.Tq) * (a.H / a.Hk),
-                a.window > 0 && a.window < a.Tk - a.Tq ? a.window + a.Tq : a.Tk);
+                a.window > 0 && a.window < a.Tk - a.Tq ? a.window + a.Tq : a.Tk, false);
 }
 
 Plan plan_of(const pdn_attn_paged_args& a) {
     const long keys = static_cast<long>(a.cache.table_width) * a.cache.page_size;
     return plan(a.cache.dtype == PDN_BF16, a.cache.d, static_cast<long>(a.cache.B) * a.cache.Hk,
                 static_cast<long>(a.cache.max_new) * (a.H / a.cache.Hk),
-                a.window > 0 && static_cast<long>(a.window) + a.cache.max_new < keys ? static_cast<long>(a.window) + a.cache.max_new : keys);
+                a.window > 0 && static_cast<long>(a.window) + a.cache.max_new < keys ? static_cast<long>(a.window) + a.cache.max_new : keys, true);
 }
 
 }  // namespace
