@@ -26,8 +26,10 @@ __host__ __device__ __forceinline__ int held(int x, int low, int high) { return 
 __host__ __device__ __forceinline__ Sequence sequence_of(const PageMap& m, int b) {
     Sequence s;
     if (m.starts) {
-        s.start = held(m.starts[b], 0, m.N);
-        s.n = held(m.starts[b + 1], s.start, m.N) - s.start;
+        const int from = m.starts[b], to = m.starts[b + 1];
+        const bool rows = 0 <= from && from <= to && to <= m.N;  // else it has none
+        s.start = rows ? from : 0;
+        s.n = rows ? to - from : 0;
     } else {
         s.n = m.N / m.B;
         s.start = b * s.n;

@@ -230,14 +230,16 @@ typedef struct pdn_attn_bwd_args {
  *   lens              [B] int32 (device): tokens of each sequence in the cache, the
  *                     new ones included.
  *   starts            [B + 1] int32 (device): sequence b's new tokens are the rows
- *                     starts[b] .. starts[b + 1] - 1 of N, its last ones; NULL: each
- *                     sequence has N / B of them (B divides N then).
+ *                     starts[b] .. starts[b + 1] - 1 of N, its last ones (starts
+ *                     ascends, from row to row); NULL: each sequence has N / B of
+ *                     them (B divides N then).
  *   max_new           at least the most new tokens of any sequence (it sizes the
  *                     launch; a sequence's rows past it are left out).
  * None of these device numbers can lead outside the arrays: table entries are
- * held to the pages there are, lens to the table's width, starts to N.  Where they
- * had to be, the sequence's results mean nothing (an append leaves such tokens
- * out).  Rows that belong to no sequence are left as they were.
+ * held to the pages there are and lens to the table's width, and a sequence whose
+ * starts do not ascend within N has no new tokens.  Where they had to be held, the
+ * sequence's results mean nothing (an append leaves such tokens out).  Rows that
+ * belong to no sequence are left as they were.
  * PDN_EUNSUPPORTED where B passes 2^20, or table_width * page_size 2^30.
  */
 typedef struct pdn_cache {
