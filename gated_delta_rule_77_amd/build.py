@@ -34,13 +34,15 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", "-I" + INCLUDE, "-I" + CSRC,
 # faster and the per-channel-gate preparation kernel with symmetric keys and
 # per-channel decay and gain 3% faster; the other kernels measured equal or
 # slower with it (that preparation kernel 10-20% slower with asymmetric keys or
-# the stabilised preconditioner).
+# the stabilised preconditioner).  The attention's forward gains 2% with it, its
+# backward loses 5%.
 ILP = ["-mllvm", "-amdgpu-sched-strategy=max-ilp"]
 VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
 EXTRA = {"chunk_fact.hip": VGPR_FORM,
          "chunk_vec.hip": VGPR_FORM,
          "chunk_vec_ilp.hip": VGPR_FORM + ILP,
-         "chunk_bwd_ilp.hip": ILP}
+         "chunk_bwd_ilp.hip": ILP,
+         "attn_fwd.hip": ILP}
 
 
 def _hipcc() -> str:

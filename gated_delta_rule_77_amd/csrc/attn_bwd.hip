@@ -139,10 +139,6 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
         }
         delta[a] = dot + __shfl_xor(dot, 32, 64);
         lse2[a] = p.lse[row] * kLog2e;
-        if (stored[a] && h == 0 && split == 0) {
-            p.delta[row] = delta[a];
-            p.lse2[row] = lse2[a];
-        }
     }
     low = uniform(wave_min_i(low));
     high = uniform(wave_max_i(high));
@@ -233,13 +229,23 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
 #pragma unroll
         for (int a = 0; a < QB; ++a) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[a][i] = ex2(fmaf(s[a][i], p.c, -lse2[a])) * (dp[a][i] - delta[a]);
+            for (int i = 0; i < 16; ++i) s[a][i] = ex2(fmaf(s[a][i], p.c, -lse2[a]));
             if constexpr (PARTLY) {
                 const Seen to = {opaque(seen[a].low - k0 - 4 * h), seen[a].count};
+                float dot = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (!sees(to, 8 * (i >> 2) + (i & 3))) s[a][i] = 0.0f;
+                for (int i = 0; i < 16; ++i) {
+                    if (!sees(to, 8 * (i >> 2) + (i & 3))) s[a][i] = dp[a][i] = 0.0f;
+                    dot = fmaf(s[a][i], dp[a][i], dot);
+                }
+                // Where all that a row sees lies in this block, D is formed from it: a row of few
+                // keys is where the rounding of o to bf16 would show most (alone it sees itself,
+                // and its gradients vanish).
+                dot = halves<false>(dot);
+                if (seen[a].low >= k0 && seen[a].low + seen[a].count <= k0 + 32) delta[a] = dot;
             }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[a][i] *= dp[a][i] - delta[a];
             df[a][0] = E::of(s[a], 0);
             df[a][1] = E::of(s[a], 1);
         }
@@ -289,6 +295,12 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
     for (int a = 0; a < QB; ++a) {
         if (!stored[a]) continue;
         const long row = (static_cast<long>(b) * p.H + head[a]) * nq + token[a];
+        // for the pass over the keys, from the one part that begins with what the row sees
+        const int first = seen[a].low / KT;
+        if (h == 0 && (seen[a].count > 0 ? first_tile <= first && first < end_tile : split == 0)) {
+            p.delta[row] = delta[a];
+            p.lse2[row] = lse2[a];
+        }
         const long out = p.splits > 1 ? (split * p.rows + row) * D : b * p.dq.sb + head[a] * p.dq.sh + token[a] * p.dq.st;
         const float scale = p.splits > 1 ? 1.0f : p.scale;
 #pragma unroll
@@ -320,10 +332,12 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dkv_kernel(BwdPar
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int h = lane >> 5;
-    const int hk = blockIdx.x % p.Hk, rest = blockIdx.x / p.Hk;
-    // the first keys have the most queries
-    const int splits = PARTS ? p.splits : 1;
-    const int split = rest % splits, tile = rest / splits % p.tiles, b = rest / splits / p.tiles;
+    // Heads of all sequences first, so that those of one XCD go through the rows side by side
+    // (packed rows of B2 Hk8 T8192 1408 us one after another, 1322 so); then the keys, of which
+    // the first have the most queries.
+    const int splits = PARTS ? p.splits : 1, heads = static_cast<int>(gridDim.x) / (p.tiles * splits);
+    const int bh = blockIdx.x % heads, rest = blockIdx.x / heads, b = bh / p.Hk, hk = bh - b * p.Hk;
+    const int split = rest % splits, tile = rest / splits;
     const int nq = p.Tq, nk = p.Tk, off = nk - nq;
     const int key0 = tile * KEYS, key1 = min(key0 + KEYS, nk) - 1;
 
@@ -617,15 +631,16 @@ size_t up256(size_t n) { return (n + 255) & ~size_t{255}; }
 
 int query_tiles(int Tq) { return (Tq + kQueries - 1) / kQueries; }
 
-// Where the grid of a pass would not fill the device, what each of its workgroups goes
-// over (keys for dq, queries of the heads for dk and dv) is dealt to `splits` of them.
-constexpr long kFill = 512;       // two workgroups to a compute unit
+// Where the grid of a pass would leave much of the device idle, at its end above all, what
+// each of its workgroups goes over (keys for dq, queries of the heads for dk and dv) is dealt
+// to `splits` of them: bf16 to four workgroups a compute unit (B2 H16/4 T2048 d128 241 us
+// with two, 203 with four, 298 with eight), fp32, whose products take 16 times as long, to
+// two of half the length (B3 H8/2 T1237 d64 234 us, 253 with four).
 constexpr int kMaxSplits = 32;
-constexpr int kLeastKeys = 256;   // of a part, for dq
-constexpr int kLeastTiles = 8;    // of 32 queries, for dk and dv
 
-int splits_of(long groups, long most) {
-    long n = groups < kFill ? (kFill + groups - 1) / groups : 1;
+int splits_of(bool bf16, long groups, long steps) {  // steps: blocks of 32 that a workgroup goes over
+    const long fill = bf16 ? 1024 : 512, most = steps / (bf16 ? 16 : 8);
+    long n = groups < fill ? (fill + groups - 1) / groups : 1;
     if (n > most) n = most;
     if (n > kMaxSplits) n = kMaxSplits;
     return n > 1 ? static_cast<int>(n) : 1;
@@ -641,8 +656,8 @@ Layout layout(const pdn_attn_bwd_args& a) {
     const size_t rows = static_cast<size_t>(f.B) * f.H * f.Tq, keys = static_cast<size_t>(f.B) * f.Hk * f.Tk;
     const long heads = static_cast<long>(f.B) * f.Hk, shared = f.H / f.Hk, window = f.window > 0 && f.window < f.Tk ? f.window : f.Tk;
     Layout l{};
-    l.q_splits = f.Tq > 0 ? splits_of(heads * ((f.Tq * shared + 127) / 128), window / kLeastKeys) : 1;
-    l.k_splits = f.Tk > 0 ? splits_of(heads * ((f.Tk + 127) / 128), shared * query_tiles(window < f.Tq ? static_cast<int>(window) : f.Tq) / kLeastTiles) : 1;
+    l.q_splits = f.Tq > 0 ? splits_of(f.dtype == PDN_BF16, heads * ((f.Tq * shared + 127) / 128), window / 32) : 1;
+    l.k_splits = f.Tk > 0 ? splits_of(f.dtype == PDN_BF16, heads * ((f.Tk + 127) / 128), shared * query_tiles(window < f.Tq ? static_cast<int>(window) : f.Tq)) : 1;
     l.lse2 = up256(rows * sizeof(float));
     l.do16 = 2 * l.lse2;
     l.first_range = l.do16 + (f.dtype == PDN_BF16 && f.o_dtype == PDN_F32 ? up256(rows * f.d * 2) : 0);

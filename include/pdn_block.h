@@ -191,11 +191,13 @@ typedef struct pdn_attn_args {
 /*
  * Its backward, which forms the probabilities again from q, k and lse:
  *
- *   D_i = <dO_i, o_i>,  dS_ij = scale P_ij (<dO_i, v_j> - D_i)
+ *   D_i = <dO_i, o_i> = sum_j P_ij <dO_i, v_j>,  dS_ij = scale P_ij (<dO_i, v_j> - D_i)
  *   dq_i = sum_j dS_ij k_j,  dk_j = sum_i dS_ij q_i,  dv_j = sum_i P_ij dO_i
  *
  * over the heads that share a key head; sums in fp32 in a fixed order (with bf16
- * P and dS are rounded to bf16 for their products, and an fp32 dO for its own).
+ * P and dS are rounded to bf16 for their products, and an fp32 dO for its own).  D is
+ * taken from o as it is kept (in bf16 off by its rounding; an fp32 o avoids that), or
+ * from P where a row's keys lie together.
  *
  *   fwd               the forward's arguments, o and lse as it wrote them;
  *                     workspace and workspace_bytes are not read.

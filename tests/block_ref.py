@@ -113,9 +113,11 @@ def attn(q, k, v, scale, mask, dtype):
     return dict(o=o, bo=bo, lse=lse, bl=torch.where(some, bl, 0.0), p=p, e=e, s=s, k=k, v=v, some=some, mask=m, size=size)
 
 
-def attn_bwd(q, k, v, o, do, scale, mask, dtype, rounded_do):
+def attn_bwd(q, k, v, o, do, scale, mask, dtype, rounded_do, odtype="fp32"):
     """dq, dk, dv and their bounds; o is what the backward is given.  rounded_do: dO is
-    fp32 and rounded to bf16 for its products."""
+    fp32 and rounded to bf16 for its products.  D_i is formed from o or from P: the two
+    differ by o's own rounding, HALF[odtype] of sum |dO o|, and what o is off by
+    otherwise: with bf16 P's rounding too, another HALF["bf16"] of sum |dO| (P |v|)."""
     Hk, rep, d = k.shape[1], q.shape[1] // k.shape[1], q.shape[-1]
     f = attn(q, k, v, scale, mask, dtype)
     p, kk, vv, m = f["p"], f["k"], f["v"], f["mask"]
@@ -125,11 +127,12 @@ def attn_bwd(q, k, v, o, do, scale, mask, dtype, rounded_do):
     delta = (do * o).sum(-1, keepdim=True)
     size_d = (do * o).abs().sum(-1, keepdim=True)
     dp, size_p = do @ vv.mT, do.abs() @ vv.abs().mT
+    off_d = HALF[odtype] * size_d + (h + 4 * f["e"] + 4 * (k.shape[2] + 8) * U) * (do.abs() * f["size"]).sum(-1, keepdim=True)
     ds = p * (dp - delta)
     n, nq = k.shape[2], q.shape[2] * rep
     # an exponential against the forward's lse: the scores' error here, and there
     e = 2 * f["e"] + 2 * (n + 8) * U + 4 * U * torch.where(f["some"], f["lse"], 0.0).abs()[..., None]
-    eds = p * (size_p * (hd + 2 * (d + 2) * U) + size_d * (hd * 0 + 2 * (d + 2) * U)) + ds.abs() * (e + 4 * U)
+    eds = p * (size_p * (hd + 2 * (d + 2) * U) + size_d * 2 * (d + 2) * U + off_d) + ds.abs() * (e + 4 * U)
     eds = eds * (1 + h) + ds.abs() * h
     ep = p * (e + 4 * U) * (1 + h) + p * h
     fold = lambda t: t.unflatten(1, (Hk, rep)).sum(2)  # noqa: E731  heads that share a key head

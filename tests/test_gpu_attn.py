@@ -143,7 +143,7 @@ def test_attn(case):
     pdn.pdn_attn_bwd(q, k, v, o, do, lse, dq, dk, dv, workspace=ws, **same)
     torch.cuda.synchronize()
     # the gradient through the o that the forward kept
-    want = ref.attn_bwd(_host(q), _host(k), _host(v), _host(o), _host(do), s32, mask, dtype, dtype == "bf16" and odtype == "fp32")
+    want = ref.attn_bwd(_host(q), _host(k), _host(v), _host(o), _host(do), s32, mask, dtype, dtype == "bf16" and odtype == "fp32", odtype)
     for n, t in (("dq", dq), ("dk", dk), ("dv", dv)):
         _close(n, t, *want[n], gdtype)
     again = [torch.empty_like(t) for t in (dq, dk, dv)]
