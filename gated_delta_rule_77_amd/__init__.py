@@ -1038,13 +1038,12 @@ def pdn_rope_freqs(rot_dim, base=10000.0, scaling=PDN_ROPE_PLAIN, factor=1.0, or
 # what a stack with attention layers needs besides the recurrence
 # ---------------------------------------------------------------------------
 
-def _rows3(c, a, field, t, name, shape, dtype):
-    """A [B,T,D] tensor and its strides (None: as they are)."""
-    if t is not None:
-        setattr(a, field, c.rows(t, name, shape, dtype))
-        sb, st, _ = t.stride()
-        setattr(a, field + "_sb", sb)
-        setattr(a, field + "_st", st)
+def _rows3(c, t, name, shape, dtype):
+    """Pointer and strides of a [B,T,D] tensor."""
+    if t is None:
+        return None, 0, 0
+    sb, st, _ = t.stride() if t.dim() == 3 else (0, 0, 0)
+    return c.rows(t, name, shape, dtype), sb, st
 
 
 def _seam(c, x, w, eps, drop_p, seed):
@@ -1072,10 +1071,10 @@ def pdn_add_norm_fwd(x, y, res=None, s=None, w=None, eps=1e-6, drop_p=0.0, seed=
     B, T, D = shape = _seam(c, x, w, eps, drop_p, seed)
     s_dtype = x.dtype if res is None and s is None else (res if res is not None else s).dtype
     a.dtype, a.s_dtype = _dtype_of(x, "x"), _CODES.get(s_dtype, -1)
-    _rows3(c, a, "x", x, "x", shape, x.dtype)
-    _rows3(c, a, "res", res, "res", shape, s_dtype)
-    _rows3(c, a, "s", s, "s", shape, s_dtype)
-    _rows3(c, a, "y", y, "y", shape, y.dtype)
+    a.x, a.x_sb, a.x_st = _rows3(c, x, "x", shape, x.dtype)
+    a.res, a.res_sb, a.res_st = _rows3(c, res, "res", shape, s_dtype)
+    a.s, a.s_sb, a.s_st = _rows3(c, s, "s", shape, s_dtype)
+    a.y, a.y_sb, a.y_st = _rows3(c, y, "y", shape, y.dtype)
     if y.dtype == _torch.float8_e4m3fn:
         a.y_dtype = PDN_E4M3
         if y_scale is None:
@@ -1099,11 +1098,11 @@ def _add_norm_bwd(s, dy, dres, ds, dx, w, dw, eps, drop_p, seed):
     a.y_dtype = _dtype_of(dy, "dy")
     if dx is not None:
         a.dtype = _dtype_of(dx, "dx")
-        _rows3(c, a, "dx", dx, "dx", shape, dx.dtype)
-    _rows3(c, a, "s", s, "s", shape, s.dtype)
-    _rows3(c, a, "dy", dy, "dy", shape, dy.dtype)
-    _rows3(c, a, "ds", ds, "ds", shape, s.dtype)
-    _rows3(c, a, "dres", dres, "dres", shape, s.dtype)
+        a.dx, a.dx_sb, a.dx_st = _rows3(c, dx, "dx", shape, dx.dtype)
+    a.s, a.s_sb, a.s_st = _rows3(c, s, "s", shape, s.dtype)
+    a.dy, a.dy_sb, a.dy_st = _rows3(c, dy, "dy", shape, dy.dtype)
+    a.ds, a.ds_sb, a.ds_st = _rows3(c, ds, "ds", shape, s.dtype)
+    a.dres, a.dres_sb, a.dres_st = _rows3(c, dres, "dres", shape, s.dtype)
     a.dw = c.plain(dw, "dw", shape[-1:], _torch.float32)
     return c
 
@@ -1121,13 +1120,11 @@ def pdn_add_norm_bwd(s, dy, dres, ds=None, dx=None, w=None, dw=None, eps=1e-6, d
     _add_norm_bwd(s, dy, dres, ds, dx, w, dw, eps, drop_p, seed).launch("pdn_add_norm_bwd", stream, workspace)
 
 
-def _rows4(c, a, field, t, name, shape, dtype):
-    """A [B,heads,T,d] tensor and its strides."""
-    setattr(a, "d_o" if field == "do" else field, c.rows(t, name, shape, dtype))
+def _rows4(c, t, name, shape, dtype):
+    """Pointer and strides of a [B,heads,T,d] tensor."""
+    p = c.rows(t, name, shape, dtype)
     sb, sh, st, _ = t.stride()
-    setattr(a, field + "_sb", sb)
-    setattr(a, field + "_sh", sh)
-    setattr(a, field + "_st", st)
+    return p, sb, sh, st
 
 
 def _attn(c, a, q, k, v, o, lse, scale, window, first):
@@ -1137,9 +1134,11 @@ def _attn(c, a, q, k, v, o, lse, scale, window, first):
     a.B, a.H, a.Hk, a.Tq, a.Tk, a.d = B, H, Hk, Tq, Tk, d
     a.dtype, a.o_dtype, a.window = _dtype_of(q, "q"), _dtype_of(o, "o"), window
     a.scale = d ** -0.5 if scale is None else scale
-    for name, t, shape in (("q", q, (B, H, Tq, d)), ("k", k, (B, Hk, Tk, d)), ("v", v, (B, Hk, Tk, d))):
-        _rows4(c, a, name, t, name, shape, q.dtype)
-    _rows4(c, a, "o", o, "o", (B, H, Tq, d), o.dtype)
+    queries, keys = (B, H, Tq, d), (B, Hk, Tk, d)
+    a.q, a.q_sb, a.q_sh, a.q_st = _rows4(c, q, "q", queries, q.dtype)
+    a.k, a.k_sb, a.k_sh, a.k_st = _rows4(c, k, "k", keys, q.dtype)
+    a.v, a.v_sb, a.v_sh, a.v_st = _rows4(c, v, "v", keys, q.dtype)
+    a.o, a.o_sb, a.o_sh, a.o_st = _rows4(c, o, "o", queries, o.dtype)
     a.lse = c.plain(lse, "lse", (B, H, Tq), _torch.float32)
     a.first = c.plain(first, "first", (B, Tq), _torch.int32)
 
@@ -1173,9 +1172,10 @@ def _attn_bwd(q, k, v, o, do, lse, dq, dk, dv, scale, window, first):
         raise ValueError("lse is required")
     _attn(c, a.fwd, q, k, v, o, lse, scale, window, first)
     a.g_dtype = _dtype_of(dq, "dq")
-    _rows4(c, a, "do", do, "do", o.shape, o.dtype)
-    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        _rows4(c, a, name, t, name, like.shape, dq.dtype)
+    a.d_o, a.do_sb, a.do_sh, a.do_st = _rows4(c, do, "do", o.shape, o.dtype)
+    a.dq, a.dq_sb, a.dq_sh, a.dq_st = _rows4(c, dq, "dq", q.shape, dq.dtype)
+    a.dk, a.dk_sb, a.dk_sh, a.dk_st = _rows4(c, dk, "dk", k.shape, dq.dtype)
+    a.dv, a.dv_sb, a.dv_sh, a.dv_st = _rows4(c, dv, "dv", v.shape, dq.dtype)
     return c
 
 

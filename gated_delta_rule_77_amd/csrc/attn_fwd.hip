@@ -693,12 +693,12 @@ Plan plan_of(const pdn_attn_paged_args& a) {
 
 }  // namespace
 
-// 128 rows to a workgroup (or one workgroup for fewer), 128 keys in the backward, and 64
+// 128 rows to a workgroup (or one workgroup for fewer), 128 keys in the backward, and 32
 // queries to a wave of its range kernel; a call with splits is a small one.
 bool attn_fits(const pdn_attn_args& a) {
     const long heads = static_cast<long>(a.B) * a.Hk, rows = static_cast<long>(a.Tq) * (a.H / a.Hk);
     return heads * ((rows + 127) / 128 + 1) * kThreads < kMaxGridThreads && heads * ((a.Tk + 127L) / 128) * kThreads < kMaxGridThreads &&
-           static_cast<long>(a.B) * (a.Tq + 64L) < kMaxGridThreads;
+           static_cast<long>(a.B) * ((a.Tq + 31L) / 32) * 64 < kMaxGridThreads;
 }
 
 bool attn_paged_fits(const pdn_attn_paged_args& a) {

@@ -20,6 +20,9 @@ constexpr long kMaxSeamRows = 1L << 23;
 constexpr int kMaxSeamWidth = 16384;
 constexpr int kMaxShared = 1 << 10;   // query heads of a key head
 constexpr long kMaxSequences = 1L << 20;
+// Elements from one token to the next that the loads of whole tiles take: their lanes'
+// offsets are 32 bits, over seven tokens of 2-byte elements or three of 4 bytes.
+constexpr int64_t kMaxTokenStep = int64_t{1} << 28;
 
 // the types a call's outputs may have: bf16 only where its inputs do
 bool valid_out(int32_t out, int32_t in) { return out == PDN_F32 || (out == PDN_BF16 && in == PDN_BF16); }
@@ -90,7 +93,8 @@ int check_add_norm_bwd(const pdn_add_norm_bwd_args* a, bool check_ws = true) {
     return check_ws ? check_workspace(a->workspace, a->workspace_bytes, pdn::add_norm_bwd_workspace_bytes(*a)) : PDN_OK;
 }
 
-bool valid_scale(float s) { return std::isfinite(s) && s > 0.0f; }
+bool valid_scale(float s) { return std::isfinite(s * 1.4427f) && s > 0.0f; }
+bool near(int64_t tokens, int64_t step) { return tokens <= 1 || step <= kMaxTokenStep; }
 
 int check_attn(const pdn_attn_args* a, bool backward = false, bool check_ws = true) {
     if (!a) return PDN_EINVAL;
@@ -111,6 +115,7 @@ int check_attn(const pdn_attn_args* a, bool backward = false, bool check_ws = tr
         int rc = check_view(view3(a->k, a->B, a->Hk, a->Tk, a->k_sb, a->k_sh, a->k_st, a->d, a->dtype), false);
         if (rc == PDN_OK) rc = check_view(view3(a->v, a->B, a->Hk, a->Tk, a->v_sb, a->v_sh, a->v_st, a->d, a->dtype), false);
         if (rc != PDN_OK) return rc;
+        if (!near(a->Tk, a->k_st) || !near(a->Tk, a->v_st)) return PDN_EUNSUPPORTED;
     }
     if (backward || !check_ws) return PDN_OK;
     return check_workspace(a->workspace, a->workspace_bytes, pdn::attn_fwd_workspace_bytes(*a));
@@ -128,6 +133,7 @@ int check_attn_bwd(const pdn_attn_bwd_args* a, bool check_ws = true) {
         rc = check_view(view3(a->d_o, f.B, f.H, f.Tq, a->do_sb, a->do_sh, a->do_st, f.d, f.o_dtype), false);
         if (rc == PDN_OK) rc = check_view(view3(a->dq, f.B, f.H, f.Tq, a->dq_sb, a->dq_sh, a->dq_st, f.d, a->g_dtype), true);
         if (rc != PDN_OK) return rc;
+        if (!near(f.Tq, f.q_st) || !near(f.Tq, a->do_st)) return PDN_EUNSUPPORTED;
     }
     if (f.Tk > 0) {
         // with no queries their gradients are zeros, and k and v are still read
@@ -180,6 +186,7 @@ int check_paged(const pdn_attn_paged_args* a, bool check_ws = true) {
     if ((c.d != 64 && c.d != 128) || !valid_out(a->o_dtype, c.dtype)) return PDN_EUNSUPPORTED;
     if (static_cast<long>(c.B) * a->H > kMaxBH || a->H / c.Hk > kMaxShared) return PDN_EUNSUPPORTED;
     if (static_cast<long>(c.max_new) * (a->H / c.Hk) > kMaxRows || !pdn::attn_paged_fits(*a)) return PDN_EUNSUPPORTED;
+    if (!near(c.page_size, c.k_st) || !near(c.page_size, c.v_st)) return PDN_EUNSUPPORTED;
     if (!aligned(a->lse, 4)) return PDN_EINVAL;
     if (c.N > 0) {
         if (!a->q || !a->o) return PDN_EINVAL;

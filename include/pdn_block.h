@@ -157,7 +157,7 @@ typedef struct pdn_add_norm_bwd_args {
  *                     rounded to bf16 for their product with v.
  *   o_dtype           PDN_F32, or PDN_BF16 where dtype is: o.
  *   window            keys that a query sees at most; 0 = all.
- *   scale             finite, > 0.
+ *   scale             finite, > 0, and so times log2(e).
  *   first             [B,Tq] int32 (device): the first key that each query may
  *                     see; NULL = 0.  So a row holds packed sequences (first = the
  *                     start of the query's own, counted in keys), padding before
@@ -166,8 +166,9 @@ typedef struct pdn_add_norm_bwd_args {
  *   k, v              strided [B,Hk,Tk,d].
  *   lse               [B,H,Tq] fp32; NULL = not written.
  *   workspace, workspace_bytes   at least pdn_attn_fwd_workspace_size() bytes.
- * PDN_EUNSUPPORTED where B * H passes 2^24, H / Hk 2^10, Tq H / Hk or Tk 2^30, or
- * the call's tiles (of 32 rows at least) a launch's 2^32 threads.
+ * PDN_EUNSUPPORTED where B * H passes 2^24, H / Hk 2^10, Tq H / Hk or Tk 2^30, the
+ * step from token to token of k or v (in the backward of q or dO too) 2^28
+ * elements, or the call's tiles (of 32 rows at least) a launch's 2^32 threads.
  */
 typedef struct pdn_attn_args {
     int32_t B, H, Hk, Tq, Tk, d;
@@ -285,6 +286,8 @@ typedef struct pdn_cache_append_args {
  *   q, o              strided [N,H,d] (strides sn, sh).
  *   lse               [N,H] fp32; NULL = not written.
  *   workspace, workspace_bytes   at least pdn_attn_paged_workspace_size() bytes.
+ * PDN_EUNSUPPORTED as pdn_attn_fwd's, max_new for Tq and a page's step from token to
+ * token for k's.
  */
 typedef struct pdn_attn_paged_args {
     pdn_cache cache;

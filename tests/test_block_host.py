@@ -184,6 +184,14 @@ REFUSED = [
 ]
 
 
+REFUSED += [  # steps from token to token past the lanes' offsets; a scale that log2(e) takes past fp32
+    ("pdn_attn_fwd", "EUNSUPPORTED", [dict(B=1, k_st=(1 << 28) + 8), dict(B=1, v_st=(1 << 28) + 8)]),
+    ("pdn_attn_fwd", "EINVAL", [dict(scale=3e38)]),
+    ("pdn_attn_bwd", "EUNSUPPORTED", [dict(fwd__q_st=(1 << 28) + 8), dict(do_st=(1 << 28) + 8), dict(fwd__k_st=1 << 29)]),
+    ("pdn_attn_paged", "EUNSUPPORTED", [dict(cache__k_st=(1 << 28) + 8), dict(cache__v_st=1 << 30)]),
+]
+
+
 @pytest.mark.parametrize("call,code,change", [(c, e, k) for c, e, ks in REFUSED for k in ks],
                          ids=lambda v: v if isinstance(v, str) else "-".join("%s=%s" % i for i in v.items()))
 def test_refusals(lib, call, code, change):
@@ -200,6 +208,14 @@ ACCEPTED = [
     ("pdn_attn_bwd", [dict(fwd__Tq=0), dict(fwd__Tk=0), dict(g_dtype=pdn.PDN_F32), dict(fwd__workspace=None), dict(fwd__o_dtype=pdn.PDN_F32)]),
     ("pdn_cache_append", [dict(cache__N=0, k=None), dict(cache__starts=None), dict(cache__d=8), dict(cache__max_new=0)]),
     ("pdn_attn_paged", [dict(cache__N=0, q=None, o=None), dict(cache__starts=None), dict(lse=None), dict(window=2 ** 31 - 1)]),
+]
+
+
+ACCEPTED += [
+    ("pdn_attn_fwd", [dict(k_st=1 << 28, v_st=1 << 28), dict(q_st=1 << 40), dict(Tk=1, k_st=1 << 40)]),
+    ("pdn_attn_bwd", [dict(fwd__q_st=1 << 28, do_st=1 << 28), dict(fwd__Tq=1, fwd__q_st=1 << 40)]),
+    ("pdn_attn_paged", [dict(cache__k_st=1 << 28, cache__v_st=1 << 28)]),
+    ("pdn_cache_append", [dict(k_sn=1 << 40)]),
 ]
 
 

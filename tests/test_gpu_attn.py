@@ -341,6 +341,25 @@ def test_far_strides():
         assert torch.equal(a, b)
 
 
+def test_furthest_token_steps():
+    """Whole tiles whose lanes' offsets use all of their 32 bits."""
+    torch, pdn = torch_mod(), _pdn()
+    T, d, step = 64, 64, 1 << 28
+    base = torch.empty((T - 1) * step + 8 * d, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator().manual_seed(62)
+    near = [_rand(gen, 1, 1, T, d, dtype="bf16") for _ in range(4)]
+    far = [base.as_strided((1, 1, T, d), (T * step, T * step, step, 1), i * d) for i in range(4)]
+    for a, b in zip(far, near):
+        a.copy_(b)
+    got = []
+    for q, k, v, do in (near, far):
+        out, lse = [torch.empty_like(near[0]) for _ in range(4)], torch.empty(1, 1, T, device="cuda")
+        pdn.pdn_attn_fwd(q, k, v, out[0], lse=lse)
+        pdn.pdn_attn_bwd(q, k, v, out[0], do, lse, *out[1:])
+        got.append(out + [lse])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 def test_gradient_against_differences():
     """dq, dk and dv of the fp32 kernel against differences of its own forward."""
     torch, pdn = torch_mod(), _pdn()
