@@ -68,12 +68,12 @@ __device__ __forceinline__ void store4(void* p, long at, int f32, const f32x4& x
     else *reinterpret_cast<bf16x4*>(static_cast<uint16_t*>(p) + at) = __builtin_convertvector(x, bf16x4);
 }
 
-template <bool BF16, int D, int QB>
-__global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_kernel(BwdParams p) {
+template <bool BF16, int D>
+__global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dq_kernel(BwdParams p) {
     using E = El<BF16>;
     using TL = Tile<BF16, D>;
     typedef typename E::Frag Frag;
-    constexpr int ROWS = 128 * QB, KT = !BF16 && D == 128 ? 32 : 64;
+    constexpr int ROWS = 128, KT = !BF16 && D == 128 ? 32 : 64;
     constexpr int S = D / 16, C = D / 32, KB = KT / 32;
     constexpr int TILE = KT * TL::ROW, DMAS = KT / TL::ROWS_PER_DMA / 4;
     __shared__ __align__(1024) char smem[4 * TILE];
@@ -89,57 +89,47 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
     const int row0 = tile * ROWS, nrows = nq * p.shared;
 
     const int t0 = row0 / p.shared, m0 = row0 - t0 * p.shared;
-    int token[QB], head[QB];
-    bool stored[QB];
-    Seen seen[QB];
-    Frag q[QB][S], dof[QB][S];
-    float lse2[QB], delta[QB];
+    const int dr = 32 * wave + (lane & 31);
+    const bool stored = row0 + dr < nrows;
+    const int r = m0 + (stored ? dr : nrows - 1 - row0), dt = quotient(r, p.inverse), token = t0 + dt, head = hk * p.shared + r - dt * p.shared;
+    const Seen seen = seen_by(token, nq, nk, p.window, p.first ? p.first[static_cast<long>(b) * nq + token] : 0);
     int low = INT32_MAX, high = -1, full_low = 0, full_high = INT32_MAX;
-#pragma unroll
-    for (int a = 0; a < QB; ++a) {
-        const int dr = 32 * (wave * QB + a) + (lane & 31);
-        stored[a] = row0 + dr < nrows;
-        const int r = m0 + (stored[a] ? dr : nrows - 1 - row0), dt = quotient(r, p.inverse);
-        token[a] = t0 + dt;
-        head[a] = hk * p.shared + r - dt * p.shared;
-        const int f = p.first ? p.first[static_cast<long>(b) * nq + token[a]] : 0;
-        seen[a] = seen_by(token[a], nq, nk, p.window, f);
-        if (seen[a].count > 0) {
-            const int last = seen[a].low + seen[a].count - 1;
-            low = min(low, seen[a].low);
-            high = max(high, last);
-            full_low = max(full_low, seen[a].low);
-            full_high = min(full_high, last);
-        }
-        const long qa = b * p.q.sb + head[a] * p.q.sh + token[a] * p.q.st;
-        const long oa = b * p.o.sb + head[a] * p.o.sh + token[a] * p.o.st;
-        const long da = b * p.d_o.sb + head[a] * p.d_o.sh + token[a] * p.d_o.st;
-        const long row = (static_cast<long>(b) * p.H + head[a]) * nq + token[a];
-        float dot = 0.0f;
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const int ch = 16 * s + 8 * h;
-            q[a][s] = E::load(p.q.p, qa + ch);
-            f32x8 x, y;
-            if (!BF16 || p.o_f32) {
-                x = El<false>::load(p.o.p, oa + ch);
-                y = El<false>::load(p.d_o.p, da + ch);
-                if constexpr (BF16) dof[a][s] = __builtin_convertvector(y, bf16x8);
-                else dof[a][s] = y;
-                if constexpr (BF16) {
-                    if (stored[a] && split == 0) *reinterpret_cast<bf16x8*>(p.do16 + row * D + ch) = dof[a][s];
-                }
-            } else if constexpr (BF16) {
-                x = __builtin_convertvector(El<true>::load(p.o.p, oa + ch), f32x8);
-                dof[a][s] = E::load(p.d_o.p, da + ch);
-                y = __builtin_convertvector(dof[a][s], f32x8);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) dot = fmaf(x[j], y[j], dot);
-        }
-        delta[a] = dot + __shfl_xor(dot, 32, 64);
-        lse2[a] = p.lse[row] * kLog2e;
+    if (seen.count > 0) {
+        const int last = seen.low + seen.count - 1;
+        low = min(low, seen.low);
+        high = max(high, last);
+        full_low = max(full_low, seen.low);
+        full_high = min(full_high, last);
     }
+    const long qa = b * p.q.sb + head * p.q.sh + token * p.q.st;
+    const long oa = b * p.o.sb + head * p.o.sh + token * p.o.st;
+    const long da = b * p.d_o.sb + head * p.d_o.sh + token * p.d_o.st;
+    const long row = (static_cast<long>(b) * p.H + head) * nq + token;
+    Frag q[S], dof[S];
+    float dot = 0.0f;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const int ch = 16 * s + 8 * h;
+        q[s] = E::load(p.q.p, qa + ch);
+        f32x8 x, y;
+        if (!BF16 || p.o_f32) {
+            x = El<false>::load(p.o.p, oa + ch);
+            y = El<false>::load(p.d_o.p, da + ch);
+            if constexpr (BF16) dof[s] = __builtin_convertvector(y, bf16x8);
+            else dof[s] = y;
+            if constexpr (BF16) {
+                if (stored && split == 0) *reinterpret_cast<bf16x8*>(p.do16 + row * D + ch) = dof[s];
+            }
+        } else if constexpr (BF16) {
+            x = __builtin_convertvector(El<true>::load(p.o.p, oa + ch), f32x8);
+            dof[s] = E::load(p.d_o.p, da + ch);
+            y = __builtin_convertvector(dof[s], f32x8);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dot = fmaf(x[j], y[j], dot);
+    }
+    float delta = dot + __shfl_xor(dot, 32, 64);
+    const float lse2 = p.lse[row] * kLog2e;
     low = uniform(wave_min_i(low));
     high = uniform(wave_max_i(high));
     full_low = uniform(wave_max_i(full_low));
@@ -185,13 +175,11 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
         }
     };
 
-    f32x16 acc[QB][C];
+    f32x16 acc[C];
 #pragma unroll
-    for (int a = 0; a < QB; ++a)
+    for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[a][c][i] = 0.0f;
+        for (int i = 0; i < 16; ++i) acc[c][i] = 0.0f;
 
     // A block of 32 keys.  `partly`: some rows may not see all of them.  A key that is not
     // finite gives scores that are not: it is taken out of the product for those that do not
@@ -199,56 +187,47 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
     auto block = [&](int k0, uint32_t kt, auto partly) __attribute__((always_inline)) {
         constexpr bool PARTLY = decltype(partly)::value;
         const uint32_t kr = kt + row_base, kc = kt + column_base, vr = kr + TILE;
-        f32x16 s[QB], dp[QB];
+        f32x16 s, dp;
 #pragma unroll
-        for (int a = 0; a < QB; ++a)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[a][i] = dp[a][i] = 0.0f;
+        for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
 #pragma unroll
         for (int st = 0; st < S; ++st) {
             const Frag kf = TL::rows(kr, 0, st);
-#pragma unroll
-            for (int a = 0; a < QB; ++a) s[a] = E::mma(kf, q[a][st], s[a]);
+            s = E::mma(kf, q[st], s);
         }
 #pragma unroll
         for (int st = 0; st < S; ++st) {
             const Frag vf = TL::rows(vr, 0, st);
-#pragma unroll
-            for (int a = 0; a < QB; ++a) dp[a] = E::mma(vf, dof[a][st], dp[a]);
+            dp = E::mma(vf, dof[st], dp);
         }
         bool dirty = false;
         if constexpr (PARTLY) {
             bool any = false;
 #pragma unroll
-            for (int a = 0; a < QB; ++a)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) any |= !(fabsf(s[a][i]) < INFINITY);
+            for (int i = 0; i < 16; ++i) any |= !(fabsf(s[i]) < INFINITY);
             dirty = __ballot(any) != 0;
         }
-        Frag df[QB][2];
+        Frag df[2];
 #pragma unroll
-        for (int a = 0; a < QB; ++a) {
+        for (int i = 0; i < 16; ++i) s[i] = ex2(fmaf(s[i], p.c, -lse2));
+        if constexpr (PARTLY) {
+            const Seen to = {opaque(seen.low - k0 - 4 * h), seen.count};
+            float dot = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[a][i] = ex2(fmaf(s[a][i], p.c, -lse2[a]));
-            if constexpr (PARTLY) {
-                const Seen to = {opaque(seen[a].low - k0 - 4 * h), seen[a].count};
-                float dot = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    if (!sees(to, 8 * (i >> 2) + (i & 3))) s[a][i] = dp[a][i] = 0.0f;
-                    dot = fmaf(s[a][i], dp[a][i], dot);
-                }
-                // Where all that a row sees lies in this block, D is formed from it: a row of few
-                // keys is where the rounding of o to bf16 would show most (alone it sees itself,
-                // and its gradients vanish).
-                dot = halves<false>(dot);
-                if (seen[a].low >= k0 && seen[a].low + seen[a].count <= k0 + 32) delta[a] = dot;
+            for (int i = 0; i < 16; ++i) {
+                if (!sees(to, 8 * (i >> 2) + (i & 3))) s[i] = dp[i] = 0.0f;
+                dot = fmaf(s[i], dp[i], dot);
             }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[a][i] *= dp[a][i] - delta[a];
-            df[a][0] = E::of(s[a], 0);
-            df[a][1] = E::of(s[a], 1);
+            // Where all that a row sees lies in this block, D is formed from it: a row of few
+            // keys is where the rounding of o to bf16 would show most (alone it sees itself,
+            // and its gradients vanish).
+            dot = halves<false>(dot);
+            if (seen.low >= k0 && seen.low + seen.count <= k0 + 32) delta = dot;
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] *= dp[i] - delta;
+        df[0] = E::of(s, 0);
+        df[1] = E::of(s, 1);
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -256,8 +235,7 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
                 Frag kf = TL::columns(kc, 16 * u, c);
                 if constexpr (PARTLY)
                     if (dirty) kf = E::finite(kf);
-#pragma unroll
-                for (int a = 0; a < QB; ++a) acc[a][c] = E::mma(kf, df[a][u], acc[a][c]);
+                acc[c] = E::mma(kf, df[u], acc[c]);
             }
     };
 
@@ -291,38 +269,34 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB == 1 ? 2 : 1) attn_dq_ker
         for (int e = 0; e < KB; ++e) block(0, kt + 32 * e * TL::ROW, std::false_type());
     }
     some(end_tile);
-#pragma unroll
-    for (int a = 0; a < QB; ++a) {
-        if (!stored[a]) continue;
-        const long row = (static_cast<long>(b) * p.H + head[a]) * nq + token[a];
-        // for the pass over the keys, from the one part that begins with what the row sees
-        const int first = seen[a].low / KT;
-        if (h == 0 && (seen[a].count > 0 ? first_tile <= first && first < end_tile : split == 0)) {
-            p.delta[row] = delta[a];
-            p.lse2[row] = lse2[a];
-        }
-        const long out = p.splits > 1 ? (split * p.rows + row) * D : b * p.dq.sb + head[a] * p.dq.sh + token[a] * p.dq.st;
-        const float scale = p.splits > 1 ? 1.0f : p.scale;
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                f32x4 x;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = seen[a].count > 0 ? acc[a][c][4 * g + i] * scale : 0.0f;
-                if (p.splits > 1) store4<false>(p.part, out + 32 * c + 8 * g + 4 * h, 1, x);
-                else store4<BF16>(p.dq.p, out + 32 * c + 8 * g + 4 * h, p.g_f32, x);
-            }
+    if (!stored) return;
+    // for the pass over the keys, from the one part that begins with what the row sees
+    const int first = seen.low / KT;
+    if (h == 0 && (seen.count > 0 ? first_tile <= first && first < end_tile : split == 0)) {
+        p.delta[row] = delta;
+        p.lse2[row] = lse2;
     }
+    const long out = p.splits > 1 ? (split * p.rows + row) * D : b * p.dq.sb + head * p.dq.sh + token * p.dq.st;
+    const float scale = p.splits > 1 ? 1.0f : p.scale;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            f32x4 x;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = seen.count > 0 ? acc[c][4 * g + i] * scale : 0.0f;
+            if (p.splits > 1) store4<false>(p.part, out + 32 * c + 8 * g + 4 * h, 1, x);
+            else store4<BF16>(p.dq.p, out + 32 * c + 8 * g + 4 * h, p.g_f32, x);
+        }
 }
 
 // PARTS: the workgroups of a block of keys are p.splits.
-template <bool BF16, int D, int KB, bool PARTS>
+template <bool BF16, int D, bool PARTS>
 __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dkv_kernel(BwdParams p) {
     using E = El<BF16>;
     using TL = Tile<BF16, D>;
     typedef typename E::Frag Frag;
-    constexpr int KEYS = 128 * KB, QT = kQueries;
+    constexpr int KEYS = 128, QT = kQueries;
     constexpr int S = D / 16, C = D / 32;
     constexpr int TILE = QT * TL::ROW, DMAS = QT / TL::ROWS_PER_DMA / 4;
     constexpr int VALUES = KEYS * TL::ROW, V_DMAS = KEYS / TL::ROWS_PER_DMA / 4;
@@ -341,17 +315,13 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dkv_kernel(BwdPar
     const int nq = p.Tq, nk = p.Tk, off = nk - nq;
     const int key0 = tile * KEYS, key1 = min(key0 + KEYS, nk) - 1;
 
-    // this lane's keys; those behind the last repeat it, unstored and unseen
-    int key[KB];
-    Frag k[KB][S];
+    // this lane's key; those behind the last repeat it, unstored and unseen
+    Frag k[S];
+    const int key = key0 + 32 * wave + (lane & 31);
+    const long j = min(key, nk - 1);
+    const long ka = b * p.k.sb + hk * p.k.sh + j * p.k.st;
 #pragma unroll
-    for (int a = 0; a < KB; ++a) {
-        key[a] = key0 + 32 * (wave * KB + a) + (lane & 31);
-        const long j = min(key[a], nk - 1);
-        const long ka = b * p.k.sb + hk * p.k.sh + j * p.k.st;
-#pragma unroll
-        for (int s = 0; s < S; ++s) k[a][s] = E::load(p.k.p, ka + 16 * s + 8 * h);
-    }
+    for (int s = 0; s < S; ++s) k[s] = E::load(p.k.p, ka + 16 * s + 8 * h);
 
     // the tiles of queries that see some of these keys
     int begin = max(key0 - off, 0) / QT, end = nq;
@@ -378,13 +348,11 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dkv_kernel(BwdPar
     end = uniform(end);
 
     if (!p.first && tid < 64) stats[0][2][tid] = stats[1][2][tid] = __int_as_float(INT32_MIN);  // before the first barrier
-    f32x16 dk[KB][C], dv[KB][C];
+    f32x16 dk[C], dv[C];
 #pragma unroll
-    for (int a = 0; a < KB; ++a)
+    for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) dk[a][c][i] = dv[a][c][i] = 0.0f;
+        for (int i = 0; i < 16; ++i) dk[c][i] = dv[c][i] = 0.0f;
 
     const uint32_t at = lds_address(smem), row_base = TL::row_base(lane), column_base = TL::column_base(lane);
     const bool copied = BF16 && p.o_f32;
@@ -442,73 +410,64 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dkv_kernel(BwdPar
         // (nothing that follows from the lane stays from block to block: there is no register for it)
         const uint32_t row = opaque(row_base), column = opaque(column_base);
         const uint32_t qr = qt + row, qc = qt + column, dr = qr + TILE, dc = qc + TILE;
-        const uint32_t vr = at + 4 * TILE + 32 * KB * wave * TL::ROW + row;
+        const uint32_t vr = at + 4 * TILE + 32 * wave * TL::ROW + row;
         const float* deltas = lses + 64;
-        f32x16 s[KB], dp[KB];
+        f32x16 s, dp;
 #pragma unroll
-        for (int a = 0; a < KB; ++a)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[a][i] = dp[a][i] = 0.0f;
+        for (int i = 0; i < 16; ++i) s[i] = dp[i] = 0.0f;
 #pragma unroll
         for (int st = 0; st < S; ++st) {
             const Frag f = TL::rows(qr, 0, st);
-#pragma unroll
-            for (int a = 0; a < KB; ++a) s[a] = E::mma(f, k[a][st], s[a]);
+            s = E::mma(f, k[st], s);
         }
 #pragma unroll
         for (int st = 0; st < S; ++st) {
             const Frag f = TL::rows(dr, 0, st);
-#pragma unroll
-            for (int a = 0; a < KB; ++a) dp[a] = E::mma(f, TL::rows(vr, 32 * a, st), dp[a]);
+            dp = E::mma(f, TL::rows(vr, 0, st), dp);
         }
         bool dirty = false;
         if constexpr (PARTLY) {
             bool any = false;
 #pragma unroll
-            for (int a = 0; a < KB; ++a)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) any |= !(fabsf(s[a][i]) < INFINITY) || !(fabsf(dp[a][i]) < INFINITY);
+            for (int i = 0; i < 16; ++i) any |= !(fabsf(s[i]) < INFINITY) || !(fabsf(dp[i]) < INFINITY);
             dirty = __ballot(any) != 0;
         }
-        Frag pf[KB][2], df[KB][2];
+        Frag pf[2], df[2];
 #pragma unroll
-        for (int a = 0; a < KB; ++a) {
+        for (int e = 0; e < 4; ++e) {
+            const f32x4 lse = *reinterpret_cast<const f32x4*>(lses + 8 * e + 4 * h);
+            const f32x4 dl = *reinterpret_cast<const f32x4*>(deltas + 8 * e + 4 * h);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int x = 4 * e + i;
+                s[x] = ex2(fmaf(s[x], p.c, -lse[i]));
+                dp[x] = s[x] * (dp[x] - dl[i]);
+                if constexpr (PARTLY)
+                    if (dirty) s[x] += 0.0f * dl[i];
+            }
+        }
+        if constexpr (PARTLY) {
+            // query r of the block sees the key from r = from on, to the window's end, and
+            // where its first key is not behind it
+            const int from = opaque(key - off - i0 - 4 * h);
+            int to = nq - i0 - 4 * h;
+            if (p.window > 0) to = min(to, from + p.window);
+            if (key >= nk) to = INT32_MIN;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const f32x4 lse = *reinterpret_cast<const f32x4*>(lses + 8 * e + 4 * h);
-                const f32x4 dl = *reinterpret_cast<const f32x4*>(deltas + 8 * e + 4 * h);
+                const f32x4 first = *reinterpret_cast<const f32x4*>(deltas + 64 + 8 * e + 4 * h);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int x = 4 * e + i;
-                    s[a][x] = ex2(fmaf(s[a][x], p.c, -lse[i]));
-                    dp[a][x] = s[a][x] * (dp[a][x] - dl[i]);
-                    if constexpr (PARTLY)
-                        if (dirty) s[a][x] += 0.0f * dl[i];
+                    const int x = 4 * e + i, r = 8 * e + i;
+                    const bool seen = (r >= from) & (r < to) & (__float_as_int(first[i]) <= key);
+                    if (!seen) s[x] = dp[x] = 0.0f;
                 }
             }
-            if constexpr (PARTLY) {
-                // query r of the block sees the key from r = from on, to the window's end, and
-                // where its first key is not behind it
-                const int from = opaque(key[a] - off - i0 - 4 * h);
-                int to = nq - i0 - 4 * h;
-                if (p.window > 0) to = min(to, from + p.window);
-                if (key[a] >= nk) to = INT32_MIN;
+        }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const f32x4 first = *reinterpret_cast<const f32x4*>(deltas + 64 + 8 * e + 4 * h);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int x = 4 * e + i, r = 8 * e + i;
-                        const bool seen = (r >= from) & (r < to) & (__float_as_int(first[i]) <= key[a]);
-                        if (!seen) s[a][x] = dp[a][x] = 0.0f;
-                    }
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                pf[a][u] = E::of(s[a], u);
-                df[a][u] = E::of(dp[a], u);
-            }
+        for (int u = 0; u < 2; ++u) {
+            pf[u] = E::of(s, u);
+            df[u] = E::of(dp, u);
         }
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -520,17 +479,14 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dkv_kernel(BwdPar
                         x = E::finite(x);
                         y = E::finite(y);
                     }
-#pragma unroll
-                for (int a = 0; a < KB; ++a) {
-                    dv[a][c] = E::mma(x, pf[a][u], dv[a][c]);
-                    dk[a][c] = E::mma(y, df[a][u], dk[a][c]);
-                }
+                dv[c] = E::mma(x, pf[u], dv[c]);
+                dk[c] = E::mma(y, df[u], dk[c]);
             }
     };
 
     // The tiles of each head in turn; runs of those whose queries all see all of the wave's
     // keys in a loop of their own.
-    const int w0 = key0 + 32 * KB * wave, w1 = w0 + 32 * KB - 1;  // this wave's keys
+    const int w0 = key0 + 32 * wave, w1 = w0 + 31;  // this wave's keys
     int count = end > begin ? (end - begin) * p.shared : 0, t = begin;
     if (PARTS && count > 0) {  // this part of them
         const int each = (count + splits - 1) / splits, from = min(split * each, count), g = from / (end - begin);
@@ -582,32 +538,29 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dkv_kernel(BwdPar
                 block(0, at + buffer * 2 * TILE + 32 * e * TL::ROW, &stats[buffer][0][32 * e], std::false_type());
         }
     }
+    if (key >= nk) return;
+    const long row = (static_cast<long>(b) * p.Hk + hk) * nk + key;
+    const long ko = !PARTS ? b * p.dk.sb + hk * p.dk.sh + key * p.dk.st : (split * p.rows + row) * D;
+    const long vo = !PARTS ? b * p.dv.sb + hk * p.dv.sh + key * p.dv.st : ((splits + split) * p.rows + row) * D;
+    const float scale = !PARTS ? p.scale : 1.0f;
 #pragma unroll
-    for (int a = 0; a < KB; ++a) {
-        if (key[a] >= nk) continue;
-        const long row = (static_cast<long>(b) * p.Hk + hk) * nk + key[a];
-        const long ko = !PARTS ? b * p.dk.sb + hk * p.dk.sh + key[a] * p.dk.st : (split * p.rows + row) * D;
-        const long vo = !PARTS ? b * p.dv.sb + hk * p.dv.sh + key[a] * p.dv.st : ((splits + split) * p.rows + row) * D;
-        const float scale = !PARTS ? p.scale : 1.0f;
+    for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+        for (int e = 0; e < 4; ++e) {
+            f32x4 x, y;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                f32x4 x, y;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[i] = dk[a][c][4 * e + i] * scale;
-                    y[i] = dv[a][c][4 * e + i];
-                }
-                if constexpr (!PARTS) {
-                    store4<BF16>(p.dk.p, ko + 32 * c + 8 * e + 4 * h, p.g_f32, x);
-                    store4<BF16>(p.dv.p, vo + 32 * c + 8 * e + 4 * h, p.g_f32, y);
-                } else {
-                    store4<false>(p.part, ko + 32 * c + 8 * e + 4 * h, 1, x);
-                    store4<false>(p.part, vo + 32 * c + 8 * e + 4 * h, 1, y);
-                }
+            for (int i = 0; i < 4; ++i) {
+                x[i] = dk[c][4 * e + i] * scale;
+                y[i] = dv[c][4 * e + i];
             }
-    }
+            if constexpr (!PARTS) {
+                store4<BF16>(p.dk.p, ko + 32 * c + 8 * e + 4 * h, p.g_f32, x);
+                store4<BF16>(p.dv.p, vo + 32 * c + 8 * e + 4 * h, p.g_f32, y);
+            } else {
+                store4<false>(p.part, ko + 32 * c + 8 * e + 4 * h, 1, x);
+                store4<false>(p.part, vo + 32 * c + 8 * e + 4 * h, 1, y);
+            }
+        }
 }
 
 // The parts' sums of each row added up, in their order: D / 4 lanes to a row.
@@ -686,7 +639,7 @@ hipError_t launch(BwdParams p, int B, const Layout& l, hipStream_t stream) {
         p.tiles = static_cast<int>((rows + 127) / 128);
         p.splits = l.q_splits;
         p.rows = rows * heads;
-        attn_dq_kernel<BF16, D, 1><<<dim3(static_cast<unsigned>(heads * p.tiles * p.splits)), block, 0, stream>>>(p);
+        attn_dq_kernel<BF16, D><<<dim3(static_cast<unsigned>(heads * p.tiles * p.splits)), block, 0, stream>>>(p);
         rc = hipGetLastError();
         if (rc == hipSuccess && p.splits > 1) rc = add_parts<BF16, D>(p, p.part, p.dq, p.H, p.Tq, p.scale, stream);
     }
@@ -695,8 +648,8 @@ hipError_t launch(BwdParams p, int B, const Layout& l, hipStream_t stream) {
         p.splits = l.k_splits;
         p.rows = heads * p.Tk;
         const dim3 grid(static_cast<unsigned>(heads * p.tiles * p.splits));
-        if (p.splits > 1) attn_dkv_kernel<BF16, D, 1, true><<<grid, block, 0, stream>>>(p);
-        else attn_dkv_kernel<BF16, D, 1, false><<<grid, block, 0, stream>>>(p);
+        if (p.splits > 1) attn_dkv_kernel<BF16, D, true><<<grid, block, 0, stream>>>(p);
+        else attn_dkv_kernel<BF16, D, false><<<grid, block, 0, stream>>>(p);
         rc = hipGetLastError();
         if (rc == hipSuccess && p.splits > 1) rc = add_parts<BF16, D>(p, p.part, p.dk, p.Hk, p.Tk, p.scale, stream);
         if (rc == hipSuccess && p.splits > 1) rc = add_parts<BF16, D>(p, p.part + p.splits * p.rows * D, p.dv, p.Hk, p.Tk, 1.0f, stream);

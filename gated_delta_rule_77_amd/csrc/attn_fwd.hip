@@ -6,7 +6,7 @@
 // key head are rows of one tile beside the tokens (row = token * shared + head), so
 // that a tile of keys is read once for all of them and a tile's diagonal is short.
 //
-// A workgroup is four waves.  WK = 1: each wave holds 32 QB rows of its own and the
+// A workgroup is four waves.  WK = 1: each wave holds 32 rows of its own and the
 // waves share tiles of KT keys in LDS, loaded one tile ahead past the registers.
 // WK > 1 (few rows, a decode step above all): WK waves share the rows, each takes
 // its part of every tile's keys, and their sums are joined at the end.  Where the
@@ -50,24 +50,21 @@ constexpr int kFewParts = 8;     // that a row's lanes join one after another
 // fp32 and, as bf16 factors, as exact as any.
 constexpr float kSlack = 8.0f;
 
-// Tiles of keys in flight: one being read, one being loaded.
-constexpr int kBuffers = 2;
-
-template <bool BF16, int D, int QB, int WK, int KT, bool PAGED>
-__global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128 * 128 ? 2 : 1) attn_fwd_kernel(FwdParams p) {
+template <bool BF16, int D, int WK, int KT, bool PAGED>
+__global__ void __launch_bounds__(kThreads, BF16 && KT * D < 128 * 128 ? 2 : 1) attn_fwd_kernel(FwdParams p) {
     using E = El<BF16>;
     using TL = Tile<BF16, D>;
     typedef typename E::Frag Frag;
     constexpr int WR = 4 / WK;                 // waves with rows of their own
-    constexpr int ROWS = 32 * QB * WR;         // of the workgroup
+    constexpr int ROWS = 32 * WR;              // of the workgroup
     constexpr int KB = KT / 32 / WK;           // a wave's blocks of 32 keys in a tile
     constexpr int S = D / 16, C = D / 32;
     constexpr int TILE = KT * TL::ROW, DMAS = KT / TL::ROWS_PER_DMA / 4;
     constexpr bool ALONE = WK == 4 && KB == 1;  // a wave reads the 32 rows of each tile that it loads
     static_assert(KB >= 1 && DMAS >= 1, "every wave has keys to read and rows to load");
-    __shared__ __align__(1024) char smem[kBuffers * 2 * TILE];
+    __shared__ __align__(1024) char smem[4 * TILE];  // keys and values of two tiles: one being read, one being loaded
     __shared__ int bounds[2][4];
-    __shared__ float joined[WK > 1 ? 2 : 1][WK > 1 ? 4 : 1][32 * QB];
+    __shared__ float joined[WK > 1 ? 2 : 1][WK > 1 ? 4 : 1][32];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int h = lane >> 5;
@@ -99,33 +96,23 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
     const int row0 = tile * ROWS, nrows = nq * p.shared;
     if (row0 >= nrows) return;
 
-    // this lane's rows: their tokens, heads and keys; rows behind the last repeat it, unstored
+    // this lane's row: its token, head and keys; rows behind the last repeat it, unstored
     const int t0 = row0 / p.shared, m0 = row0 - t0 * p.shared;
-    int token[QB], head[QB];
-    bool stored[QB];
-    Seen seen[QB];
-    Frag q[QB][S];
+    const int dr = 32 * (wave / WK) + (lane & 31);
+    const bool stored = row0 + dr < nrows;
+    const int r = m0 + (stored ? dr : nrows - 1 - row0), dt = quotient(r, p.inverse), token = t0 + dt, head = hk * p.shared + r - dt * p.shared;
+    const Seen seen = seen_by(token, nq, nk, p.window, !PAGED && p.first ? p.first[static_cast<long>(b) * p.Tq + token] : 0);
     int low = INT32_MAX, high = -1, full_low = 0, full_high = INT32_MAX;
-#pragma unroll
-    for (int a = 0; a < QB; ++a) {
-        const int dr = 32 * ((wave / WK) * QB + a) + (lane & 31);
-        stored[a] = row0 + dr < nrows;
-        const int r = m0 + (stored[a] ? dr : nrows - 1 - row0), dt = quotient(r, p.inverse);
-        token[a] = t0 + dt;
-        head[a] = hk * p.shared + r - dt * p.shared;
-        const int f = !PAGED && p.first ? p.first[static_cast<long>(b) * p.Tq + token[a]] : 0;
-        seen[a] = seen_by(token[a], nq, nk, p.window, f);
-        if (seen[a].count > 0) {
-            const int last = seen[a].low + seen[a].count - 1;
-            low = min(low, seen[a].low);
-            high = max(high, last);
-            full_low = max(full_low, seen[a].low);
-            full_high = min(full_high, last);
-        }
-        const char* at = qb + (token[a] * p.q_st + head[a] * p.q_sh) * E::BYTES;
-#pragma unroll
-        for (int s = 0; s < S; ++s) q[a][s] = E::load(at, 16 * s + 8 * h);
+    if (seen.count > 0) {
+        const int last = seen.low + seen.count - 1;
+        low = min(low, seen.low);
+        high = max(high, last);
+        full_low = max(full_low, seen.low);
+        full_high = min(full_high, last);
     }
+    Frag q[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) q[s] = E::load(qb + (token * p.q_st + head * p.q_sh) * E::BYTES, 16 * s + 8 * h);
     low = uniform(wave_min_i(low));
     high = uniform(wave_max_i(high));
     full_low = uniform(wave_max_i(full_low));
@@ -200,162 +187,128 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
     };
 
     // 0 v, summed over the channels, of a block's keys: a result's rows
-    auto times_zero = [&](uint32_t vr, int r0) __attribute__((always_inline)) {
+    auto times_zero = [&](uint32_t vr) __attribute__((always_inline)) {
         f32x16 x;
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = 0.0f;
 #pragma unroll
-        for (int st = 0; st < S; ++st) x = E::mma(TL::rows(vr, r0, st), E::zero(), x);
+        for (int st = 0; st < S; ++st) x = E::mma(TL::rows(vr, 0, st), E::zero(), x);
         return x;
     };
-    auto not_finite = [&](uint32_t vr, int r0) __attribute__((always_inline)) {
-        const f32x16 x = times_zero(vr, r0);
+    auto not_finite = [&](uint32_t vr) __attribute__((always_inline)) {
+        const f32x16 x = times_zero(vr);
         bool any = false;
 #pragma unroll
         for (int i = 0; i < 16; ++i) any |= x[i] != x[i];
         return __ballot(any);
     };
 
-    f32x16 acc[QB][C];
-    float mc[QB], sum[QB];   // maximum times c; this half wave's part of the sum
+    f32x16 acc[C];
+    float mc = -INFINITY, sum = 0.0f;   // maximum times c; this half wave's part of the sum
 #pragma unroll
-    for (int a = 0; a < QB; ++a) {
-        mc[a] = -INFINITY;
-        sum[a] = 0.0f;
+    for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[a][c][i] = 0.0f;
-    }
+        for (int i = 0; i < 16; ++i) acc[c][i] = 0.0f;
 
     // The maximum moved where a row's scores pass it (each row by itself: what another
     // holds has no part in its rounding either).
-    auto move = [&](const float (&top)[QB]) __attribute__((always_inline)) {
-        bool moves = false;
-#pragma unroll
-        for (int a = 0; a < QB; ++a) moves |= top[a] > mc[a] + kSlack;
+    auto move = [&](float top) __attribute__((always_inline)) {
+        const bool moves = top > mc + kSlack;
         if (__ballot(moves) == 0) return;
+        const float to = moves ? top : mc;
+        const float by = to == mc ? 1.0f : ex2(mc - to);
+        mc = to;
+        sum *= by;
 #pragma unroll
-        for (int a = 0; a < QB; ++a) {
-            const float to = top[a] > mc[a] + kSlack ? top[a] : mc[a];
-            const float by = to == mc[a] ? 1.0f : ex2(mc[a] - to);
-            mc[a] = to;
-            sum[a] *= by;
+        for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) acc[a][c][i] *= by;
-        }
+            for (int i = 0; i < 16; ++i) acc[c][i] *= by;
     };
 
     // a block of 32 keys of which some rows may not see all
-    auto some_seen = [&](int r0, int k0, uint32_t kt, uint32_t vt) __attribute__((always_inline)) {
+    auto some_seen = [&](int k0, uint32_t kt, uint32_t vt) __attribute__((always_inline)) {
         if (k0 > high || k0 + 31 < low) return;
         const uint32_t kr = kt + row_base, vr = vt + row_base, vc = vt + column_base;
-        f32x16 s[QB];
+        f32x16 s;
 #pragma unroll
-        for (int a = 0; a < QB; ++a)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[a][i] = 0.0f;
+        for (int i = 0; i < 16; ++i) s[i] = 0.0f;
 #pragma unroll
         for (int st = 0; st < S; ++st) {
-            const Frag kf = TL::rows(kr, r0, st);
-#pragma unroll
-            for (int a = 0; a < QB; ++a) s[a] = E::mma(kf, q[a][st], s[a]);
+            const Frag kf = TL::rows(kr, 0, st);
+            s = E::mma(kf, q[st], s);
         }
         // Unseen keys: no part in the maximum, a probability of zero.  Zero times a value
         // that is not finite would still be NaN: such values (which 0 v shows) are taken out
         // of the product, and make the probabilities of those that see them NaN instead.
-        const bool dirty = not_finite(vr, r0) != 0;
-        float top[QB];
+        const bool dirty = not_finite(vr) != 0;
+        const Seen to = {opaque(seen.low - k0 - 4 * h), seen.count};
+        float x = -INFINITY;
 #pragma unroll
-        for (int a = 0; a < QB; ++a) {
-            const Seen to = {opaque(seen[a].low - k0 - 4 * h), seen[a].count};
-            float x = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (!sees(to, 8 * (i >> 2) + (i & 3))) s[a][i] = -INFINITY;
-                x = fmaxf(x, s[a][i]);
-            }
-            top[a] = halves<true>(x) * p.c;
+        for (int i = 0; i < 16; ++i) {
+            if (!sees(to, 8 * (i >> 2) + (i & 3))) s[i] = -INFINITY;
+            x = fmaxf(x, s[i]);
         }
-        move(top);
-        Frag pf[QB][2];
+        move(halves<true>(x) * p.c);
+        Frag pf[2];
+        const float m = mc == -INFINITY ? 0.0f : mc;
+        float add = 0.0f;
 #pragma unroll
-        for (int a = 0; a < QB; ++a) {
-            const float m = mc[a] == -INFINITY ? 0.0f : mc[a];
-            float add = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                s[a][i] = ex2(fmaf(s[a][i], p.c, -m));
-                add += s[a][i];
-            }
-            sum[a] += add;
-            if (dirty) {
-                const f32x16 poison = times_zero(vr, r0);
-                const Seen to = {opaque(seen[a].low - k0 - 4 * h), seen[a].count};
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (sees(to, 8 * (i >> 2) + (i & 3))) s[a][i] += poison[i];
-            }
-            pf[a][0] = E::of(s[a], 0);
-            pf[a][1] = E::of(s[a], 1);
+        for (int i = 0; i < 16; ++i) {
+            s[i] = ex2(fmaf(s[i], p.c, -m));
+            add += s[i];
         }
+        sum += add;
+        if (dirty) {
+            const f32x16 poison = times_zero(vr);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (sees(to, 8 * (i >> 2) + (i & 3))) s[i] += poison[i];
+        }
+        pf[0] = E::of(s, 0);
+        pf[1] = E::of(s, 1);
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                Frag vf = TL::columns(vc, r0 + 16 * u, c);
+                Frag vf = TL::columns(vc, 16 * u, c);
                 if (dirty) vf = E::finite(vf);
-#pragma unroll
-                for (int a = 0; a < QB; ++a) acc[a][c] = E::mma(vf, pf[a][u], acc[a][c]);
+                acc[c] = E::mma(vf, pf[u], acc[c]);
             }
     };
 
     // a wave's keys of a tile that all its rows see
-    auto all_seen = [&](int r0, uint32_t kt, uint32_t vt) __attribute__((always_inline)) {
+    auto all_seen = [&](uint32_t kt, uint32_t vt) __attribute__((always_inline)) {
         const uint32_t kr = kt + row_base, vc = vt + column_base;
-        f32x16 s[KB][QB];
+        f32x16 s[KB];
 #pragma unroll
         for (int e = 0; e < KB; ++e) {
 #pragma unroll
-            for (int a = 0; a < QB; ++a)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s[e][a][i] = 0.0f;
+            for (int i = 0; i < 16; ++i) s[e][i] = 0.0f;
 #pragma unroll
             for (int st = 0; st < S; ++st) {
-                const Frag kf = TL::rows(kr, r0 + 32 * e, st);
-#pragma unroll
-                for (int a = 0; a < QB; ++a) s[e][a] = E::mma(kf, q[a][st], s[e][a]);
+                const Frag kf = TL::rows(kr, 32 * e, st);
+                s[e] = E::mma(kf, q[st], s[e]);
             }
         }
-        float top[QB];
+        float x = s[0][0];
 #pragma unroll
-        for (int a = 0; a < QB; ++a) {
-            float x = s[0][a][0];
+        for (int e = 0; e < KB; ++e)
 #pragma unroll
-            for (int e = 0; e < KB; ++e)
+            for (int i = 0; i < 16; ++i) x = fmaxf(x, s[e][i]);
+        move(halves<true>(x) * p.c);
+        Frag pf[KB][2];
+        const float m = mc == -INFINITY ? 0.0f : mc;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x = fmaxf(x, s[e][a][i]);
-            top[a] = halves<true>(x) * p.c;
-        }
-        move(top);
-        Frag pf[KB][QB][2];
+        for (int e = 0; e < KB; ++e) {
+            float add = 0.0f;
 #pragma unroll
-        for (int a = 0; a < QB; ++a) {
-            const float m = mc[a] == -INFINITY ? 0.0f : mc[a];
-#pragma unroll
-            for (int e = 0; e < KB; ++e) {
-                float add = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    s[e][a][i] = ex2(fmaf(s[e][a][i], p.c, -m));
-                    add += s[e][a][i];
-                }
-                sum[a] += add;
-                pf[e][a][0] = E::of(s[e][a], 0);
-                pf[e][a][1] = E::of(s[e][a], 1);
+            for (int i = 0; i < 16; ++i) {
+                s[e][i] = ex2(fmaf(s[e][i], p.c, -m));
+                add += s[e][i];
             }
+            sum += add;
+            pf[e][0] = E::of(s[e], 0);
+            pf[e][1] = E::of(s[e], 1);
         }
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -363,9 +316,8 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
             for (int e = 0; e < KB; ++e)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const Frag vf = TL::columns(vc, r0 + 32 * e + 16 * u, c);
-#pragma unroll
-                    for (int a = 0; a < QB; ++a) acc[a][c] = E::mma(vf, pf[e][a][u], acc[a][c]);
+                    const Frag vf = TL::columns(vc, 32 * e + 16 * u, c);
+                    acc[c] = E::mma(vf, pf[e][u], acc[c]);
                 }
     };
 
@@ -397,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
             uint32_t kt;
             next(kt);
 #pragma unroll 1
-            for (int e = 0; e < KB; ++e) some_seen(0, t * KT + rw + 32 * e, kt + (rw + 32 * e) * TL::ROW, kt + TILE + (rw + 32 * e) * TL::ROW);
+            for (int e = 0; e < KB; ++e) some_seen(t * KT + rw + 32 * e, kt + (rw + 32 * e) * TL::ROW, kt + TILE + (rw + 32 * e) * TL::ROW);
             done();
         }
     };
@@ -419,64 +371,59 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
     for (; t < to; ++t) {
         uint32_t kt;
         next(kt);
-        all_seen(0, kt + rw * TL::ROW, kt + TILE + rw * TL::ROW);
+        all_seen(kt + rw * TL::ROW, kt + TILE + rw * TL::ROW);
         done();
     }
     some(end_tile);
-#pragma unroll
-    for (int a = 0; a < QB; ++a) sum[a] = halves<false>(sum[a]);
+    sum = halves<false>(sum);
 
     // a row of the sums
-    auto index = [&](int a) { return (static_cast<long>(b) * p.H + head[a]) * p.Tq + token[a]; };
-    auto store4 = [&](int a, int ch, f32x4 x) {  // four channels of one row
+    auto index = [&]() { return (static_cast<long>(b) * p.H + head) * p.Tq + token; };
+    auto store4 = [&](int ch, f32x4 x) {  // four channels of one row
         if (p.splits > 1) {
-            if (first_tile < end_tile) *reinterpret_cast<f32x4*>(p.part + (split * p.rows + index(a)) * D + ch) = x;
+            if (first_tile < end_tile) *reinterpret_cast<f32x4*>(p.part + (split * p.rows + index()) * D + ch) = x;
             return;
         }
-        const long at = (PAGED ? (orow + token[a]) * p.o_st : b * p.o_sb + token[a] * p.o_st) + head[a] * p.o_sh + ch;
+        const long at = (PAGED ? (orow + token) * p.o_st : b * p.o_sb + token * p.o_st) + head * p.o_sh + ch;
         if (!BF16 || p.o_f32) {
             *reinterpret_cast<f32x4*>(static_cast<float*>(p.o) + at) = x;
         } else {
             *reinterpret_cast<bf16x4*>(static_cast<uint16_t*>(p.o) + at) = __builtin_convertvector(x, bf16x4);
         }
     };
-    auto store_sums = [&](int a, float m, float l) {
+    auto store_sums = [&](float m, float l) {
         if (p.splits > 1) {
-            float* ml = p.part + p.splits * p.rows * D + (split * p.rows + index(a)) * 2;
-            ml[0] = seen[a].count > 0 ? m : -INFINITY;
-            ml[1] = seen[a].count > 0 ? l : 0.0f;
+            float* ml = p.part + p.splits * p.rows * D + (split * p.rows + index()) * 2;
+            ml[0] = seen.count > 0 ? m : -INFINITY;
+            ml[1] = seen.count > 0 ? l : 0.0f;
         } else if (p.lse) {
-            p.lse[PAGED ? (orow + token[a]) * p.H + head[a] : index(a)] = seen[a].count > 0 ? (m + lg2(l)) * kLn2 : -INFINITY;
+            p.lse[PAGED ? (orow + token) * p.H + head : index()] = seen.count > 0 ? (m + lg2(l)) * kLn2 : -INFINITY;
         }
     };
     // what turns a row's sums into its output (or leaves them, for the join)
     auto norm = [&](float l) { return p.splits > 1 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l; };
 
     if constexpr (WK == 1) {
+        if (!stored) return;
+        const bool none = seen.count == 0;
+        const float n = norm(sum);
 #pragma unroll
-        for (int a = 0; a < QB; ++a) {
-            if (!stored[a]) continue;
-            const bool none = seen[a].count == 0;
-            const float n = norm(sum[a]);
+        for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int c = 0; c < C; ++c)
+            for (int g = 0; g < 4; ++g) {
+                f32x4 x;
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    f32x4 x;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] = none ? 0.0f : acc[a][c][4 * g + i] * n;
-                    store4(a, 32 * c + 8 * g + 4 * h, x);
-                }
-            if (h == 0) store_sums(a, mc[a], sum[a]);
-        }
+                for (int i = 0; i < 4; ++i) x[i] = none ? 0.0f : acc[c][4 * g + i] * n;
+                store4(32 * c + 8 * g + 4 * h, x);
+            }
+        if (h == 0) store_sums(mc, sum);
     } else {
         // The WK waves of a row: their maxima and sums, then their scaled sums by channel
         // through the tiles' memory.  A wave adds up D / WK of the channels.
-        static_assert(kBuffers * 2 * TILE >= 4 * QB * 32 * (D + 4) * 4, "the waves' sums fit the tiles' memory");
-        static_assert(QB == 1, "one block of rows a wave");
+        static_assert(4 * TILE >= 4 * 32 * (D + 4) * 4, "the waves' sums fit the tiles' memory");
         if (h == 0) {
-            joined[0][wave][lane & 31] = mc[0];
-            joined[1][wave][lane & 31] = sum[0];
+            joined[0][wave][lane & 31] = mc;
+            joined[1][wave][lane & 31] = sum;
         }
         __syncthreads();
         const int w0 = wave / WK * WK;
@@ -488,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
             const float mw = joined[0][w0 + w][lane & 31];
             l += mw == -INFINITY ? joined[1][w0 + w][lane & 31] : joined[1][w0 + w][lane & 31] * ex2(mw - m);
         }
-        const float by = mc[0] == -INFINITY ? 1.0f : ex2(mc[0] - m);
+        const float by = mc == -INFINITY ? 1.0f : ex2(mc - m);
         float* mine = reinterpret_cast<float*>(smem) + (wave * 32 + (lane & 31)) * (D + 4);
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -496,12 +443,12 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
             for (int g = 0; g < 4; ++g) {
                 f32x4 x;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = acc[0][c][4 * g + i] * by;
+                for (int i = 0; i < 4; ++i) x[i] = acc[c][4 * g + i] * by;
                 *reinterpret_cast<f32x4*>(mine + 32 * c + 8 * g + 4 * h) = x;
             }
         __syncthreads();
-        if (!stored[0]) return;
-        const bool none = seen[0].count == 0;
+        if (!stored) return;
+        const bool none = seen.count == 0;
         const float n = norm(l);
         constexpr int PART = D / WK;
 #pragma unroll
@@ -513,9 +460,9 @@ __global__ void __launch_bounds__(kThreads, BF16 && QB * D < 256 && KT * D < 128
                 x += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(smem) + ((w0 + w) * 32 + (lane & 31)) * (D + 4) + ch);
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = none ? 0.0f : x[i] * n;
-            store4(0, ch, x);
+            store4(ch, x);
         }
-        if (h == 0 && wave % WK == 0) store_sums(0, m, l);
+        if (h == 0 && wave % WK == 0) store_sums(m, l);
     }
 }
 
@@ -608,25 +555,18 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(JoinParams p) {
 
 // How a call is laid over the device, by its sizes alone.
 struct Plan {
-    int qb, wk, rows;   // blocks of rows a wave, waves that share rows, rows of a workgroup
+    int wk;             // waves that share rows
     int tiles, splits;
 };
-
 
 constexpr long kUnits = 256;  // compute units
 
 Plan plan(bool bf16, int d, long heads, long rows, long keys, bool ragged) {
     Plan p{};
     const bool wide = !bf16 && d == 128;  // 512-byte rows: half the keys to a tile
-    if (rows <= (wide ? 64 : 32)) {
-        p.qb = 1;
-        p.wk = wide ? 2 : 4;
-    } else {
-        p.qb = 1;
-        p.wk = 1;
-    }
-    p.rows = 32 * p.qb * (4 / p.wk);
-    p.tiles = static_cast<int>((rows + p.rows - 1) / p.rows);
+    p.wk = rows > (wide ? 64 : 32) ? 1 : wide ? 2 : 4;
+    const long tile = 32 * (4 / p.wk);
+    p.tiles = static_cast<int>((rows + tile - 1) / tile);
     const long groups = heads * p.tiles;
     long splits = 1, least = bf16 ? 512 : 256;
     if (p.wk > 1 && groups < kUnits) {
@@ -652,8 +592,8 @@ hipError_t launch_kind(const FwdParams& p, const Plan& pl, long groups, hipStrea
     const dim3 grid(static_cast<unsigned>(groups)), block(kThreads);
     constexpr bool wide = !BF16 && D == 128;
     constexpr int WK = wide ? 2 : 4, KT_FEW = wide ? 64 : 128, KT = wide ? 32 : 64;
-    if (pl.wk > 1) attn_fwd_kernel<BF16, D, 1, WK, KT_FEW, PAGED><<<grid, block, 0, stream>>>(p);
-    else attn_fwd_kernel<BF16, D, 1, 1, KT, PAGED><<<grid, block, 0, stream>>>(p);
+    if (pl.wk > 1) attn_fwd_kernel<BF16, D, WK, KT_FEW, PAGED><<<grid, block, 0, stream>>>(p);
+    else attn_fwd_kernel<BF16, D, 1, KT, PAGED><<<grid, block, 0, stream>>>(p);
     return hipGetLastError();
 }
 
