@@ -50,6 +50,27 @@ constexpr int kFewParts = 8;     // that a row's lanes join one after another
 // fp32 and, as bf16 factors, as exact as any.
 constexpr float kSlack = 8.0f;
 
+// Chunks of few sequences of a paged cache: the longest sequence's workgroups are dealt
+// first, so that the last to start are short ones (8 sequences of up to 512 new and 16384
+// tokens 288 us in the given order, 245 so; 16 of up to 256 and 8192 164 and 115; 32 of up
+// to 128 and 4096 122 and 106).  Every workgroup finds its sequence by itself, which with
+// many of them costs more than it gives (32 of one length 174 and 178 us, 64 of different
+// lengths 148 and 156).
+constexpr int kRanked = 32;
+
+// Which of the sequences (as many as a wave has lanes at the most) is the r-th longest, the
+// earlier first among equals.
+__device__ __forceinline__ int by_length(const PageMap& m, int r, int lane) {
+    const Sequence s = sequence_of(m, min(lane, m.B - 1));
+    const int len = s.n > 0 ? s.len : 0;
+    int rank = 0;
+    for (int j = 0; j < m.B; ++j) {
+        const int other = __builtin_amdgcn_readlane(len, j);
+        rank += (other > len) | ((other == len) & (j < lane));
+    }
+    return __builtin_ctzll(__ballot((lane < m.B) & (rank == r)));
+}
+
 template <bool BF16, int D, int WK, int KT, bool PAGED>
 __global__ void __launch_bounds__(kThreads, BF16 && KT * D < 128 * 128 ? 2 : 1) attn_fwd_kernel(FwdParams p) {
     using E = El<BF16>;
@@ -73,7 +94,10 @@ __global__ void __launch_bounds__(kThreads, BF16 && KT * D < 128 * 128 ? 2 : 1) 
     // are in as few L2s as that allows.  Then the parts of the keys, the tiles of rows (those
     // with the most keys first), and the sequences.
     const int hk = blockIdx.x % p.Hk, rest = blockIdx.x / p.Hk;
-    const int split = rest % p.splits, tile = p.tiles - 1 - rest / p.splits % p.tiles, b = rest / p.splits / p.tiles;
+    const int split = rest % p.splits, tile = p.tiles - 1 - rest / p.splits % p.tiles;
+    int b = rest / p.splits / p.tiles;
+    if constexpr (PAGED && WK == 1)
+        if (p.map.B <= kRanked) b = by_length(p.map, b, lane);
 
     int nq = p.Tq, nk = p.Tk;
     const char *qb = static_cast<const char*>(p.q), *kb = static_cast<const char*>(p.k), *vb = static_cast<const char*>(p.v);

@@ -50,6 +50,10 @@ PAGED = [
     (2, 16, 1, 128, "bf16", "bf16", 1024, [3, 2], [1500, 9], 0),
     (5, 2, 1, 64, "bf16", "bf16", 16, [2, 0, 0, 1, 3], [2, 0, 9, 4, 3], 0),
 ]
+PAGED += [  # chunks of many sequences, with equal lengths among them: in order of length, and (33) as given
+    (n, 4, 2, 64, "bf16", "bf16", 16, [(7 * b) % 31 for b in range(n)], [(7 * b) % 31 + 64 * (b % 3) + (b % 2) for b in range(n)], 0)
+    for n in (31, 32, 33)
+]
 ids = lambda c: "B%d-H%d.%d-d%d-%s-%s-p%d-n%s-L%s-w%d" % (c[:7] + (".".join(map(str, c[7])), ".".join(map(str, c[8])), c[9]))  # noqa: E731
 
 
