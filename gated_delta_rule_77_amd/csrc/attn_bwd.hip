@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dq_kernel(BwdPara
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int h = lane >> 5;
-    const int hk = blockIdx.x % p.Hk, rest = blockIdx.x / p.Hk;  // as in the forward
-    const int split = rest % p.splits, tile = p.tiles - 1 - rest / p.splits % p.tiles, b = rest / p.splits / p.tiles;
+    const int hk = blockIdx.x % p.Hk, rest = blockIdx.x / p.Hk, batch = gridDim.x / (p.Hk * p.splits * p.tiles);  // as in the forward
+    const int b = rest % batch, split = rest / batch % p.splits, tile = p.tiles - 1 - rest / batch / p.splits;
     const int nq = p.Tq, nk = p.Tk;
     const char* kb = static_cast<const char*>(p.k.p) + (b * p.k.sb + hk * p.k.sh) * E::BYTES;
     const char* vb = static_cast<const char*>(p.v.p) + (b * p.v.sb + hk * p.v.sh) * E::BYTES;

@@ -91,11 +91,23 @@ __global__ void __launch_bounds__(kThreads, BF16 && KT * D < 128 * 128 ? 2 : 1) 
     const int h = lane >> 5;
     // Key heads first: their workgroups are dealt over the XCDs, so that every XCD (and every
     // part of it) has its share of each sequence, whatever their lengths, and a head's keys
-    // are in as few L2s as that allows.  Then the parts of the keys, the tiles of rows (those
-    // with the most keys first), and the sequences.
+    // are in as few L2s as that allows.  Then the sequences, the parts of the keys and the tiles
+    // of rows, those with the most keys first, so that the last to start are short ones (tiles
+    // before sequences: B2 H16/4 T2048 d128 66 us, 56 so; fp32 B2 H8 T2048 d64 152 and 113; B4
+    // H16/4 T8192 d128 1036 and 1027; fp32 B3 H8/2 T1237 after 100 d64 79 and 84).  A cache's
+    // sequences, of lengths of their own, come one after another.
     const int hk = blockIdx.x % p.Hk, rest = blockIdx.x / p.Hk;
-    const int split = rest % p.splits, tile = p.tiles - 1 - rest / p.splits % p.tiles;
-    int b = rest / p.splits / p.tiles;
+    int b, split, tile;
+    if constexpr (PAGED) {
+        split = rest % p.splits;
+        tile = p.tiles - 1 - rest / p.splits % p.tiles;
+        b = rest / p.splits / p.tiles;
+    } else {
+        const int batch = gridDim.x / (p.Hk * p.splits * p.tiles);
+        b = rest % batch;
+        split = rest / batch % p.splits;
+        tile = p.tiles - 1 - rest / batch / p.splits;
+    }
     if constexpr (PAGED && WK == 1)
         if (p.map.B <= kRanked) b = by_length(p.map, b, lane);
 
