@@ -1,8 +1,8 @@
-// What the attention kernels share: 32x32 matrix tiles of bf16 or fp32 operands,
-// tiles of rows in LDS, and which keys a query sees.  Not a public header.
+// What the attention kernels share: 32x32 matrix tiles of bf16 or fp32 operands (these
+// as sums of bf16 parts), tiles of rows in LDS, and which keys a query sees.  Not a
+// public header.
 //
-// A matrix instruction's operands hold 8 consecutive k-slots to a lane, for both
-// types: lane l holds row (or column) l % 32 and slots 8 (l / 32) .. + 7.  Which k a
+// A matrix instruction's operands hold 8 consecutive k-slots to a lane: lane l holds row (or column) l % 32 and slots 8 (l / 32) .. + 7.  Which k a
 // slot stands for is free as long as both operands agree.  A result's 16 registers
 // of lane l are column l % 32, rows 8 (i / 4) + 4 (l / 32) + i % 4; registers 8 s ..
 // 8 s + 7 of a result are therefore an operand of the next product, whose slots
@@ -60,10 +60,40 @@ template <>
 struct El<false> {
     static constexpr int BYTES = 4;
     typedef f32x8 Frag;
-    static __device__ __forceinline__ f32x16 mma(const Frag& a, const Frag& b, f32x16 c) {
+    // x = x0 + x1 + x2 in bf16, each the nearest to what is left: 24 bits of a normal x.
+    // (|x| from 3.396e38 on rounds to infinity; below 2^-110 the last parts lose bits as
+    // bf16 has no more exponents: 2^-133 at the most.)
+    static __device__ __forceinline__ void parts(const Frag& f, bf16x8 (&p)[3]) {
+        Frag left = f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
-        return c;
+        for (int i = 0; i < 3; ++i) {
+            p[i] = __builtin_convertvector(left, bf16x8);
+            if (i == 2) break;
+            const u32x4 w = __builtin_bit_cast(u32x4, p[i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                left[2 * j] -= __uint_as_float(w[j] << 16);
+                left[2 * j + 1] -= __uint_as_float(w[j] & 0xffff0000u);
+            }
+        }
+    }
+    // An fp32 product as six of bf16 parts, the smallest first.  |x1| <= 2^-8 |x| and |x2| <=
+    // 2^-17 |x| (half steps of 8 bits), so that what is left out, x1 y2 + x2 y1 + x2 y2, is
+    // 2^-24 of |x y| at the most: one fp32 rounding.  The fp32 instruction takes 64 cycles
+    // for 4096 operations, these 32 for 32768: six take 3/8 of its time, and forming the
+    // parts (5.5 operations an element) most of what that leaves (B3 H8/2 T1237 after 100
+    // d64: forward 85 -> 58 us, dq 107 -> 94, dk and dv 153 -> 116; error against 64 bits
+    // 2.4e-7 -> 2.0e-7).
+    static __device__ __forceinline__ f32x16 mma(const Frag& a, const Frag& b, f32x16 c) {
+        bf16x8 x[3], y[3];
+        parts(a, x);
+        parts(b, y);
+        c = El<true>::mma(x[2], y[0], c);
+        c = El<true>::mma(x[0], y[2], c);
+        c = El<true>::mma(x[1], y[1], c);
+        c = El<true>::mma(x[1], y[0], c);
+        c = El<true>::mma(x[0], y[1], c);
+        return El<true>::mma(x[0], y[0], c);
     }
     static __device__ __forceinline__ Frag load(const void* p, long i) {
         const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);

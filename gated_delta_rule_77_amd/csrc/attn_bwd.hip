@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dq_kernel(BwdPara
 
 // PARTS: the workgroups of a block of keys are p.splits.
 template <bool BF16, int D, bool PARTS>
-__global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dkv_kernel(BwdParams p) {
+__global__ void __launch_bounds__(kThreads, BF16 || D == 64 ? 2 : 1) attn_dkv_kernel(BwdParams p) {
     using E = El<BF16>;
     using TL = Tile<BF16, D>;
     typedef typename E::Frag Frag;
@@ -587,8 +587,9 @@ int query_tiles(int Tq) { return (Tq + kQueries - 1) / kQueries; }
 // Where the grid of a pass would leave much of the device idle, at its end above all, what
 // each of its workgroups goes over (keys for dq, queries of the heads for dk and dv) is dealt
 // to `splits` of them: bf16 to four workgroups a compute unit (B2 H16/4 T2048 d128 241 us
-// with two, 203 with four, 298 with eight), fp32, whose products take 16 times as long, to
-// two of half the length (B3 H8/2 T1237 d64 234 us, 253 with four).
+// with two, 203 with four, 298 with eight), fp32, whose steps take three times as long, to
+// two (B4 H8/2 T1000 d64 148 us, with four 153; B3 T1237 181 and 176) of half the length (B3
+// T1000 137 us, 158 of the same length).
 constexpr int kMaxSplits = 32;
 
 int splits_of(bool bf16, long groups, long steps) {  // steps: blocks of 32 that a workgroup goes over

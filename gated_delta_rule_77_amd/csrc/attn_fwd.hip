@@ -72,7 +72,7 @@ __device__ __forceinline__ int by_length(const PageMap& m, int r, int lane) {
 }
 
 template <bool BF16, int D, int WK, int KT, bool PAGED>
-__global__ void __launch_bounds__(kThreads, BF16 && KT * D < 128 * 128 ? 2 : 1) attn_fwd_kernel(FwdParams p) {
+__global__ void __launch_bounds__(kThreads, (BF16 || D == 64) && KT * D * El<BF16>::BYTES < 32768 ? 2 : 1) attn_fwd_kernel(FwdParams p) {
     using E = El<BF16>;
     using TL = Tile<BF16, D>;
     typedef typename E::Frag Frag;
@@ -627,7 +627,7 @@ template <bool BF16, int D, bool PAGED>
 hipError_t launch_kind(const FwdParams& p, const Plan& pl, long groups, hipStream_t stream) {
     const dim3 grid(static_cast<unsigned>(groups)), block(kThreads);
     constexpr bool wide = !BF16 && D == 128;
-    constexpr int WK = wide ? 2 : 4, KT_FEW = wide ? 64 : 128, KT = wide ? 32 : 64;
+    constexpr int WK = wide ? 2 : 4, KT_FEW = wide ? 64 : 128, KT = BF16 ? 64 : 32;
     if (pl.wk > 1) attn_fwd_kernel<BF16, D, WK, KT_FEW, PAGED><<<grid, block, 0, stream>>>(p);
     else attn_fwd_kernel<BF16, D, 1, KT, PAGED><<<grid, block, 0, stream>>>(p);
     return hipGetLastError();

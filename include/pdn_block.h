@@ -154,7 +154,9 @@ typedef struct pdn_add_norm_bwd_args {
  *   d                 channels of a head, of v too: 64 or 128.
  *   dtype             PDN_F32 or PDN_BF16: q, k, v.  Scores, their sums and the
  *                     outputs' sums are fp32; with bf16 the probabilities are
- *                     rounded to bf16 for their product with v.
+ *                     rounded to bf16 for their product with v.  A product of two
+ *                     fp32 numbers is within 2^-24 of its own (factors below 2^-110
+ *                     count to 2^-133); those from 3.396e38 on count as infinite.
  *   o_dtype           PDN_F32, or PDN_BF16 where dtype is: o.
  *   window            keys that a query sees at most; 0 = all.
  *   scale             finite, > 0, and so times log2(e).

@@ -341,6 +341,24 @@ def test_far_strides():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_key_gives_its_value(d):
+    """fp32 values of every size and of 24 bits come back.  The key's weight w is one but for the
+    rounding of its exponent, and leaves by o = (w v) / w: in halves of a step (2^-24) one of
+    w v's parts that are left out, six of its sums, one each of 1 / w and the last product,
+    and one for the second order."""
+    torch, pdn = torch_mod(), _pdn()
+    gen = torch.Generator().manual_seed(63)
+    T = 200
+    q, k, v = (_rand(gen, 1, 1, T, d) for _ in range(3))
+    v *= torch.exp2(torch.randint(-100, 120, v.shape, generator=gen).float().cuda())
+    v[..., 0], v[..., 1] = 3.39e38, -3.39e38
+    first = torch.arange(T, dtype=torch.int32, device="cuda")[None]
+    o = torch.empty_like(q)
+    pdn.pdn_attn_fwd(q, k, v, o, first=first)
+    assert ((o.double() - v.double()).abs() <= 10 * 2.0 ** -24 * v.double().abs()).all()
+
+
 def test_furthest_token_steps():
     """Whole tiles whose lanes' offsets use all of their 32 bits."""
     torch, pdn = torch_mod(), _pdn()
