@@ -12,6 +12,14 @@
 // its part of every tile's keys, and their sums are joined at the end.  Where the
 // grid would not fill the device, the keys are dealt to `splits` workgroups, whose
 // sums a second kernel joins.
+//
+// Many rows are bound by the units that turn scores into probabilities beside those that
+// multiply: of the cycles of B4 H16/4 T8192 d128 in bf16 the matrix units take 57%, the
+// vector units 52% (1040 us, 1.06 PFLOP/s; a window of 2048 over T65536 0.97).  Two waves a
+// SIMD cover each other; 64 rows a wave, which halve the reads of LDS (29% of its cycles),
+// leave no registers for a second and ran at 470 TFLOP/s.  fp32 is bound by forming parts
+// (vector units 65%, matrix units 38%).  Few rows are bound by the keys' bytes: 256
+// sequences of 2048 to 8192 tokens, H16/4 d128, 2.7 GB at 5.4 TB/s.
 #include "attn.h"
 #include "block.h"
 #include "layer.h"
@@ -42,12 +50,14 @@ struct FwdParams {
 };
 
 constexpr int kThreads = 256;
-constexpr int kLeastKeys = 256;  // of a part of the keys
 constexpr int kMaxSplits = 128;
-constexpr int kFewParts = 8;     // that a row's lanes join one after another
+// Parts that a row's lanes join one after another; more of them are joined by a workgroup a
+// row (64 parts of one token, H16: call of 58 and 34 us; 4 parts of 16 tokens the same).
+constexpr int kFewParts = 8;
 // A row's maximum is moved (and its sums scaled) when a score passes it by this
 // much, in powers of two: until then the exponentials stay below 2^8, well inside
-// fp32 and, as bf16 factors, as exact as any.
+// fp32 and, as bf16 factors, as exact as any (B4 H16/4 T8192 1053 us, 1100 where every
+// larger score moves it).
 constexpr float kSlack = 8.0f;
 
 // Chunks of few sequences of a paged cache: the longest sequence's workgroups are dealt
@@ -162,8 +172,7 @@ __global__ void __launch_bounds__(kThreads, (BF16 || D == 64) && KT * D * El<BF1
     const int all_high = uniform(max(max(bounds[1][0], bounds[1][1]), max(bounds[1][2], bounds[1][3])));
     int first_tile = all_low / KT, end_tile = all_high < 0 ? first_tile : all_high / KT + 1;
     if (p.splits > 1) {
-        // even parts, but not shorter than what is worth a workgroup (short sequences of a batch)
-        const int n = max((end_tile - first_tile + p.splits - 1) / p.splits, kLeastKeys / KT);
+        const int n = (end_tile - first_tile + p.splits - 1) / p.splits;
         first_tile += split * n;
         end_tile = min(end_tile, first_tile + n);
     }
@@ -514,7 +523,8 @@ struct JoinParams {
 };
 
 // G = 1: D / 4 lanes to a row, which take its parts one after another.  G > 1: a workgroup
-// to a row, G groups of such lanes with every G-th part each.
+// to a row, G groups of such lanes with every G-th part each.  Bound by latency: 5 us for
+// two parts of 4096 rows, 6.5 for 64 of 16, d128.
 template <int D, int G, bool PAGED>
 __global__ void __launch_bounds__(kThreads) attn_join_kernel(JoinParams p) {
     constexpr int LPR = D / 4;
@@ -597,6 +607,14 @@ struct Plan {
 
 constexpr long kUnits = 256;  // compute units
 
+// Waves share rows where a call has no more of them than a wave holds (one token of 256
+// sequences 560 us, so 501; of one with 65536 tokens 36.4 and 33.8; of one of 1024 17.6 and
+// 14.1).  The keys are then dealt until every unit has a workgroup (twice that: 41.9 us for
+// the one of 65536), or, where the heads alone give it one, eight of at least 1024 keys, so
+// that unequal sequences end together (four 513 us, sixteen 526).  With more rows each unit
+// is given two, four for a cache's chunks, whose lengths differ (8 of up to 512 new and 16384
+// tokens: with two 388 us, four 272, eight 269; contiguous 512 of 16384 tokens: one 93, two
+// 83, four 94).
 Plan plan(bool bf16, int d, long heads, long rows, long keys, bool ragged) {
     Plan p{};
     const bool wide = !bf16 && d == 128;  // 512-byte rows: half the keys to a tile
