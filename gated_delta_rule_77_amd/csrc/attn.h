@@ -107,9 +107,10 @@ struct El<false> {
         for (int j = 0; j < 8; ++j) w[j] = r[8 * s + j];
         return w;
     }
+    // what has no finite parts to zero
     static __device__ __forceinline__ Frag finite(Frag f) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = (__float_as_uint(f[j]) & 0x7f800000u) == 0x7f800000u ? 0.0f : f[j];
+        for (int j = 0; j < 8; ++j) f[j] = (__float_as_uint(f[j]) & 0x7fffffffu) >= 0x7f7f8000u ? 0.0f : f[j];
         return f;
     }
 };

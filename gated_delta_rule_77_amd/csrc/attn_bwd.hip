@@ -14,9 +14,9 @@
 // the vector units 41 to 45% (T65536 with a window of 2048, H16/4 d128: dq 1.6 ms, 1.01
 // PFLOP/s; dk and dv 2.2 to 2.4 ms, 0.93), the second also by its reads of LDS, 40 KB a wave
 // and block, for which 38% of the cycles go: K stays in registers, V, which would leave no
-// second wave to a SIMD, does not, and two blocks of keys a wave spill (1800 us, 2826 for
-// packed rows of B2 H32/8 T8192).  Packed rows lose 40% more where blocks hold ends of
-// sequences, and to the longest sequence's workgroups, which end last.
+// second wave to a SIMD, does not, and two blocks of keys a wave spill (an early form 1800
+// us, so 2826).  Packed rows of B2 H32/8 T8192 run at 0.55 PFLOP/s there: blocks hold ends
+// of sequences, and the longest sequences' workgroups end last.
 #include "attn.h"
 #include "block.h"
 #include "layer.h"

@@ -342,6 +342,32 @@ def test_far_strides():
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("big", [3.4028234e38, -3.3962e38])
+def test_the_largest_numbers_count_as_infinite(d, big):
+    """fp32 numbers from 3.396e38 on: no part in what does not see them either."""
+    torch, pdn = torch_mod(), _pdn()
+    T, at = 150, 77
+    gen = torch.Generator().manual_seed(64)
+    q, k, v, do = (_rand(gen, 1, 1, T, d) for _ in range(4))
+
+    def both(q, k, v, do):
+        o, lse = torch.empty_like(q), torch.empty(1, 1, T, device="cuda")
+        pdn.pdn_attn_fwd(q, k, v, o, lse=lse)
+        g = [torch.empty_like(q) for _ in range(3)]
+        pdn.pdn_attn_bwd(q, k, v, o, do, lse, *g)
+        return [o, *g]
+
+    clean = both(q, k, v, do)
+    for which in range(4):
+        args = [t.clone() for t in (q, k, v, do)]
+        args[which][:, :, at, 2] = big
+        got = both(*args)
+        assert torch.equal(got[0][:, :, :at], clean[0][:, :, :at]) and torch.equal(got[1][:, :, :at], clean[1][:, :, :at])
+        if which in (0, 3):   # keys behind the query see nothing of it
+            assert torch.equal(got[2][:, :, at + 1:], clean[2][:, :, at + 1:]) and torch.equal(got[3][:, :, at + 1:], clean[3][:, :, at + 1:])
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_one_key_gives_its_value(d):
     """fp32 values of every size and of 24 bits come back.  The key's weight w is one but for the
     rounding of its exponent, and leaves by o = (w v) / w: in halves of a step (2^-24) one of
