@@ -245,6 +245,30 @@ __device__ __forceinline__ bool sees(const Seen& s, int key) {
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float lg2(float x) { return __builtin_amdgcn_logf(x); }
 
+// What a row's exponentials go by, ref being one of its largest scores: those of scores s are
+// 2^(fma(s - base, c, -m)).  Any m near ref c does, as all of the row's have the same: while
+// |ref c| is below 2^24 its rounding is off by half at most, base is 0 and the fused product
+// exact but for its one rounding.  Beyond, the rounding would pass the range of an exponential
+// (|ref c| = 2^31: by 64): base is then ref itself and m is 0.
+constexpr float kFar = 0x1p24f;
+struct Shift {
+    float base, m;
+};
+__device__ __forceinline__ Shift shift_of(float ref, float c) {
+    const float m = ref * c;
+    return fabsf(m) >= kFar && ref != -INFINITY ? Shift{ref, 0.0f} : Shift{0.0f, m};
+}
+// What turns sums that went by `from` into such that go by `to`, not below it (-inf: no score yet).
+__device__ __forceinline__ float weight(float from, float to, float c) {
+    const Shift a = shift_of(from, c), b = shift_of(to, c);
+    return from == to || from == -INFINITY ? 1.0f : ex2(fmaf(a.base - b.base, c, a.m - b.m));
+}
+// The logarithm of the sum of exponentials, `sum` of them going by ref.
+__device__ __forceinline__ float log_of(float ref, float sum, float c) {
+    const Shift s = shift_of(ref, c);
+    return s.base == 0.0f ? (s.m + lg2(sum)) * kLn2 : fmaf(ref, c * kLn2, lg2(sum) * kLn2);
+}
+
 // x, of which the compiler knows nothing: keeps what follows from it within a loop,
 // where taking it out would cost registers.
 __device__ __forceinline__ int opaque(int x) {

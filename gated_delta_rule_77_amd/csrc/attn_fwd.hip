@@ -249,32 +249,49 @@ __global__ void __launch_bounds__(kThreads, (BF16 || D == 64) && KT * D * El<BF1
     };
 
     f32x16 acc[C];
-    float mc = -INFINITY, sum = 0.0f;   // maximum times c; this half wave's part of the sum
+    float ref = -INFINITY, limit = -INFINITY, m = 0.0f;  // maximum; the score that moves it; what is subtracted for it
+    float sum = 0.0f;                                    // this half wave's part of the sum
+    uint64_t far = 0;                                    // rows whose scores lose the maximum before they are scaled
+    const float slack = kSlack / p.c;
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[c][i] = 0.0f;
 
     // The maximum moved where a row's scores pass it (each row by itself: what another
-    // holds has no part in its rounding either).
-    auto move = [&](float top) __attribute__((always_inline)) {
-        const bool moves = top > mc + kSlack;
-        if (__ballot(moves) == 0) return;
-        const float to = moves ? top : mc;
-        const float by = to == mc ? 1.0f : ex2(mc - to);
-        mc = to;
-        sum *= by;
+    // holds has no part in its rounding either); and taken from N registers of scores each of
+    // the rows for which scaling comes after.
+    auto move = [&](float top, auto& s, auto n) __attribute__((always_inline)) {
+        const bool moves = top > limit;
+        const uint64_t moving = __ballot(moves);
+        if ((moving | far) == 0) return;
+        if (moving) {
+            const float to = moves ? top : ref, by = weight(ref, to, p.c);
+            const Shift shift = shift_of(to, p.c);
+            ref = to;
+            limit = to + slack;
+            m = to == -INFINITY ? 0.0f : shift.m;
+            far = __ballot(shift.base != 0.0f);
+            sum *= by;
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+            for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[c][i] *= by;
+                for (int i = 0; i < 16; ++i) acc[c][i] *= by;
+        }
+        if (far) {
+            const float base = shift_of(ref, p.c).base;
+#pragma unroll
+            for (int e = 0; e < decltype(n)::value; ++e)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[e][i] -= base;
+        }
     };
 
     // a block of 32 keys of which some rows may not see all
     auto some_seen = [&](int k0, uint32_t kt, uint32_t vt) __attribute__((always_inline)) {
         if (k0 > high || k0 + 31 < low) return;
         const uint32_t kr = kt + row_base, vr = vt + row_base, vc = vt + column_base;
-        f32x16 s;
+        f32x16 scores[1], &s = scores[0];
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[i] = 0.0f;
 #pragma unroll
@@ -293,9 +310,8 @@ __global__ void __launch_bounds__(kThreads, (BF16 || D == 64) && KT * D * El<BF1
             if (!sees(to, 8 * (i >> 2) + (i & 3))) s[i] = -INFINITY;
             x = fmaxf(x, s[i]);
         }
-        move(halves<true>(x) * p.c);
+        move(halves<true>(x), scores, std::integral_constant<int, 1>());
         Frag pf[2];
-        const float m = mc == -INFINITY ? 0.0f : mc;
         float add = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -340,9 +356,8 @@ __global__ void __launch_bounds__(kThreads, (BF16 || D == 64) && KT * D * El<BF1
         for (int e = 0; e < KB; ++e)
 #pragma unroll
             for (int i = 0; i < 16; ++i) x = fmaxf(x, s[e][i]);
-        move(halves<true>(x) * p.c);
+        move(halves<true>(x), s, std::integral_constant<int, KB>());
         Frag pf[KB][2];
-        const float m = mc == -INFINITY ? 0.0f : mc;
 #pragma unroll
         for (int e = 0; e < KB; ++e) {
             float add = 0.0f;
@@ -436,13 +451,13 @@ __global__ void __launch_bounds__(kThreads, (BF16 || D == 64) && KT * D * El<BF1
             *reinterpret_cast<bf16x4*>(static_cast<uint16_t*>(p.o) + at) = __builtin_convertvector(x, bf16x4);
         }
     };
-    auto store_sums = [&](float m, float l) {
+    auto store_sums = [&](float top, float l) {
         if (p.splits > 1) {
             float* ml = p.part + p.splits * p.rows * D + (split * p.rows + index()) * 2;
-            ml[0] = seen.count > 0 ? m : -INFINITY;
+            ml[0] = seen.count > 0 ? top : -INFINITY;
             ml[1] = seen.count > 0 ? l : 0.0f;
         } else if (p.lse) {
-            p.lse[PAGED ? (orow + token) * p.H + head : index()] = seen.count > 0 ? (m + lg2(l)) * kLn2 : -INFINITY;
+            p.lse[PAGED ? (orow + token) * p.H + head : index()] = seen.count > 0 ? log_of(top, l, p.c) : -INFINITY;
         }
     };
     // what turns a row's sums into its output (or leaves them, for the join)
@@ -461,26 +476,23 @@ __global__ void __launch_bounds__(kThreads, (BF16 || D == 64) && KT * D * El<BF1
                 for (int i = 0; i < 4; ++i) x[i] = none ? 0.0f : acc[c][4 * g + i] * n;
                 store4(32 * c + 8 * g + 4 * h, x);
             }
-        if (h == 0) store_sums(mc, sum);
+        if (h == 0) store_sums(ref, sum);
     } else {
         // The WK waves of a row: their maxima and sums, then their scaled sums by channel
         // through the tiles' memory.  A wave adds up D / WK of the channels.
         static_assert(4 * TILE >= 4 * 32 * (D + 4) * 4, "the waves' sums fit the tiles' memory");
         if (h == 0) {
-            joined[0][wave][lane & 31] = mc;
+            joined[0][wave][lane & 31] = ref;
             joined[1][wave][lane & 31] = sum;
         }
         __syncthreads();
         const int w0 = wave / WK * WK;
-        float m = -INFINITY, l = 0.0f;
+        float top = -INFINITY, l = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WK; ++w) m = fmaxf(m, joined[0][w0 + w][lane & 31]);
+        for (int w = 0; w < WK; ++w) top = fmaxf(top, joined[0][w0 + w][lane & 31]);
 #pragma unroll
-        for (int w = 0; w < WK; ++w) {
-            const float mw = joined[0][w0 + w][lane & 31];
-            l += mw == -INFINITY ? joined[1][w0 + w][lane & 31] : joined[1][w0 + w][lane & 31] * ex2(mw - m);
-        }
-        const float by = mc == -INFINITY ? 1.0f : ex2(mc - m);
+        for (int w = 0; w < WK; ++w) l += joined[1][w0 + w][lane & 31] * weight(joined[0][w0 + w][lane & 31], top, p.c);
+        const float by = weight(ref, top, p.c);
         float* mine = reinterpret_cast<float*>(smem) + (wave * 32 + (lane & 31)) * (D + 4);
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -507,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, (BF16 || D == 64) && KT * D * El<BF1
             for (int i = 0; i < 4; ++i) x[i] = none ? 0.0f : x[i] * n;
             store4(ch, x);
         }
-        if (h == 0 && wave % WK == 0) store_sums(m, l);
+        if (h == 0 && wave % WK == 0) store_sums(top, l);
     }
 }
 
@@ -519,6 +531,7 @@ struct JoinParams {
     long rows, o_sb, o_sh, o_st;
     int splits, H, Tq;
     int o_f32;
+    float c;
     PageMap map;
 };
 
@@ -545,7 +558,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(JoinParams p) {
     float m = -INFINITY, l = 0.0f;
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
     if constexpr (G > 1) {
-        __shared__ float weight[kMaxSplits];
+        __shared__ float weights[kMaxSplits];
         __shared__ float red[2][4];
         __shared__ f32x4 sums[G][LPR];
         const int tid = threadIdx.x, wave = tid >> 6;
@@ -560,15 +573,15 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(JoinParams p) {
         if ((tid & 63) == 0) red[0][wave] = top;
         __syncthreads();
         m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-        const float w = ls == 0.0f ? 0.0f : ms == -INFINITY ? 1.0f : ex2(ms - m);
-        if (tid < p.splits) weight[tid] = w;
+        const float w = ls == 0.0f ? 0.0f : weight(ms, m, p.c);
+        if (tid < p.splits) weights[tid] = w;
         const float part = wave_sum(ls * w);
         if ((tid & 63) == 0) red[1][wave] = part;
         __syncthreads();
         l = red[1][0] + red[1][1] + red[1][2] + red[1][3];
 #pragma unroll 4
         for (int s = group; s < p.splits; s += G) {
-            const float by = weight[s];
+            const float by = weights[s];
             // a part without keys has left nothing there
             if (by != 0.0f) x += *reinterpret_cast<const f32x4*>(p.part + (s * p.rows + row) * D + ch) * by;
         }
@@ -584,7 +597,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(JoinParams p) {
         for (int s = 0; s < p.splits; ++s) {
             const float ms = ml[s * p.rows * 2], ls = ml[s * p.rows * 2 + 1];
             const f32x4 y = *reinterpret_cast<const f32x4*>(p.part + (s * p.rows + row) * D + ch);
-            const float by = ls == 0.0f ? 0.0f : ms == -INFINITY ? 1.0f : ex2(ms - m);
+            const float by = ls == 0.0f ? 0.0f : weight(ms, m, p.c);
             l = fmaf(ls, by, l);
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] += by == 0.0f ? 0.0f : y[i] * by;  // a part without keys has left nothing there
@@ -596,7 +609,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(JoinParams p) {
     for (int i = 0; i < 4; ++i) x[i] *= n;
     if (p.o_f32) *reinterpret_cast<f32x4*>(static_cast<float*>(p.o) + at) = x;
     else *reinterpret_cast<bf16x4*>(static_cast<uint16_t*>(p.o) + at) = __builtin_convertvector(x, bf16x4);
-    if (p.lse && ch == 0) p.lse[out] = none ? -INFINITY : (m + lg2(l)) * kLn2;
+    if (p.lse && ch == 0) p.lse[out] = none ? -INFINITY : log_of(m, l, p.c);
 }
 
 // How a call is laid over the device, by its sizes alone.
@@ -743,6 +756,7 @@ hipError_t launch_attn_fwd(const pdn_attn_args& a, hipStream_t stream) {
     j.H = a.H;
     j.Tq = a.Tq;
     j.o_f32 = p.o_f32;
+    j.c = p.c;
     return launch_join<false>(j, a.d, stream);
 }
 
@@ -789,6 +803,7 @@ hipError_t launch_attn_paged(const pdn_attn_paged_args& a, hipStream_t stream) {
     j.H = a.H;
     j.Tq = c.max_new;
     j.o_f32 = p.o_f32;
+    j.c = p.c;
     j.map = p.map;
     return launch_join<true>(j, c.d, stream);
 }

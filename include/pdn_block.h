@@ -159,7 +159,9 @@ typedef struct pdn_add_norm_bwd_args {
  *                     count to 2^-133); those from 3.396e38 on count as infinite.
  *   o_dtype           PDN_F32, or PDN_BF16 where dtype is: o.
  *   window            keys that a query sees at most; 0 = all.
- *   scale             finite, > 0, and so times log2(e).
+ *   scale             finite, > 0, and so times log2(e).  A row's probabilities come from its
+ *                     scores' differences, whatever their size; lse is +-inf where it
+ *                     passes fp32.
  *   first             [B,Tq] int32 (device): the first key that each query may
  *                     see; NULL = 0.  So a row holds packed sequences (first = the
  *                     start of the query's own, counted in keys), padding before

@@ -1,0 +1,80 @@
+"""GPU checks of attention, contiguous and paged, at the ends of its range: scores of any
+size."""
+import numpy as np
+import pytest
+
+import block_ref as ref
+import test_gpu_paged as paged
+from block_ref import HALF, U
+from gpu_util import torch_mod
+from test_gpu_attn import _close, _dt, _host, _nan, _pdn
+
+pytestmark = pytest.mark.gpu
+
+
+# -- scores of any size -------------------------------------------------------
+
+def _peaks(gen, H, Hk, Tq, Tk, dtype, power, sign, low=None):
+    """q, k, v of one sequence whose scores are one product each, exact in either type: 2^power
+    (1 + n / 128) for n = 0 .. 127, or from 2^low to 2^power along the keys."""
+    torch = torch_mod()
+    d = 64
+    q, k = torch.zeros(1, H, Tq, d), torch.zeros(1, Hk, Tk, d)
+    q[..., 5] = sign * 2.0 ** (power // 2)
+    if low is None:
+        k[..., 5] = 2.0 ** (power - power // 2) * (1 + torch.randint(0, 128, (1, Hk, Tk), generator=gen) / 128)
+    else:
+        k[..., 5] = torch.exp2(torch.linspace(low, power, Tk).round() - power // 2)
+    v = torch.randn(1, Hk, Tk, d, generator=gen)
+    return [t.to(_dt(dtype)).cuda() for t in (q, k, v)]
+
+
+def _peaked(o, lse, q, k, v, scale, dtype):
+    """Against the softmax in 64 bits.  Scores are exact, and a difference of two is off by its own
+    rounding only: an exponential that counts by 2^-18 at most (its exponent is above -30 there,
+    the scale's rounding and its own two), which is nothing where scores are equal."""
+    torch = torch_mod()
+    q, k, v = _host(q), _host(k), _host(v)
+    rep = q.shape[1] // k.shape[1]
+    k, v = k.repeat_interleave(rep, 1), v.repeat_interleave(rep, 1)
+    seen = ref.seen(q.shape[2], k.shape[2], 0, None)[:, None]
+    s = ((q @ k.mT) * scale).masked_fill(~seen, -torch.inf)
+    p = torch.softmax(s, -1)
+    size, n = p @ v.abs(), k.shape[2]
+    half = HALF["bf16"] if dtype == "bf16" else 0.0
+    _close("o", o, p @ v, size * (half + 2.0 ** -17 + 2 * (n + 8) * U), dtype)
+    want = torch.logsumexp(s, -1)
+    _close("lse", lse, want, want.abs() * 6 * U + 2.0 ** -18 + 2 * (n + 8) * U, "fp32")
+
+
+# few and many rows, one workgroup and several, joined by lanes and by workgroups
+@pytest.mark.parametrize("H,Hk,Tq,Tk", [(1, 1, 1, 1), (2, 1, 200, 200), (2, 1, 3, 2500), (2, 2, 1, 6000), (1, 1, 300, 2600)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_scores_of_any_size(dtype, H, Hk, Tq, Tk):
+    """Finite scores from 1e7 to 1e30, of either sign: the largest key's value comes out, the mean
+    where several are the largest."""
+    torch, pdn = torch_mod(), _pdn()
+    gen = torch.Generator().manual_seed(91)
+    for power, low in ((24, None), (31, None), (34, None), (60, None), (100, None), (100, -10), (40, 10)):
+        for sign in (1.0, -1.0):
+            for scale in (0.125, 0.11, 3.0):
+                q, k, v = _peaks(gen, H, Hk, Tq, Tk, dtype, power, sign, low)
+                o, lse = torch.empty_like(q), _nan((1, H, Tq))
+                pdn.pdn_attn_fwd(q, k, v, o, lse=lse, scale=scale)
+                _peaked(o, lse, q, k, v, float(np.float32(scale)), dtype)
+
+
+@pytest.mark.parametrize("news,lens", [([1], [700]), ([1], [6000]), ([90], [2000])])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_scores_of_any_size_over_pages(dtype, news, lens):
+    torch, pdn = torch_mod(), _pdn()
+    gen, kp, vp, table, dlens, starts, _ = paged._paged_case(1, 1, 64, dtype, 16, news, lens, 92)
+    for power, sign in ((34, 1.0), (34, -1.0), (100, 1.0)):
+        q, k, v = _peaks(gen, 2, 1, news[0], lens[0], dtype, power, sign)
+        j = torch.arange(lens[0], device="cuda")
+        at = table[0, j // 16].long(), j % 16
+        kp[at], vp[at] = k[0].transpose(0, 1), v[0].transpose(0, 1)
+        rows = q[0].transpose(0, 1).contiguous()
+        o, lse = torch.empty_like(rows), _nan((news[0], 2))
+        pdn.pdn_attn_paged(rows, o, kp, vp, table, dlens, starts=starts, max_new=news[0], lse=lse, scale=0.125)
+        _peaked(o.transpose(0, 1)[None], lse.T[None], q, k, v, 0.125, dtype)
