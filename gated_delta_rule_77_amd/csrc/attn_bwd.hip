@@ -137,7 +137,8 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dq_kernel(BwdPara
         for (int j = 0; j < 8; ++j) dot = fmaf(x[j], y[j], dot);
     }
     float delta = dot + __shfl_xor(dot, 32, 64);
-    const float lse2 = p.lse[row] * kLog2e;
+    // A row without a score above -inf has given 0: all of its probabilities are to be 0.
+    const float lse = p.lse[row], lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
     low = uniform(wave_min_i(low));
     high = uniform(wave_max_i(high));
     full_low = uniform(wave_max_i(full_low));

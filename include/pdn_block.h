@@ -209,7 +209,10 @@ typedef struct pdn_attn_args {
  *   d_o               strided [B,H,Tq,d] in o_dtype.
  *   g_dtype           PDN_F32, or PDN_BF16 where dtype is: dq, dk, dv.
  *   dq, dk, dv        strided as q, k, v; every element is written.
- * Queries that see nothing pass nothing on, whatever their q and dO hold.
+ * Queries that see nothing pass nothing on, whatever their q and dO hold; nor do those
+ * that see no score above -inf, where these are finite.  P is formed from lse as it is
+ * held, and so off by 2^-21 |lse| of itself at the most (of scores of 2^21 and more the
+ * gradients mean nothing).
  */
 typedef struct pdn_attn_bwd_args {
     pdn_attn_args fwd;

@@ -1,5 +1,5 @@
 """GPU checks of attention, contiguous and paged, at the ends of its range: scores of any
-size."""
+size, rows whose scores are all -inf."""
 import numpy as np
 import pytest
 
@@ -7,7 +7,7 @@ import block_ref as ref
 import test_gpu_paged as paged
 from block_ref import HALF, U
 from gpu_util import torch_mod
-from test_gpu_attn import _close, _dt, _host, _nan, _pdn
+from test_gpu_attn import _close, _dt, _host, _nan, _pdn, _rand
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +78,34 @@ def test_scores_of_any_size_over_pages(dtype, news, lens):
         o, lse = torch.empty_like(rows), _nan((news[0], 2))
         pdn.pdn_attn_paged(rows, o, kp, vp, table, dlens, starts=starts, max_new=news[0], lse=lse, scale=0.125)
         _peaked(o.transpose(0, 1)[None], lse.T[None], q, k, v, 0.125, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rows_whose_scores_are_all_minus_infinity(dtype):
+    """q and k finite, their products not: such a query gives o = 0 and lse = -inf, as one that
+    sees nothing, and passes nothing on."""
+    torch, pdn = torch_mod(), _pdn()
+    gen = torch.Generator().manual_seed(93)
+    B, H, Hk, T, d = 1, 4, 2, 300, 64
+    q, k, v = _rand(gen, B, H, T, d, dtype=dtype), _rand(gen, B, Hk, T, d, dtype=dtype), _rand(gen, B, Hk, T, d, dtype=dtype)
+    do = _rand(gen, B, H, T, d, dtype=dtype)
+    q[..., 7], k[..., 7] = 0.0, -2.0 ** 80
+    none = torch.tensor([0, 3, 40, 64, 130, 131, 299], device="cuda")
+    q[:, :, none] = 0.0
+    q[:, :, none, 7] = 2.0 ** 80
+
+    o, lse = torch.empty_like(q), _nan((B, H, T))
+    pdn.pdn_attn_fwd(q, k, v, o, lse=lse)
+    g = [torch.full_like(t, float("nan")) for t in (q, k, v)]
+    pdn.pdn_attn_bwd(q, k, v, o, do, lse, *g)
+    assert not o[:, :, none].any() and (lse[:, :, none] == -float("inf")).all() and not g[0][:, :, none].any()
+    # as where these queries see nothing by their mask
+    first = torch.zeros(B, T, dtype=torch.int32)
+    first[:, none.cpu()] = T
+    mask, scale = ref.seen(T, T, 0, first), float(np.float32(d ** -0.5))
+    want = ref.attn(_host(q), _host(k), _host(v), scale, mask, dtype)
+    _close("o", o, want["o"], want["bo"], dtype)
+    _close("lse", lse, want["lse"], want["bl"], "fp32")
+    want = ref.attn_bwd(_host(q), _host(k), _host(v), _host(o), _host(do), scale, mask, dtype, False, dtype)
+    for n, t in zip(("dq", "dk", "dv"), g):
+        _close(n, t, *want[n], dtype)
