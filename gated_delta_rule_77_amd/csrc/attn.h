@@ -44,6 +44,13 @@ struct El<true> {
         for (int j = 0; j < 8; ++j) w[j] = r[8 * s + j];
         return __builtin_convertvector(w, bf16x8);
     }
+    static __device__ __forceinline__ bool is_finite(const Frag& f) {
+        const u32x4 w = __builtin_bit_cast(u32x4, f);
+        bool all = true;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) all &= (w[j] & 0x7f80u) != 0x7f80u && (w[j] & 0x7f800000u) != 0x7f800000u;
+        return all;
+    }
     // infinities and NaN to zero
     static __device__ __forceinline__ Frag finite(const Frag& f) {
         u32x4 w = __builtin_bit_cast(u32x4, f);
@@ -107,10 +114,17 @@ struct El<false> {
         for (int j = 0; j < 8; ++j) w[j] = r[8 * s + j];
         return w;
     }
+    static __device__ __forceinline__ bool has_parts(float x) { return (__float_as_uint(x) & 0x7fffffffu) < 0x7f7f8000u; }
+    static __device__ __forceinline__ bool is_finite(const Frag& f) {
+        bool all = true;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) all &= has_parts(f[j]);
+        return all;
+    }
     // what has no finite parts to zero
     static __device__ __forceinline__ Frag finite(Frag f) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = (__float_as_uint(f[j]) & 0x7fffffffu) >= 0x7f7f8000u ? 0.0f : f[j];
+        for (int j = 0; j < 8; ++j) f[j] = has_parts(f[j]) ? f[j] : 0.0f;
         return f;
     }
 };

@@ -137,8 +137,18 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dq_kernel(BwdPara
         for (int j = 0; j < 8; ++j) dot = fmaf(x[j], y[j], dot);
     }
     float delta = dot + __shfl_xor(dot, 32, 64);
-    // A row without a score above -inf has given 0: all of its probabilities are to be 0.
-    const float lse = p.lse[row], lse2 = lse == -INFINITY ? INFINITY : lse * kLog2e;
+    // A row without a score above -inf has given 0: all of its probabilities are to be 0.  A
+    // query that is not finite may give such scores too (any other makes lse NaN): its
+    // probabilities are to be NaN, for all keys that it sees, in whatever tile they lie.
+    const float lse = p.lse[row];
+    float lse2 = lse * kLog2e;
+    if (__ballot(lse == -INFINITY)) {
+        bool sound = true;
+#pragma unroll
+        for (int s = 0; s < S; ++s) sound &= E::is_finite(q[s]);
+        const uint64_t sounds = __ballot(sound), both = sounds & (sounds >> 32);
+        if (lse == -INFINITY) lse2 = both >> (lane & 31) & 1 ? INFINITY : NAN;
+    }
     low = uniform(wave_min_i(low));
     high = uniform(wave_max_i(high));
     full_low = uniform(wave_max_i(full_low));
@@ -192,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dq_kernel(BwdPara
 
     // A block of 32 keys.  `partly`: some rows may not see all of them.  A key that is not
     // finite gives scores that are not: it is taken out of the product for those that do not
-    // see it, and those that do have them from P.
+    // see it, and those that do have 0 times it from dP.
     auto block = [&](int k0, uint32_t kt, auto partly) __attribute__((always_inline)) {
         constexpr bool PARTLY = decltype(partly)::value;
         const uint32_t kr = kt + row_base, kc = kt + column_base, vr = kr + TILE;
@@ -215,6 +225,10 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dq_kernel(BwdPara
 #pragma unroll
             for (int i = 0; i < 16; ++i) any |= !(fabsf(s[i]) < INFINITY);
             dirty = __ballot(any) != 0;
+            if (dirty) {
+#pragma unroll
+                for (int st = 0; st < S; ++st) dp = E::mma(TL::rows(kr, 0, st), E::zero(), dp);
+            }
         }
         Frag df[2];
 #pragma unroll

@@ -145,8 +145,10 @@ typedef struct pdn_add_norm_bwd_args {
  *
  * A query that sees no key (or none whose score is above -inf) gives o = 0 and
  * lse = -inf.  What a query does not see has no part in its output, infinities and
- * NaN included; a non-finite value that it does see makes its output non-finite,
- * in that channel at least.
+ * NaN included.  Of what it does see, a number of v that is not finite makes its
+ * output non-finite, in that channel at least and whatever its probability; a score
+ * of +inf or NaN makes all of it NaN; a score of -inf is a probability of 0 (an
+ * infinite number of bf16 may give one, one of fp32 gives NaN).
  *
  *   B, H, Hk, Tq, Tk  sizes; B, H, Hk >= 1; Hk divides H (head h reads key head
  *                     h / (H / Hk)); Tq, Tk >= 0, Tq > Tk included (queries
@@ -209,6 +211,8 @@ typedef struct pdn_attn_args {
  *   d_o               strided [B,H,Tq,d] in o_dtype.
  *   g_dtype           PDN_F32, or PDN_BF16 where dtype is: dq, dk, dv.
  *   dq, dk, dv        strided as q, k, v; every element is written.
+ * A key or value that is not finite makes dq of all queries that see it non-finite, a
+ * query or its dO dk and dv of all keys that it sees, in its own channel at least.
  * Queries that see nothing pass nothing on, whatever their q and dO hold; nor do those
  * that see no score above -inf, where these are finite.  P is formed from lse as it is
  * held, and so off by 2^-21 |lse| of itself at the most (of scores of 2^21 and more the

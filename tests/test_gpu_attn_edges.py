@@ -1,5 +1,5 @@
 """GPU checks of attention, contiguous and paged, at the ends of its range: scores of any
-size, rows whose scores are all -inf."""
+size, rows whose scores are all -inf, keys and queries that are not finite."""
 import numpy as np
 import pytest
 
@@ -109,3 +109,43 @@ def test_rows_whose_scores_are_all_minus_infinity(dtype):
     want = ref.attn_bwd(_host(q), _host(k), _host(v), _host(o), _host(do), scale, mask, dtype, False, dtype)
     for n, t in zip(("dq", "dk", "dv"), g):
         _close(n, t, *want[n], dtype)
+
+
+# -- what is not finite and is seen ------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_infinite_keys_and_queries_reach_the_gradients(dtype, d):
+    """A key or query with an infinity, its scores -inf (in fp32 NaN), a value or dO with one:
+    wherever a tile ends, the gradients of what it has a part in are not finite, the others' as
+    ever."""
+    torch, pdn = torch_mod(), _pdn()
+    gen = torch.Generator().manual_seed(94)
+    T = 300
+    q, k, v, do = (_rand(gen, 1, 2, T, d, dtype=dtype) for _ in range(4))
+    q[..., 3], k[..., 3] = 0.5, 0.25
+
+    def both(q, k, v, do):
+        o, lse = torch.empty_like(q), _nan((1, 2, T))
+        pdn.pdn_attn_fwd(q, k, v, o, lse=lse)
+        g = [torch.empty_like(t) for t in (q, k, v)]
+        pdn.pdn_attn_bwd(q, k, v, o, do, lse, *g)
+        return [o, *g]
+
+    clean = both(q, k, v, do)
+    for at in (5, 31, 70, 128, 290):
+        for which in range(4):
+            args = [t.clone() for t in (q, k, v, do)]
+            args[which][:, :, at, 3] = -float("inf")
+            o, dq, dk, dv = both(*args)
+            if which in (1, 2):
+                assert torch.equal(o[:, :, :at], clean[0][:, :, :at]) and torch.equal(dq[:, :, :at], clean[1][:, :, :at])
+                assert not torch.isfinite(dq[:, :, at:, 3]).any()     # of all that see it
+                if which == 1 and dtype == "bf16":
+                    assert torch.isfinite(o.float()).all()            # a probability of zero
+            else:
+                others = torch.arange(T, device="cuda") != at
+                assert torch.equal(o[:, :, others], clean[0][:, :, others]) and torch.equal(dq[:, :, others], clean[1][:, :, others])
+                for got, was in ((dk, clean[2]), (dv, clean[3])):
+                    assert not torch.isfinite(got[:, :, :at + 1, 3]).any()   # of all that it sees
+                    assert torch.equal(got[:, :, at + 1:], was[:, :, at + 1:])
