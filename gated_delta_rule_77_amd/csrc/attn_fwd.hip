@@ -43,7 +43,7 @@ struct FwdParams {
     float c;             // scale * log2(e)
     int o_f32;
     int tiles, splits;   // of rows; of the keys
-    float* part;         // splits > 1: [splits][rows][D] sums, then [splits][rows][2] (maximum, sum)
+    float* part;         // splits > 1: [splits][rows][D] sums, then [splits][rows][2] (maximum, sum; kNoPart: no tiles, no sums)
     long rows;           // B H Tq
     // paged: q_st, o_st step rows of N; k_sb, v_sb step pages
     PageMap map;
@@ -54,6 +54,10 @@ constexpr int kMaxSplits = 128;
 // Parts that a row's lanes join one after another; more of them are joined by a workgroup a
 // row (64 parts of one token, H16: call of 58 and 34 us; 4 parts of 16 tokens the same).
 constexpr int kFewParts = 8;
+// In the place of a sum of exponentials: the part had no keys, and its sums are unwritten.
+// (Sums that are there count however small their weight is, as 0 times a value that is not
+// finite does.)
+constexpr float kNoPart = -1.0f;
 // A row's maximum is moved (and its sums scaled) when a score passes it by this
 // much, in powers of two: until then the exponentials stay below 2^8, well inside
 // fp32 and, as bf16 factors, as exact as any (B4 H16/4 T8192 1053 us, 1100 where every
@@ -455,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, (BF16 || D == 64) && KT * D * El<BF1
         if (p.splits > 1) {
             float* ml = p.part + p.splits * p.rows * D + (split * p.rows + index()) * 2;
             ml[0] = seen.count > 0 ? top : -INFINITY;
-            ml[1] = seen.count > 0 ? l : 0.0f;
+            ml[1] = first_tile >= end_tile ? kNoPart : seen.count > 0 ? l : 0.0f;
         } else if (p.lse) {
             p.lse[PAGED ? (orow + token) * p.H + head : index()] = seen.count > 0 ? log_of(top, l, p.c) : -INFINITY;
         }
@@ -562,7 +566,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(JoinParams p) {
         __shared__ float red[2][4];
         __shared__ f32x4 sums[G][LPR];
         const int tid = threadIdx.x, wave = tid >> 6;
-        float ms = -INFINITY, ls = 0.0f;
+        float ms = -INFINITY, ls = kNoPart;
         if (tid < p.splits) {
             ms = ml[tid * p.rows * 2];
             ls = ml[tid * p.rows * 2 + 1];
@@ -573,17 +577,16 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(JoinParams p) {
         if ((tid & 63) == 0) red[0][wave] = top;
         __syncthreads();
         m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-        const float w = ls == 0.0f ? 0.0f : weight(ms, m, p.c);
+        const float w = ls == kNoPart ? kNoPart : weight(ms, m, p.c);
         if (tid < p.splits) weights[tid] = w;
-        const float part = wave_sum(ls * w);
+        const float part = wave_sum(ls == kNoPart ? 0.0f : ls * w);
         if ((tid & 63) == 0) red[1][wave] = part;
         __syncthreads();
         l = red[1][0] + red[1][1] + red[1][2] + red[1][3];
 #pragma unroll 4
         for (int s = group; s < p.splits; s += G) {
             const float by = weights[s];
-            // a part without keys has left nothing there
-            if (by != 0.0f) x += *reinterpret_cast<const f32x4*>(p.part + (s * p.rows + row) * D + ch) * by;
+            if (by != kNoPart) x += *reinterpret_cast<const f32x4*>(p.part + (s * p.rows + row) * D + ch) * by;
         }
         sums[group][threadIdx.x % LPR] = x;
         __syncthreads();
@@ -597,10 +600,10 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(JoinParams p) {
         for (int s = 0; s < p.splits; ++s) {
             const float ms = ml[s * p.rows * 2], ls = ml[s * p.rows * 2 + 1];
             const f32x4 y = *reinterpret_cast<const f32x4*>(p.part + (s * p.rows + row) * D + ch);
-            const float by = ls == 0.0f ? 0.0f : weight(ms, m, p.c);
-            l = fmaf(ls, by, l);
+            const float by = weight(ms, m, p.c);
+            if (ls != kNoPart) l = fmaf(ls, by, l);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] += by == 0.0f ? 0.0f : y[i] * by;  // a part without keys has left nothing there
+            for (int i = 0; i < 4; ++i) x[i] += ls == kNoPart ? 0.0f : y[i] * by;
         }
     }
     const bool none = l == 0.0f;

@@ -149,3 +149,21 @@ def test_infinite_keys_and_queries_reach_the_gradients(dtype, d):
                 for got, was in ((dk, clean[2]), (dv, clean[3])):
                     assert not torch.isfinite(got[:, :, :at + 1, 3]).any()   # of all that it sees
                     assert torch.equal(got[:, :, at + 1:], was[:, :, at + 1:])
+
+
+@pytest.mark.parametrize("H,Hk,Tq,Tk", [(2, 1, 200, 200), (2, 1, 3, 2500), (2, 2, 1, 6000), (1, 1, 300, 2600)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+def test_a_seen_value_that_is_not_finite_shows(dtype, H, Hk, Tq, Tk, bad):
+    """Also where its key's probability is zero, and its workgroup's part of the sum with it."""
+    torch, pdn = torch_mod(), _pdn()
+    gen = torch.Generator().manual_seed(95)
+    q, k, v = _rand(gen, 1, H, Tq, 64, dtype=dtype), _rand(gen, 1, Hk, Tk, 64, dtype=dtype), _rand(gen, 1, Hk, Tk, 64, dtype=dtype)
+    q[..., 0] = 64.0
+    k[..., 0] = 0.0
+    k[:, :, :2 * Tk // 3, 0] = -512.0     # these count for nothing beside the rest
+    v[:, :, 9, 2] = float(bad)
+    o = torch.empty_like(q)
+    pdn.pdn_attn_fwd(q, k, v, o)
+    see = torch.arange(Tq, device="cuda") + Tk - Tq >= 9
+    assert not torch.isfinite(o[:, :, see, 2].float()).any() and torch.isfinite(o[:, :, ~see].float()).all()
