@@ -207,9 +207,13 @@ __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirs
 // From memory to LDS past the registers: 16 (or 4) bytes a lane, lane l's to LDS address
 // dst + 16 l (4 l).  Written out, because the compiler puts a wait for every such load of
 // its own before the next read of LDS, also of another buffer.  They have no result
-// register, and m0 no other use in these kernels.  landed() waits for all of this
-// wave's loads; the compiler takes note of its wait (and drops its own for what it
-// loaded before).
+// register.  landed() waits for all of this wave's loads; the compiler takes note of its wait
+// (and drops its own for what it loaded before).
+// Two things the compiler does not see to in such a block: that m0, which cannot be named as
+// overwritten, has no other use, and that five instructions lie between a vector instruction
+// that writes a scalar register (as uniform() is) and a load that takes its address from
+// there.  tests/test_attn_listing.py holds every build to both: to bring m0 back and the five
+// in each block cost 256 single tokens over up to 8192 501 -> 516 us, a windowed step 1%.
 __device__ __forceinline__ void to_lds(const void* src, uint32_t dst) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(uniform(dst)), "v"(src) : "memory");
 }
