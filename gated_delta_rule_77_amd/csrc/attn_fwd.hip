@@ -630,15 +630,22 @@ constexpr long kUnits = 256;  // compute units
 // that unequal sequences end together (four 513 us, sixteen 526).  With more rows each unit
 // is given two, four for a cache's chunks, whose lengths differ (8 of up to 512 new and 16384
 // tokens: with two 388 us, four 272, eight 269; contiguous 512 of 16384 tokens: one 93, two
-// 83, four 94).
-Plan plan(bool bf16, int d, long heads, long rows, long keys, bool ragged) {
+// 83, four 94).  A part has 512 keys at least; of fp32, whose tiles take three times as long, 256
+// or, with more rows, 96 (500 tokens of 16384, H4/2 d64 with a window of 300: one part 32 us,
+// three 20), of which there are no more than lanes join (T1500 H4/2 d64: five 30 us, eight 28,
+// eleven 34).  Keys are those that a workgroup can see: with a window that and its tokens
+// (bf16 T4096 H4 d128: a window of 64 in one part 14 us, in the four that all keys would give
+// 21; of 300 22 and 24).
+Plan plan(bool bf16, int d, long heads, long rows, long shared, long keys, long window, bool ragged) {
     Plan p{};
     const bool wide = !bf16 && d == 128;  // 512-byte rows: half the keys to a tile
     p.wk = rows > (wide ? 64 : 32) ? 1 : wide ? 2 : 4;
     const long tile = 32 * (4 / p.wk);
     p.tiles = static_cast<int>((rows + tile - 1) / tile);
     const long groups = heads * p.tiles;
-    long splits = 1, least = bf16 ? 512 : 256;
+    const long tokens = (rows < tile ? rows : tile) / shared + 1;
+    if (window > 0 && window + tokens < keys) keys = window + tokens;
+    long splits = 1, least = bf16 ? 512 : p.wk > 1 ? 256 : 96;
     if (p.wk > 1 && groups < kUnits) {
         splits = kUnits / groups;
     } else if (p.wk > 1) {
@@ -646,6 +653,7 @@ Plan plan(bool bf16, int d, long heads, long rows, long keys, bool ragged) {
         least = 1024;
     } else if (groups < (ragged ? 4 : 2) * kUnits) {
         splits = ((ragged ? 4 : 2) * kUnits + groups - 1) / groups;
+        if (!bf16 && splits > kFewParts) splits = kFewParts;
     }
     if (splits > keys / least) splits = keys / least;
     if (splits > kMaxSplits) splits = kMaxSplits;
@@ -690,15 +698,15 @@ hipError_t launch_join(const JoinParams& p, int d, hipStream_t stream) {
 }
 
 Plan plan_of(const pdn_attn_args& a) {
-    return plan(a.dtype == PDN_BF16, a.d, static_cast<long>(a.B) * a.Hk, static_cast<long>(a.Tq) * (a.H / a.Hk),
-                a.window > 0 && a.window < a.Tk - a.Tq ? a.window + a.Tq : a.Tk, false);
+    const long shared = a.H / a.Hk;
+    return plan(a.dtype == PDN_BF16, a.d, static_cast<long>(a.B) * a.Hk, a.Tq * shared, shared, a.Tk, a.window, false);
 }
 
 Plan plan_of(const pdn_attn_paged_args& a) {
-    const long keys = static_cast<long>(a.cache.table_width) * a.cache.page_size;
-    return plan(a.cache.dtype == PDN_BF16, a.cache.d, static_cast<long>(a.cache.B) * a.cache.Hk,
-                static_cast<long>(a.cache.max_new) * (a.H / a.cache.Hk),
-                a.window > 0 && static_cast<long>(a.window) + a.cache.max_new < keys ? static_cast<long>(a.window) + a.cache.max_new : keys, true);
+    const pdn_cache& c = a.cache;
+    const long shared = a.H / c.Hk;
+    return plan(c.dtype == PDN_BF16, c.d, static_cast<long>(c.B) * c.Hk, c.max_new * shared, shared,
+                static_cast<long>(c.table_width) * c.page_size, a.window, true);
 }
 
 }  // namespace
