@@ -1038,6 +1038,12 @@ def pdn_rope_freqs(rot_dim, base=10000.0, scaling=PDN_ROPE_PLAIN, factor=1.0, or
 # what a stack with attention layers needs besides the recurrence
 # ---------------------------------------------------------------------------
 
+def _in_32_bits(joined):
+    """Of numbers joined by |: the structs' fields would take one past 32 bits for another."""
+    if joined >> 31:
+        raise ValueError("sizes, windows and bounds must lie between 0 and 2^31 - 1")
+
+
 def _rows3(c, t, name, shape, dtype):
     """Pointer and strides of a [B,T,D] tensor."""
     if t is None:
@@ -1050,6 +1056,7 @@ def _seam(c, x, w, eps, drop_p, seed):
     if x.dim() != 3:
         raise ValueError("the rows must be [B,T,D]")
     a, (B, T, D) = c.a, x.shape
+    _in_32_bits(B | T | D)
     a.B, a.T, a.D, a.eps, a.drop_p = B, T, D, eps, drop_p
     a.w = c.plain(w, "w", (D,), _torch.float32)
     a.seed = c.plain(seed, "seed", (2,), _torch.int64)
@@ -1131,6 +1138,7 @@ def _attn(c, a, q, k, v, o, lse, scale, window, first):
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B,H,Tq,d], k and v [B,Hk,Tk,d]")
     (B, H, Tq, d), (_, Hk, Tk, _) = q.shape, k.shape
+    _in_32_bits(B | H | Tq | d | Hk | Tk | window)
     a.B, a.H, a.Hk, a.Tq, a.Tk, a.d = B, H, Hk, Tq, Tk, d
     a.dtype, a.o_dtype, a.window = _dtype_of(q, "q"), _dtype_of(o, "o"), window
     a.scale = d ** -0.5 if scale is None else scale
@@ -1193,7 +1201,7 @@ def _cache(c, m, N, k_pages, v_pages, table, lens, starts, max_new):
     if k_pages.dim() != 4 or table.dim() != 2:
         raise ValueError("k_pages and v_pages must be [pages,page_size,Hk,d], table [B,pages of a sequence]")
     shape, B = k_pages.shape, table.shape[0]
-    m.pages, m.page_size, m.Hk, m.d = shape
+    m.pages, m.page_size, m.Hk, m.d = pages, page_size, Hk, d = shape
     m.B, m.N, m.table_width, m.dtype = B, N, table.shape[1], _dtype_of(k_pages, "k_pages")
     m.k_pages, m.v_pages = c.rows(k_pages, "k_pages", shape, k_pages.dtype), c.rows(v_pages, "v_pages", shape, k_pages.dtype)
     m.k_sp, m.k_st, m.k_sh, _ = k_pages.stride()
@@ -1203,7 +1211,10 @@ def _cache(c, m, N, k_pages, v_pages, table, lens, starts, max_new):
     m.starts = c.plain(starts, "starts", (B + 1,), _torch.int32)
     if starts is None and B > 0 and N % B:
         raise ValueError("without starts every sequence has the same number of new tokens: %d rows, %d sequences" % (N, B))
-    m.max_new = max_new if max_new is not None else N if starts is not None or B == 0 else N // B
+    if max_new is None:
+        max_new = N if starts is not None or B == 0 else N // B
+    _in_32_bits(pages | page_size | Hk | d | B | N | max_new)
+    m.max_new = max_new
 
 
 def pdn_cache_append(k, v, k_pages, v_pages, table, lens, starts=None, max_new=None, stream=None) -> None:
@@ -1233,6 +1244,7 @@ def _attn_paged(q, o, k_pages, v_pages, table, lens, starts, max_new, scale, win
     _cache(c, a.cache, N, k_pages, v_pages, table, lens, starts, max_new)
     if d != a.cache.d:
         raise ValueError("q's heads hold %d channels, the cache's %d" % (d, a.cache.d))
+    _in_32_bits(H | window)
     a.H, a.o_dtype, a.window = H, _dtype_of(o, "o"), window
     a.scale = d ** -0.5 if scale is None else scale
     a.q, a.o = c.rows(q, "q", (N, H, d), k_pages.dtype), c.rows(o, "o", (N, H, d), o.dtype)

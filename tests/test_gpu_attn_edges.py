@@ -167,3 +167,32 @@ def test_a_seen_value_that_is_not_finite_shows(dtype, H, Hk, Tq, Tk, bad):
     pdn.pdn_attn_fwd(q, k, v, o)
     see = torch.arange(Tq, device="cuda") + Tk - Tq >= 9
     assert not torch.isfinite(o[:, :, see, 2].float()).any() and torch.isfinite(o[:, :, ~see].float()).all()
+
+
+# -- numbers past 32 bits -------------------------------------------------------
+
+def test_numbers_past_32_bits_are_refused():
+    """Sizes, windows and bounds that the library's 32-bit fields would take for others."""
+    torch, pdn = torch_mod(), _pdn()
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731
+    q, o = z(1, 2, 8, 64), z(1, 2, 8, 64)
+    for window in (2 ** 31, 2 ** 32 + 3, -2 ** 32):
+        with pytest.raises((ValueError, pdn.PdnError)):
+            pdn.pdn_attn_fwd(q, q, q, o, window=window)
+    many = z(1, 1, 1, 64).expand(1, 1, 2 ** 32 + 8, 64)
+    with pytest.raises((ValueError, pdn.PdnError)):
+        pdn.pdn_attn_fwd(q, many, many, o)
+    lse = z(1, 2, 8, dtype=torch.float32)
+    with pytest.raises((ValueError, pdn.PdnError)):
+        pdn.pdn_attn_bwd(q, many, many, o, o, lse, q.clone(), many, many)
+    rows = z(1, 1, 8).expand(1, 2 ** 32 + 1, 8)
+    with pytest.raises((ValueError, pdn.PdnError)):
+        pdn.pdn_add_norm_fwd(rows, z(1, 1, 8).expand(rows.shape))
+    with pytest.raises((ValueError, pdn.PdnError)):
+        pdn.pdn_add_norm_bwd(rows, rows, z(1, 1, 8).expand(rows.shape))
+    pages, table, lens, starts = z(3, 16, 2, 64), z(2, 3, dtype=torch.int32), z(2, dtype=torch.int32), z(3, dtype=torch.int32)
+    for bound in (2 ** 31, 2 ** 32 + 4, -2 ** 32):
+        with pytest.raises((ValueError, pdn.PdnError)):
+            pdn.pdn_attn_paged(z(4, 2, 64), z(4, 2, 64), pages, pages, table, lens, starts=starts, max_new=bound)
+        with pytest.raises((ValueError, pdn.PdnError)):
+            pdn.pdn_cache_append(z(4, 2, 64), z(4, 2, 64), pages, pages.clone(), table, lens, starts=starts, max_new=bound)
