@@ -1,9 +1,11 @@
 """GPU checks of attention, contiguous and paged, at the ends of its range: scores of any
-size, rows whose scores are all -inf, keys and queries that are not finite."""
+size, rows whose scores are all -inf, keys and queries that are not finite, keys dealt to many
+workgroups, pages by the hundred."""
 import numpy as np
 import pytest
 
 import block_ref as ref
+import test_gpu_attn as contiguous
 import test_gpu_paged as paged
 from block_ref import HALF, U
 from gpu_util import torch_mod
@@ -167,6 +169,45 @@ def test_a_seen_value_that_is_not_finite_shows(dtype, H, Hk, Tq, Tk, bad):
     pdn.pdn_attn_fwd(q, k, v, o)
     see = torch.arange(Tq, device="cuda") + Tk - Tq >= 9
     assert not torch.isfinite(o[:, :, see, 2].float()).any() and torch.isfinite(o[:, :, ~see].float()).all()
+
+
+# -- paths that depend on a call's sizes --------------------------------------
+
+MANY = [  # keys dealt to more than eight workgroups, and to more than a wave's 64
+    (1, 2, 1, 1, 5200, 64, "bf16", "bf16", "bf16", 0, None),
+    (1, 1, 1, 1, 34000, 128, "bf16", "bf16", "bf16", 0, None),
+    (1, 2, 1, 1, 34000, 64, "bf16", "fp32", "fp32", 0, None),
+    (1, 2, 1, 2, 3000, 64, "fp32", "fp32", "fp32", 0, None),
+    (1, 2, 1, 1, 2600, 128, "fp32", "fp32", "fp32", 0, None),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=contiguous.ids)
+def test_keys_dealt_to_many_workgroups(case):
+    B, H, Hk, Tq, Tk, d, dtype, odtype = case[:8]
+    e = lambda *s, t=dtype: torch_mod().empty(s, dtype=_dt(t), device="cuda")  # noqa: E731
+    size = _pdn().pdn_attn_fwd_workspace_size(e(B, H, Tq, d), e(B, Hk, Tk, d), e(B, Hk, Tk, d), e(B, H, Tq, d, t=odtype))
+    assert size > (64 if Tk > 32768 else 8) * B * H * Tq * (d + 2) * 4
+    contiguous.test_attn(case)
+
+
+_long = lambda n, every, far: [far if b % every == 1 else 1 + (7 * b) % 40 for b in range(n)]  # noqa: E731
+PAGES = [
+    (1, 4, 1, 64, "bf16", "bf16", 64, [1], [5000], 0),
+    (1, 2, 1, 64, "fp32", "fp32", 16, [1], [2600], 0),
+    (1, 2, 1, 128, "fp32", "fp32", 32, [2], [2600], 0),
+    (1, 2, 1, 128, "bf16", "bf16", 128, [1], [34000], 0),
+    # every unit has a workgroup by the heads alone
+    (128, 4, 2, 64, "bf16", "bf16", 32, [1] * 128, [1 + (397 * b) % 2100 for b in range(128)], 0),
+    # hundreds of pages to one workgroup, one token and several of a sequence
+    (130, 2, 1, 64, "bf16", "bf16", 16, [1] * 130, _long(130, 40, 5000), 0),
+    (256, 4, 4, 64, "bf16", "bf16", 16, [40 if b == 41 else 1 for b in range(256)], _long(256, 40, 3300), 0),
+]
+
+
+@pytest.mark.parametrize("case", PAGES, ids=lambda c: "B%d-H%d.%d-d%d-%s-p%d-L%d" % (*c[:5], c[6], max(c[8])))
+def test_pages_by_the_hundred_and_parts_by_the_dozen(case):
+    paged.test_paged(case)
 
 
 # -- numbers past 32 bits -------------------------------------------------------
