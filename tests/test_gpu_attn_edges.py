@@ -1,6 +1,6 @@
 """GPU checks of attention, contiguous and paged, at the ends of its range: scores of any
 size, rows whose scores are all -inf, keys and queries that are not finite, keys dealt to many
-workgroups, pages by the hundred."""
+workgroups, pages by the hundred, D of rows with keys in several blocks."""
 import numpy as np
 import pytest
 
@@ -9,7 +9,7 @@ import test_gpu_attn as contiguous
 import test_gpu_paged as paged
 from block_ref import HALF, U
 from gpu_util import torch_mod
-from test_gpu_attn import _close, _dt, _host, _nan, _pdn, _rand
+from test_gpu_attn import _close, _dt, _host, _make, _nan, _pdn, _rand
 
 pytestmark = pytest.mark.gpu
 
@@ -208,6 +208,42 @@ PAGES = [
 @pytest.mark.parametrize("case", PAGES, ids=lambda c: "B%d-H%d.%d-d%d-%s-p%d-L%d" % (*c[:5], c[6], max(c[8])))
 def test_pages_by_the_hundred_and_parts_by_the_dozen(case):
     paged.test_paged(case)
+
+
+# -- D ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("case", [(1, 2, 1, 200, 240, 128, "bf16", "bf16", "fp32", 0, None), (1, 2, 2, 150, 250, 64, "bf16", "fp32", "fp32", 40, None),
+                                  (2, 4, 2, 90, 1500, 64, "bf16", "bf16", "fp32", 0, None), (1, 2, 1, 200, 240, 64, "fp32", "fp32", "fp32", 0, None)],
+                         ids=contiguous.ids)
+def test_rows_of_several_blocks_take_d_from_o(case):
+    """Every query sees more than 32 keys, so that no block of 32 holds them all: D is <dO, o> of
+    the o that is given, without the rounding of P that a D formed from P would bring.  An o that
+    is off by more than that shows it: the gradients are those of this o."""
+    torch, pdn = torch_mod(), _pdn()
+    B, H, Hk, Tq, Tk, d, dtype, odtype, gdtype, window, kind = case
+    gen, q, k, v, do, first, mask = _make(case, 96)
+    assert mask.sum(-1).min() > 32
+    o, lse = _nan((B, H, Tq, d), odtype), _nan((B, H, Tq))
+    pdn.pdn_attn_fwd(q, k, v, o, lse=lse, window=window)
+    o = (o.float() + 0.25).to(o.dtype)
+    grads = [_nan(t.shape, gdtype) for t in (q, k, v)]
+    pdn.pdn_attn_bwd(q, k, v, o, do, lse, *grads, window=window)
+    scale = float(np.float32(d ** -0.5))
+    f = ref.attn(_host(q), _host(k), _host(v), scale, mask, dtype)
+    p, kk, vv, rep = f["p"], f["k"], f["v"], H // Hk
+    h, hd = HALF["bf16"] if dtype == "bf16" else 0.0, HALF["bf16"] if dtype == "bf16" and odtype == "fp32" else 0.0
+    dof, of = _host(do), _host(o)
+    dp, size_p = dof @ vv.mT, dof.abs() @ vv.abs().mT
+    delta, size_d = (dof * of).sum(-1, keepdim=True), (dof * of).abs().sum(-1, keepdim=True)
+    ds = p * (dp - delta)
+    # as block_ref.attn_bwd counts, with D's own sum of d products in the place of what P would add
+    e = 2 * f["e"] + 2 * (Tk + 8) * U + 4 * U * f["lse"].abs()[..., None]
+    eds = p * (size_p * (hd + 2 * (d + 2) * U) + size_d * 2 * (d + 2) * U) + ds.abs() * (e + 4 * U)
+    eds = eds * (1 + h) + ds.abs() * h
+    fold = lambda t: t.unflatten(1, (Hk, rep)).sum(2)  # noqa: E731
+    qf, sums = _host(q), 2 * (max(Tk, Tq * rep) + 8) * U
+    _close("dq", grads[0], scale * (ds @ kk), scale * (eds @ kk.abs() + sums * (ds.abs() @ kk.abs())), gdtype)
+    _close("dk", grads[1], scale * fold(ds.mT @ qf), scale * fold(eds.mT @ qf.abs() + sums * (ds.abs().mT @ qf.abs())), gdtype)
 
 
 # -- numbers past 32 bits -------------------------------------------------------
