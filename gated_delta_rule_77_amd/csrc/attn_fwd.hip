@@ -60,7 +60,7 @@ constexpr int kFewParts = 8;
 constexpr float kNoPart = -1.0f;
 // A row's maximum is moved (and its sums scaled) when a score passes it by this
 // much, in powers of two: until then the exponentials stay below 2^8, well inside
-// fp32 and, as bf16 factors, as exact as any (B4 H16/4 T8192 1053 us, 1100 where every
+// fp32 for values up to 2^119 / Tk and, as bf16 factors, as exact as any (B4 H16/4 T8192 1053 us, 1100 where every
 // larger score moves it).
 constexpr float kSlack = 8.0f;
 

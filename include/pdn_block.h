@@ -44,7 +44,10 @@ int pdn_block_version(void);
  *
  * and, for PDN_E4M3, by groups of channels:
  *
- *   y_scale = max(2^-64, max |y|) / 448,   y = nearest e4m3 of y / y_scale
+ *   y_scale = top / 448,   y = nearest e4m3 of y (448 / top),   top = max(2^-64, max |y|)
+ *
+ * with each quotient and product rounded to fp32 (which of two neighbours a number next
+ * to their middle becomes goes by that).
  *
  *   B, T, D           sizes; B >= 1; T >= 0; D a multiple of 8, <= 16384.
  *   dtype             PDN_F32 or PDN_BF16: x.
@@ -159,6 +162,9 @@ typedef struct pdn_add_norm_bwd_args {
  *                     rounded to bf16 for their product with v.  A product of two
  *                     fp32 numbers is within 2^-24 of its own (factors below 2^-110
  *                     count to 2^-133); those from 3.396e38 on count as infinite.
+ *                     The outputs' sums run over probabilities that are up to 2^8.5
+ *                     times a key's, and are divided at the end: they stay finite where
+ *                     |v| Tk is below 2^119; beyond, a finite o may come out infinite or NaN.
  *   o_dtype           PDN_F32, or PDN_BF16 where dtype is: o.
  *   window            keys that a query sees at most; 0 = all.
  *   scale             finite, > 0, and so times log2(e).  A row's probabilities come from its

@@ -246,6 +246,26 @@ def test_rows_of_several_blocks_take_d_from_o(case):
     _close("dk", grads[1], scale * fold(ds.mT @ qf), scale * fold(eds.mT @ qf.abs() + sums * (ds.abs().mT @ qf.abs())), gdtype)
 
 
+# -- the largest values --------------------------------------------------------
+
+@pytest.mark.parametrize("H,Hk,Tq,Tk", [(2, 1, 200, 200), (2, 1, 3, 2500), (1, 1, 300, 2600)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_values_up_to_the_limit(dtype, H, Hk, Tq, Tk):
+    """|v| of 3.4e38 / (2^8 Tk), and scores that rise along the keys by less than moves the
+    maximum at every one: finite, and as the softmax gives it."""
+    torch, pdn = torch_mod(), _pdn()
+    gen = torch.Generator().manual_seed(97)
+    q, k = torch.zeros(1, H, Tq, 64), torch.zeros(1, Hk, Tk, 64)
+    q[..., 0], k[..., 0] = 1.0, (torch.arange(Tk) % 128) / 32.0
+    v = torch.full((1, Hk, Tk, 64), 3.39e38 / (256 * Tk))
+    v[..., 1::2] *= torch.rand(1, Hk, Tk, 32, generator=gen)
+    q, k, v = (t.to(_dt(dtype)).cuda() for t in (q, k, v))
+    o = torch.empty_like(q)
+    pdn.pdn_attn_fwd(q, k, v, o, scale=1.0)
+    f = ref.attn(_host(q), _host(k), _host(v), 1.0, ref.seen(Tq, Tk, 0, None), dtype)
+    _close("o", o, f["o"], f["bo"], dtype)
+
+
 # -- numbers past 32 bits -------------------------------------------------------
 
 def test_numbers_past_32_bits_are_refused():
