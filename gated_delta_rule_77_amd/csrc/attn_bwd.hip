@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 2 : 1) attn_dq_kernel(BwdPara
             for (int i = 0; i < 16; ++i) any |= !(fabsf(s[i]) < INFINITY);
             dirty = __ballot(any) != 0;
             if (dirty) {
-#pragma unroll
+#pragma unroll 1  // (rare: unrolled its operands cost the whole kernel registers)
                 for (int st = 0; st < S; ++st) dp = E::mma(TL::rows(kr, 0, st), E::zero(), dp);
             }
         }
