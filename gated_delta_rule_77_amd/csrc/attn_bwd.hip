@@ -45,7 +45,7 @@ struct BwdParams {
     const int32_t* first;
     float *delta, *lse2;   // D, and lse in powers of two: [B,H,Tq]
     uint16_t* do16;        // bf16 copy of an fp32 dO, [B,H,Tq,D]; else null
-    int* first_range;      // [B][tiles of queries][2]: least and largest `first`; null without
+    int* first_least;      // [B][tiles of queries]: least `first`; null without
     int H, Hk, shared;
     uint32_t inverse;
     int Tq, Tk, window;
@@ -57,16 +57,12 @@ struct BwdParams {
     int query_tiles;
 };
 
-// The least and largest first key of each tile of queries.
-__global__ void __launch_bounds__(64) first_range_kernel(const int32_t* first, int Tq, int tiles, int* out) {
+// The least first key of each tile of queries.
+__global__ void __launch_bounds__(64) first_least_kernel(const int32_t* first, int Tq, int tiles, int* out) {
     const int b = blockIdx.x / tiles, t = blockIdx.x - b * tiles;
     const int i = min(t * kQueries + static_cast<int>(threadIdx.x % kQueries), Tq - 1);
-    const int f = first[static_cast<long>(b) * Tq + i];
-    const int lo = wave_min_i(f), hi = wave_max_i(f);
-    if (threadIdx.x == 0) {
-        out[2 * blockIdx.x] = lo;
-        out[2 * blockIdx.x + 1] = hi;
-    }
+    const int least = wave_min_i(first[static_cast<long>(b) * Tq + i]);
+    if (threadIdx.x == 0) out[blockIdx.x] = least;
 }
 
 // Four channels of an output's row.
@@ -324,7 +320,10 @@ __global__ void __launch_bounds__(kThreads, BF16 || D == 64 ? 2 : 1) attn_dkv_ke
     constexpr int TILE = QT * TL::ROW, DMAS = QT / TL::ROWS_PER_DMA / 4;
     constexpr int VALUES = KEYS * TL::ROW, V_DMAS = KEYS / TL::ROWS_PER_DMA / 4;
     __shared__ __align__(1024) char smem[4 * TILE + VALUES];  // two tiles of queries and dO, the keys' values
-    __shared__ __align__(16) float stats[2][3][64];  // of a tile's queries (QT of them): lse, D, first key
+    // Of a tile's queries: lse, D, first key.  A wave's load fills 64 places, of which QT are read
+    // (with half of its lanes off for it the pass took 1.6% longer: packed rows of B2 H32/8 T8192
+    // d128 850 and 864 us).
+    __shared__ __align__(16) float stats[2][3][64];
     __shared__ int range[2][4];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -353,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, BF16 || D == 64 ? 2 : 1) attn_dkv_ke
     if (p.first) {
         int lo = INT32_MAX, hi = -1;
         for (int t = begin + tid; t < end; t += kThreads)
-            if (p.first_range[2 * (b * p.query_tiles + t)] <= key1) {
+            if (p.first_least[b * p.query_tiles + t] <= key1) {
                 lo = min(lo, t);
                 hi = t;
             }
@@ -507,8 +506,9 @@ __global__ void __launch_bounds__(kThreads, BF16 || D == 64 ? 2 : 1) attn_dkv_ke
             }
     };
 
-    // The tiles of each head in turn; runs of those whose queries all see all of the wave's
-    // keys in a loop of their own.
+    // The tiles of each head in turn, QT / 32 blocks each (one: written without these loops the
+    // compiler's order of the masked block costs the pass 2%); runs of those whose queries all see
+    // all of the wave's keys in a loop of their own.
     const int w0 = key0 + 32 * wave, w1 = w0 + 31;  // this wave's keys
     int count = end > begin ? (end - begin) * p.shared : 0, t = begin;
     if (PARTS && count > 0) {  // this part of them
@@ -625,7 +625,7 @@ int splits_of(bool bf16, long groups, long steps) {  // steps: blocks of 32 that
 
 struct Layout {
     int q_splits, k_splits;
-    size_t delta, lse2, do16, first_range, part, bytes;  // offsets in the workspace
+    size_t delta, lse2, do16, first_least, part, bytes;  // offsets in the workspace
 };
 
 Layout layout(const pdn_attn_bwd_args& a) {
@@ -637,8 +637,8 @@ Layout layout(const pdn_attn_bwd_args& a) {
     l.k_splits = f.Tk > 0 ? splits_of(f.dtype == PDN_BF16, heads * ((f.Tk + 127) / 128), shared * query_tiles(window < f.Tq ? static_cast<int>(window) : f.Tq)) : 1;
     l.lse2 = up256(rows * sizeof(float));
     l.do16 = 2 * l.lse2;
-    l.first_range = l.do16 + (f.dtype == PDN_BF16 && f.o_dtype == PDN_F32 ? up256(rows * f.d * 2) : 0);
-    l.part = l.first_range + (f.first ? up256(static_cast<size_t>(f.B) * query_tiles(f.Tq) * 2 * sizeof(int)) : 0);
+    l.first_least = l.do16 + (f.dtype == PDN_BF16 && f.o_dtype == PDN_F32 ? up256(rows * f.d * 2) : 0);
+    l.part = l.first_least + (f.first ? up256(static_cast<size_t>(f.B) * query_tiles(f.Tq) * sizeof(int)) : 0);
     // dq's parts have been added up before dk's and dv's are formed
     const size_t q = l.q_splits > 1 ? l.q_splits * rows * f.d * sizeof(float) : 0;
     const size_t k = l.k_splits > 1 ? 2 * l.k_splits * keys * f.d * sizeof(float) : 0;
@@ -703,7 +703,7 @@ hipError_t launch_attn_bwd(const pdn_attn_bwd_args& a, hipStream_t stream) {
     p.delta = reinterpret_cast<float*>(ws + l.delta);
     p.lse2 = reinterpret_cast<float*>(ws + l.lse2);
     p.do16 = reinterpret_cast<uint16_t*>(ws + l.do16);
-    p.first_range = reinterpret_cast<int*>(ws + l.first_range);
+    p.first_least = reinterpret_cast<int*>(ws + l.first_least);
     p.H = f.H;
     p.Hk = f.Hk;
     p.shared = f.H / f.Hk;
@@ -717,8 +717,7 @@ hipError_t launch_attn_bwd(const pdn_attn_bwd_args& a, hipStream_t stream) {
     p.g_f32 = a.g_dtype == PDN_F32;
     p.query_tiles = query_tiles(f.Tq);
     if (f.first && f.Tq > 0) {
-        first_range_kernel<<<dim3(static_cast<unsigned>(f.B * p.query_tiles)), dim3(64), 0, stream>>>(f.first, f.Tq, p.query_tiles,
-                                                                                                     p.first_range);
+        first_least_kernel<<<dim3(static_cast<unsigned>(f.B * p.query_tiles)), dim3(64), 0, stream>>>(f.first, f.Tq, p.query_tiles, p.first_least);
         const hipError_t rc = hipGetLastError();
         if (rc != hipSuccess) return rc;
     }

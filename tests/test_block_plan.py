@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 import gated_delta_rule_77_amd as pdn
-from test_block_host import _attn, _paged, lib  # noqa: F401  the fixture
+from test_block_host import _attn, _attnb, _paged, lib  # noqa: F401  the fixture
 
 
 def _parts(lib, call, a, rows):
@@ -45,3 +45,19 @@ def test_windows_bound_the_parts_of_a_cache(lib, window, new):  # noqa: F811
     assert parts == 1 or parts * 512 <= sees + 1
     if window == 0:
         assert parts > 1
+
+
+def test_first_keys_cost_the_backward_one_number_a_tile(lib):  # noqa: F811
+    """The least first key of each 32 queries; every part of the workspace ends at 256 bytes."""
+    sizes = []
+    for first in (0x10000, None):
+        a, n = _attnb(fwd__Tq=6400, fwd__Tk=6400, fwd__first=first), ctypes.c_size_t(0)
+        for name in ("fwd__q", "fwd__k", "fwd__v", "fwd__o", "d_o", "dq", "dk", "dv"):
+            path = name.split("__")
+            at = a.fwd if len(path) == 2 else a
+            stem = {"d_o": "do"}.get(path[-1], path[-1])
+            for s, step in (("sb", 1 << 24), ("sh", 1 << 20), ("st", 128)):
+                setattr(at, stem + "_" + s, step)
+        assert lib.pdn_attn_bwd_workspace_size(ctypes.byref(a), ctypes.byref(n)) == pdn.PDN_OK
+        sizes.append(n.value)
+    assert sizes[0] - sizes[1] == -(-4 * 2 * 200 // 256) * 256
