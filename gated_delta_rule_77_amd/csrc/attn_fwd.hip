@@ -630,12 +630,12 @@ constexpr long kUnits = 256;  // compute units
 // that unequal sequences end together (four 513 us, sixteen 526).  With more rows each unit
 // is given two, four for a cache's chunks, whose lengths differ (8 of up to 512 new and 16384
 // tokens: with two 388 us, four 272, eight 269; contiguous 512 of 16384 tokens: one 93, two
-// 83, four 94).  A part has 512 keys at least; of fp32, whose tiles take three times as long, 256
-// or, with more rows, 96 (500 tokens of 16384, H4/2 d64 with a window of 300: one part 32 us,
-// three 20), of which there are no more than lanes join (T1500 H4/2 d64: five 30 us, eight 28,
-// eleven 34).  Keys are those that a workgroup can see: with a window that and its tokens
-// (bf16 T4096 H4 d128: a window of 64 in one part 14 us, in the four that all keys would give
-// 21; of 300 22 and 24).
+// 83, four 94).  A part has 512 keys at least, in fp32, whose tiles take three times as long,
+// 256, or with more rows 96 while lanes join the parts (500 tokens of 16384, H4/2 d64 with a
+// window of 300: one part 32 us, three 20; T1500 H4/2 d64: five 30 us, eight 28, eleven 34; 113
+// of up to 11056, B2 H12 d64: eight 92 us, 43 65).  Keys are those that a workgroup can see:
+// with a window that and its tokens (bf16 T4096 H4 d128: a window of 64 in one part 14 us, in
+// the four that all keys would give 21; of 300 22 and 24).
 Plan plan(bool bf16, int d, long heads, long rows, long shared, long keys, long window, bool ragged) {
     Plan p{};
     const bool wide = !bf16 && d == 128;  // 512-byte rows: half the keys to a tile
@@ -645,17 +645,17 @@ Plan plan(bool bf16, int d, long heads, long rows, long shared, long keys, long 
     const long groups = heads * p.tiles;
     const long tokens = (rows < tile ? rows : tile) / shared + 1;
     if (window > 0 && window + tokens < keys) keys = window + tokens;
-    long splits = 1, least = bf16 ? 512 : p.wk > 1 ? 256 : 96;
+    long splits = 1, most = keys / (bf16 ? 512 : 256);
     if (p.wk > 1 && groups < kUnits) {
         splits = kUnits / groups;
     } else if (p.wk > 1) {
         splits = (8 * kUnits + groups - 1) / groups;
-        least = 1024;
+        most = keys / 1024;
     } else if (groups < (ragged ? 4 : 2) * kUnits) {
         splits = ((ragged ? 4 : 2) * kUnits + groups - 1) / groups;
-        if (!bf16 && splits > kFewParts) splits = kFewParts;
+        if (!bf16 && most < kFewParts) most = keys / 96 < kFewParts ? keys / 96 : kFewParts;
     }
-    if (splits > keys / least) splits = keys / least;
+    if (splits > most) splits = most;
     if (splits > kMaxSplits) splits = kMaxSplits;
     p.splits = splits > 1 ? static_cast<int>(splits) : 1;
     return p;

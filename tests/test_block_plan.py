@@ -36,6 +36,13 @@ def test_windows_bound_the_parts(lib, window, Tq, Tk, bf16):  # noqa: F811
         assert parts > 1
 
 
+# fewer than nine parts are joined by lanes and may be short in fp32; long keys give more of the usual length
+@pytest.mark.parametrize("Tk,least,most", [(300, 3, 3), (700, 7, 7), (1500, 8, 8), (2600, 10, 10), (11056, 22, 22)])
+def test_short_parts_are_few_and_long_keys_have_many(lib, Tk, least, most):  # noqa: F811
+    a = _call(B=2, H=12, Hk=12, Tq=113, Tk=Tk, window=0, dtype=pdn.PDN_F32, o_dtype=pdn.PDN_F32)
+    assert least <= _parts(lib, "pdn_attn_fwd", a, 2 * 12 * 113) <= most
+
+
 @pytest.mark.parametrize("window", [1, 64, 200, 700, 2000, 0])
 @pytest.mark.parametrize("new", [1, 7, 400])
 def test_windows_bound_the_parts_of_a_cache(lib, window, new):  # noqa: F811
