@@ -264,27 +264,31 @@ __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x)
 __device__ __forceinline__ float lg2(float x) { return __builtin_amdgcn_logf(x); }
 
 // What a row's exponentials go by, ref being one of its largest scores: those of scores s are
-// 2^(fma(s - base, c, -m)).  Any m near ref c does, as all of the row's have the same: while
-// |ref c| is below 2^24 its rounding is off by half at most, base is 0 and the fused product
-// exact but for its one rounding.  Beyond, the rounding would pass the range of an exponential
-// (|ref c| = 2^31: by 64): base is then ref itself and m is 0.
-constexpr float kFar = 0x1p24f;
+// 2^fma(s, c, -m).  Any m near ref c does, as all of the row's have the same: its rounding is
+// off by 32 at most while |ref c| is below 2^30, and the fused product exact but for its one
+// rounding.  Beyond, that would soon pass an exponential's range; but two different scores are
+// 64 apart there, and all but the largest count for nothing.  A power of two that brings ref to
+// 2^30 .. 2^31 keeps them so, and takes ref itself to exactly 0.
+constexpr float kFar = 0x1p30f;
 struct Shift {
-    float base, m;
+    float c, m;
+    bool far;
 };
 __device__ __forceinline__ Shift shift_of(float ref, float c) {
     const float m = ref * c;
-    return fabsf(m) >= kFar && ref != -INFINITY ? Shift{ref, 0.0f} : Shift{0.0f, m};
+    if (!(fabsf(m) >= kFar && fabsf(ref) < INFINITY)) return Shift{c, m, false};
+    const float by = __builtin_amdgcn_ldexpf(1.0f, min(31 - __builtin_amdgcn_frexp_expf(ref), 127));
+    return Shift{by, ref * by, true};
 }
 // What turns sums that went by `from` into such that go by `to`, not below it (-inf: no score yet).
 __device__ __forceinline__ float weight(float from, float to, float c) {
     const Shift a = shift_of(from, c), b = shift_of(to, c);
-    return from == to || from == -INFINITY ? 1.0f : ex2(fmaf(a.base - b.base, c, a.m - b.m));
+    return from == to || from == -INFINITY ? 1.0f : a.far || b.far ? 0.0f : ex2(a.m - b.m);
 }
 // The logarithm of the sum of exponentials, `sum` of them going by ref.
 __device__ __forceinline__ float log_of(float ref, float sum, float c) {
     const Shift s = shift_of(ref, c);
-    return s.base == 0.0f ? (s.m + lg2(sum)) * kLn2 : fmaf(ref, c * kLn2, lg2(sum) * kLn2);
+    return s.far ? fmaf(ref, c * kLn2, lg2(sum) * kLn2) : (s.m + lg2(sum)) * kLn2;
 }
 
 // x, of which the compiler knows nothing: keeps what follows from it within a loop,

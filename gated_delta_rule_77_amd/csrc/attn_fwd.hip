@@ -15,10 +15,10 @@
 //
 // Many rows are bound by the units that turn scores into probabilities beside those that
 // multiply: of the cycles of B4 H16/4 T8192 d128 in bf16 the matrix units take 57%, the
-// vector units 52% (1040 us, 1.06 PFLOP/s; a window of 2048 over T65536 0.97).  Two waves a
+// vector units 51% (1040 us, 1.06 PFLOP/s; a window of 2048 over T65536 0.92).  Two waves a
 // SIMD cover each other; 64 rows a wave, which halve the reads of LDS (29% of its cycles),
 // leave no registers for a second and ran at 470 TFLOP/s.  fp32 is bound by forming parts
-// (vector units 65%, matrix units 38%).  Few rows are bound by the keys' bytes: 256
+// (vector units 66%, matrix units 38%).  Few rows are bound by the keys' bytes: 256
 // sequences of 2048 to 8192 tokens, H16/4 d128, 2.7 GB at 5.4 TB/s.
 #include "attn.h"
 #include "block.h"
@@ -59,9 +59,9 @@ constexpr int kFewParts = 8;
 // finite does.)
 constexpr float kNoPart = -1.0f;
 // A row's maximum is moved (and its sums scaled) when a score passes it by this
-// much, in powers of two: until then the exponentials stay below 2^8, well inside
-// fp32 for values up to 2^119 / Tk and, as bf16 factors, as exact as any (B4 H16/4 T8192 1053 us, 1100 where every
-// larger score moves it).
+// much, in powers of two: until then the exponentials stay below 2^8 (times what the
+// rounding of the subtrahend makes of it), well inside fp32 for values up to 2^119 / Tk and, as
+// bf16 factors, as exact as any (B4 H16/4 T8192 1053 us, 1100 where every larger score moves it).
 constexpr float kSlack = 8.0f;
 
 // Chunks of few sequences of a paged cache: the longest sequence's workgroups are dealt
@@ -253,9 +253,8 @@ __global__ void __launch_bounds__(kThreads, (BF16 || D == 64) && KT * D * El<BF1
     };
 
     f32x16 acc[C];
-    float ref = -INFINITY, limit = -INFINITY, m = 0.0f;  // maximum; the score that moves it; what is subtracted for it
-    float sum = 0.0f;                                    // this half wave's part of the sum
-    uint64_t far = 0;                                    // rows whose scores lose the maximum before they are scaled
+    // the maximum, and what its exponentials go by; the score that moves it; this half wave's part of the sum
+    float ref = -INFINITY, by = p.c, m = 0.0f, limit = -INFINITY, sum = 0.0f;
     const float slack = kSlack / p.c;
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -263,39 +262,28 @@ __global__ void __launch_bounds__(kThreads, (BF16 || D == 64) && KT * D * El<BF1
         for (int i = 0; i < 16; ++i) acc[c][i] = 0.0f;
 
     // The maximum moved where a row's scores pass it (each row by itself: what another
-    // holds has no part in its rounding either); and taken from N registers of scores each of
-    // the rows for which scaling comes after.
-    auto move = [&](float top, auto& s, auto n) __attribute__((always_inline)) {
+    // holds has no part in its rounding either).
+    auto move = [&](float top) __attribute__((always_inline)) {
         const bool moves = top > limit;
-        const uint64_t moving = __ballot(moves);
-        if ((moving | far) == 0) return;
-        if (moving) {
-            const float to = moves ? top : ref, by = weight(ref, to, p.c);
-            const Shift shift = shift_of(to, p.c);
-            ref = to;
-            limit = to + slack;
-            m = to == -INFINITY ? 0.0f : shift.m;
-            far = __ballot(shift.base != 0.0f);
-            sum *= by;
+        if (__ballot(moves) == 0) return;
+        const float to = moves ? top : ref, keep = weight(ref, to, p.c);
+        const Shift shift = shift_of(to, p.c);
+        ref = to;
+        limit = to + slack;
+        by = shift.c;
+        m = to == -INFINITY ? 0.0f : shift.m;
+        sum *= keep;
 #pragma unroll
-            for (int c = 0; c < C; ++c)
+        for (int c = 0; c < C; ++c)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[c][i] *= by;
-        }
-        if (far) {
-            const float base = shift_of(ref, p.c).base;
-#pragma unroll
-            for (int e = 0; e < decltype(n)::value; ++e)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s[e][i] -= base;
-        }
+            for (int i = 0; i < 16; ++i) acc[c][i] *= keep;
     };
 
     // a block of 32 keys of which some rows may not see all
     auto some_seen = [&](int k0, uint32_t kt, uint32_t vt) __attribute__((always_inline)) {
         if (k0 > high || k0 + 31 < low) return;
         const uint32_t kr = kt + row_base, vr = vt + row_base, vc = vt + column_base;
-        f32x16 scores[1], &s = scores[0];
+        f32x16 s;
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[i] = 0.0f;
 #pragma unroll
@@ -314,12 +302,12 @@ __global__ void __launch_bounds__(kThreads, (BF16 || D == 64) && KT * D * El<BF1
             if (!sees(to, 8 * (i >> 2) + (i & 3))) s[i] = -INFINITY;
             x = fmaxf(x, s[i]);
         }
-        move(halves<true>(x), scores, std::integral_constant<int, 1>());
+        move(halves<true>(x));
         Frag pf[2];
         float add = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            s[i] = ex2(fmaf(s[i], p.c, -m));
+            s[i] = ex2(fmaf(s[i], by, -m));
             add += s[i];
         }
         sum += add;
@@ -360,14 +348,14 @@ __global__ void __launch_bounds__(kThreads, (BF16 || D == 64) && KT * D * El<BF1
         for (int e = 0; e < KB; ++e)
 #pragma unroll
             for (int i = 0; i < 16; ++i) x = fmaxf(x, s[e][i]);
-        move(halves<true>(x), s, std::integral_constant<int, KB>());
+        move(halves<true>(x));
         Frag pf[KB][2];
 #pragma unroll
         for (int e = 0; e < KB; ++e) {
             float add = 0.0f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                s[e][i] = ex2(fmaf(s[e][i], p.c, -m));
+                s[e][i] = ex2(fmaf(s[e][i], by, -m));
                 add += s[e][i];
             }
             sum += add;
@@ -496,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, (BF16 || D == 64) && KT * D * El<BF1
         for (int w = 0; w < WK; ++w) top = fmaxf(top, joined[0][w0 + w][lane & 31]);
 #pragma unroll
         for (int w = 0; w < WK; ++w) l += joined[1][w0 + w][lane & 31] * weight(joined[0][w0 + w][lane & 31], top, p.c);
-        const float by = weight(ref, top, p.c);
+        const float keep = weight(ref, top, p.c);
         float* mine = reinterpret_cast<float*>(smem) + (wave * 32 + (lane & 31)) * (D + 4);
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -504,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, (BF16 || D == 64) && KT * D * El<BF1
             for (int g = 0; g < 4; ++g) {
                 f32x4 x;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = acc[c][4 * g + i] * by;
+                for (int i = 0; i < 4; ++i) x[i] = acc[c][4 * g + i] * keep;
                 *reinterpret_cast<f32x4*>(mine + 32 * c + 8 * g + 4 * h) = x;
             }
         __syncthreads();

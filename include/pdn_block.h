@@ -74,9 +74,10 @@ int pdn_block_version(void);
  *   y                 strided [B,T,D].
  *   y_scale           [B,T,D / group] (group 0: [B,T]) fp32, given exactly for
  *                     PDN_E4M3.
- * A row that holds an infinity or NaN gives NaN where 0 times an infinity would;
- * in 8 bits NaN elements do not count for their group's scale, an infinity makes
- * its group NaN.  PDN_EUNSUPPORTED where B * T reaches 2^23.
+ * The sum of squares is fp32: a row in which it passes 3.4e38 has r = 0.  A row that
+ * holds an infinity or NaN gives NaN where 0 times an infinity would; in 8 bits NaN
+ * elements do not count for their group's scale, an infinity makes its group NaN.
+ * PDN_EUNSUPPORTED where B * T reaches 2^23.
  */
 typedef struct pdn_add_norm_args {
     int32_t B, T, D;
@@ -162,9 +163,10 @@ typedef struct pdn_add_norm_bwd_args {
  *                     rounded to bf16 for their product with v.  A product of two
  *                     fp32 numbers is within 2^-24 of its own (factors below 2^-110
  *                     count to 2^-133); those from 3.396e38 on count as infinite.
- *                     The outputs' sums run over probabilities that are up to 2^8.5
- *                     times a key's, and are divided at the end: they stay finite where
- *                     |v| Tk is below 2^119; beyond, a finite o may come out infinite or NaN.
+ *                     The outputs' sums run over exponentials of up to 2^8.5 (2^40 in
+ *                     rows whose largest score passes 2^23) and are divided at the end:
+ *                     they stay finite where |v| Tk is below 2^119 (2^87); beyond, a
+ *                     finite o may come out infinite or NaN.
  *   o_dtype           PDN_F32, or PDN_BF16 where dtype is: o.
  *   window            keys that a query sees at most; 0 = all.
  *   scale             finite, > 0, and so times log2(e).  A row's probabilities come from its
