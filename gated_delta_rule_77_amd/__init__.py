@@ -1223,7 +1223,8 @@ def pdn_cache_append(k, v, k_pages, v_pages, table, lens, starts=None, max_new=N
     starts[b + 1] - 1 (int32 [B + 1]; None: N / B each) to its last tokens of lens[b]
     (int32 [B], the new ones included) by table (int32 [B,width], its pages in
     order).  max_new: at least the most new tokens of any sequence (None: N / B, or N
-    with starts)."""
+    with starts: what it says of them sizes the launch, here and in pdn_attn_paged,
+    which takes a sequence for a chunk of that many where it is left out)."""
     c = _Call(CacheAppendArgs, k)
     if k.dim() != 3:
         raise ValueError("k and v must be [N,Hk,d]")

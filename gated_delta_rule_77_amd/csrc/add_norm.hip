@@ -10,7 +10,7 @@
 // Bound by bytes: each tensor once, a row held in registers between its sums and
 // its outputs (8 channels a lane and step, TPR lanes to a row).  B4 T8192 D2048 bf16 to
 // 8 bits 75 us, 6.3 TB/s; B2 T8192 D4096 with fp32 sums and dropout 145 us forward and
-// 211 to 224 backward, 5.5 and 4.9 TB/s.  Dropout's bits are formed from the element's
+// 211 to 233 backward, 5.5 and 4.9 TB/s.  Dropout's bits are formed from the element's
 // place, forward and backward: ten rounds of Philox for eight elements, some 25 issue
 // slots an element, beside its 6 to 14 bytes.
 #include "block.h"

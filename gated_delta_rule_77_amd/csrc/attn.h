@@ -2,8 +2,9 @@
 // as sums of bf16 parts), tiles of rows in LDS, and which keys a query sees.  Not a
 // public header.
 //
-// A matrix instruction's operands hold 8 consecutive k-slots to a lane: lane l holds row (or column) l % 32 and slots 8 (l / 32) .. + 7.  Which k a
-// slot stands for is free as long as both operands agree.  A result's 16 registers
+// A matrix instruction's operands hold 8 consecutive k-slots to a lane: lane l holds row (or
+// column) l % 32 and slots 8 (l / 32) .. + 7.  Which k a slot stands for is free as long as both
+// operands agree.  A result's 16 registers
 // of lane l are column l % 32, rows 8 (i / 4) + 4 (l / 32) + i % 4; registers 8 s ..
 // 8 s + 7 of a result are therefore an operand of the next product, whose slots
 // stand for rows 16 s + 4 (l / 32) + {0 .. 3, 8 .. 11}.  So scores are formed

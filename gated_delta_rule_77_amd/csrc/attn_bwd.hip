@@ -11,12 +11,15 @@
 // one pass would take 10.
 //
 // Bound as the forward is: in both passes the matrix units take 50 to 57% of the cycles and
-// the vector units 41 to 45% (T65536 with a window of 2048, H16/4 d128: dq 1.6 ms, 1.01
-// PFLOP/s; dk and dv 2.2 to 2.4 ms, 0.93), the second also by its reads of LDS, 40 KB a wave
+// the vector units 40 to 45% (T65536 with a window of 2048, H16/4 d128: dq 1.5 to 1.6 ms,
+// 1.03 PFLOP/s; dk and dv 2.2 to 2.3 ms, 0.96), the second also by its reads of LDS, 40 KB a wave
 // and block, for which 38% of the cycles go: K stays in registers, V, which would leave no
-// second wave to a SIMD, does not, and two blocks of keys a wave spill (an early form 1800
-// us, so 2826).  Packed rows of B2 H32/8 T8192 run at 0.55 PFLOP/s there: blocks hold ends
-// of sequences, and the longest sequences' workgroups end last.
+// second wave to a SIMD, does not.  Even so its kernels of d128 lack some: in bf16 9 vector
+// registers (11 with parts) and 28 scalar ones are kept in memory or in other registers, read
+// again once a tile and twice a masked block; in fp32 dq's lacks 19.  Two blocks of keys a wave
+// lack far more (an early form 1800 us, so 2826).  Packed rows of B2 H32/8 T8192 run at 0.50
+// to 0.55 PFLOP/s there: blocks hold ends of sequences, and the longest sequences' workgroups
+// end last.
 #include "attn.h"
 #include "block.h"
 #include "layer.h"

@@ -15,10 +15,10 @@
 //
 // Many rows are bound by the units that turn scores into probabilities beside those that
 // multiply: of the cycles of B4 H16/4 T8192 d128 in bf16 the matrix units take 57%, the
-// vector units 51% (1040 us, 1.06 PFLOP/s; a window of 2048 over T65536 0.92).  Two waves a
+// vector units 52% (1031 us, 1.07 PFLOP/s; a window of 2048 over T65536 0.92 to 0.96).  Two waves a
 // SIMD cover each other; 64 rows a wave, which halve the reads of LDS (29% of its cycles),
 // leave no registers for a second and ran at 470 TFLOP/s.  fp32 is bound by forming parts
-// (vector units 66%, matrix units 38%).  Few rows are bound by the keys' bytes: 256
+// (vector units 65%, matrix units 37%).  Few rows are bound by the keys' bytes: 256
 // sequences of 2048 to 8192 tokens, H16/4 d128, 2.7 GB at 5.4 TB/s.
 #include "attn.h"
 #include "block.h"
